@@ -61,7 +61,13 @@ typedef enum {
                                       exceeds NSG_NOALLOC_MAX_BYTES */
 } nsg_status_t;
 
-typedef enum { NSG_F16 = 0, NSG_BF16 = 1, NSG_F32 = 2 } nsg_dtype_t;
+typedef enum {
+  NSG_F16 = 0,
+  NSG_BF16 = 1,
+  NSG_F32 = 2,
+  NSG_F8E4M3 = 3, /* OCP 8-bit types, taken and written by the calls that say so */
+  NSG_F8E5M2 = 4  /* only (the others return NSG_ERR_UNSUPPORTED_DTYPE) */
+} nsg_dtype_t;
 
 typedef enum {
   NSG_STANDARD = 0, /* Algorithm 1 */
@@ -369,6 +375,127 @@ nsg_status_t ns_muon_step(void *W, int32_t w_dtype, void *M, int32_t m_dtype, co
                           double weight_decay, double scale, int32_t stochastic, uint64_t seed,
                           uint64_t step, const nsg_params_t *p, void *workspace,
                           size_t workspace_bytes, int32_t *status, void *stream);
+
+/* ---- The expert layer around the Muon step --------------------------------
+ * What produces the bucket [E, N, K] of weight gradients that ns_muon_step
+ * takes, and uses the weights that it updates: tokens sorted by expert and
+ * brought back with their router weights, operands in 8-bit floating point with
+ * one scale for each block of 128, and the products of such operands.  One
+ * plain linear layer is the case E = 1.
+ *
+ * For every call of this section:
+ *   - Device pointers, `stream`, errors and reentrancy as above: nothing is
+ *     allocated, nothing waits, a bad argument is reported before anything is
+ *     enqueued.  Pointers are aligned to their elements, 8-bit data to 16 bytes
+ *     (else NSG_ERR_INVALID_ARG).  Outputs must not overlap inputs.
+ *   - Results are reproducible bit for bit and do not depend on what else is in
+ *     the batch: sums have a fixed order, no atomics on memory.
+ *   - Rows are ld elements apart (ld >= their length) where a call has an ld,
+ *     packed otherwise.
+ *   - Index and offset arrays are device data that the host cannot check: an
+ *     index outside its range counts as "none" and offsets are clamped to their
+ *     range, so wrong ones give wrong results, never an access out of bounds.
+ *   - Limits: E <= NSG_MAX_EXPERTS, at most NSG_MAX_ROWS tokens or sorted rows, other
+ *     sides at most NSG_MAX_SIDE; beyond them NSG_ERR_SHAPE. */
+#define NSG_MAX_EXPERTS 1024
+#define NSG_MAX_ROWS (1 << 26)
+
+/* Sort the P = T k choices ids[t][j] (device, int32 or int64 by id_bits) by
+ * expert, stably.  An id outside 0 .. E-1 is dropped (as by a capacity limit).
+ *   offsets  [E + 1]: sorted rows offsets[e] .. offsets[e + 1] - 1 are expert e's
+ *   rows     [T][k]: the sorted row of each choice, -1 if dropped
+ *   tokens   [P]: the token t in each sorted row, -1 behind offsets[E]
+ *   workspace  nsg_expert_sort_workspace_size bytes, 4-byte aligned (may be 0
+ *              bytes and NULL); two calls that may overlap need two */
+nsg_status_t nsg_expert_sort_workspace_size(int64_t T, int64_t k, int64_t E, size_t *bytes);
+nsg_status_t nsg_expert_sort(const void *ids, int32_t id_bits, int64_t T, int64_t k, int64_t E,
+                             int32_t *offsets, int32_t *rows, int32_t *tokens,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* out[r] = x[tokens[r]] for r < P, zeros where tokens[r] is no row of x.
+ * x [T][C] (ldx), out [P][C]; dtype F16, BF16 or F32. */
+nsg_status_t nsg_expert_dispatch(const void *x, int32_t dtype, int64_t T, int64_t C, int64_t ldx,
+                                 const int32_t *tokens, int64_t P, void *out, void *stream);
+
+/* out[t] = sum_j weights[t][j] y[rows[t][j]], summed in fp32 in the order of j
+ * and rounded once; choices that are no row of y are left out, and a token with
+ * none gets zeros.  weights NULL: all 1, which is the gradient of
+ * nsg_expert_dispatch.  y [P][C] (ldy), out [T][C], both of dtype. */
+nsg_status_t nsg_expert_combine(const void *y, int32_t dtype, int64_t P, int64_t C, int64_t ldy,
+                                const int32_t *rows, int64_t T, int64_t k, const float *weights,
+                                void *out, void *stream);
+
+/* The gradient of nsg_expert_combine for dout [T][C] (lddo):
+ *   dy[rows[t][j]] = weights[t][j] dout[t]   [P][C], rounded once; the rows behind
+ *                    offsets[E] are zero
+ *   dw[t][j] = <dout[t], y[rows[t][j]]>      fp32, 0 for a dropped choice
+ * with P = T k, rows and offsets as nsg_expert_sort gives them (every row at
+ * most once).  weights NULL: all 1. */
+nsg_status_t nsg_expert_combine_backward(const void *dout, int64_t lddo, const void *y, int64_t ldy,
+                                         int32_t dtype, int64_t P, int64_t C, const int32_t *offsets,
+                                         int64_t E, const int32_t *rows, int64_t T, int64_t k,
+                                         const float *weights, void *dy, float *dw, void *stream);
+
+/* Quantise x [B][R][C] (ldx; batches R ldx apart) to 8 bits with block scales:
+ *   s = max(amax / F, 2^-126),  q = RNE(x (1 / s)),  x ~ q s
+ * amax: largest finite |x| of the block, F: 448 (e4m3) or 57344 (e5m2), each
+ * operation in fp32.  Infinities and NaN become NaN (an infinity stays one in
+ * e5m2) and do not change the scale of their block.
+ *   block  NSG_BLOCK_ROW: 128 elements of a row; scale [B][Cp/128][R]
+ *          NSG_BLOCK_TILE: 128 x 128 tiles; scale [B][Cp/128][ceil(R/128)]
+ *   q      [B][R][Cp], Cp = C rounded up to a multiple of 128, zeros behind C
+ *   q_t, scale_t  (tiles only, both or neither) the transposed matrix with the
+ *          same numbers: [B][C][Rp] and [B][Rp/128][ceil(C/128)]
+ * B <= 65535. */
+#define NSG_BLOCK_ROW 0
+#define NSG_BLOCK_TILE 1
+nsg_status_t nsg_quantize_fp8(const void *x, int32_t x_dtype, int64_t B, int64_t R, int64_t C,
+                              int64_t ldx, int32_t block, int32_t q_dtype, void *q, float *scale,
+                              void *q_t, float *scale_t, void *stream);
+
+/* Quantise the P sorted rows of E experts along the rows, transposed, as
+ * nsg_expert_wgrad_fp8 contracts them.  Sorted row r is row tokens[r] of
+ * x [R][C] (ldx), or row r where tokens is NULL (then P == R).
+ *   q_t    [C][cap], cap = 128 (floor(P / 128) + E) (nsg_fp8_columns): expert
+ *          e's rows are the columns from the multiple of 128 where the experts
+ *          before it end; every column that is no row holds zeros
+ *   scale  [cap/128][C], one for 128 columns of a row of q_t */
+nsg_status_t nsg_fp8_columns(int64_t P, int64_t E, int64_t *cap);
+nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R, int64_t C, int64_t ldx,
+                                      const int32_t *offsets, int64_t E, const int32_t *tokens, int64_t P,
+                                      int32_t q_dtype, void *q_t, float *scale, void *stream);
+
+/* out_b [M][N] = A_b B_b^T for b in [0, batch): A_b and B_b are the values
+ * q s of operands as nsg_quantize_fp8 lays them out (qa [batch][M][K], qb
+ * [batch][N][K], K their padded length; a_block, b_block say which scales they
+ * have).  Products of a block of 128 are summed in fp32, blocks in fp32, and
+ * the result is rounded once to out_dtype (F16, BF16 or F32).  With a 16-bit
+ * out_dtype the 8-bit matrix instructions are used, which cut the products of 8
+ * consecutive k off at 2^-13 of the largest one's power of two before they are
+ * summed (about 1e-5 relative, far below that rounding); with F32 the products are
+ * exact. */
+nsg_status_t nsg_gemm_fp8_nt(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t batch,
+                             int64_t M, int64_t N, int64_t K, const void *qa, const float *sa,
+                             int32_t a_block, const void *qb, const float *sb, int32_t b_block,
+                             void *out, void *stream);
+
+/* The experts' products: out [P][N], out[r] = A[tokens[r]] B_e^T for the sorted
+ * rows r of expert e (tokens NULL: A[r], T == P), zeros where tokens[r] is no
+ * row of A and behind offsets[E].  qa [T][K] with row scales, qb [E][N][K]. */
+nsg_status_t nsg_expert_gemm_fp8(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t T,
+                                 int64_t P, int64_t E, int64_t N, int64_t K, const void *qa,
+                                 const float *sa, const int32_t *tokens, const void *qb,
+                                 const float *sb, int32_t b_block, const int32_t *offsets, void *out,
+                                 void *stream);
+
+/* The experts' weight gradients: out [E][N][K], out_e = sum over expert e's rows
+ * r of dy[r]^T x[r], for dy [P][N] and x [P][K] quantised by
+ * nsg_quantize_fp8_columns with the same offsets (qa_t [N][cap], qb_t [K][cap]).
+ * An expert without rows gets zeros.  This is the bucket ns_muon_step takes. */
+nsg_status_t nsg_expert_wgrad_fp8(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t P,
+                                  int64_t E, int64_t N, int64_t K, const void *qa_t, const float *sa,
+                                  const void *qb_t, const float *sb, const int32_t *offsets, void *out,
+                                  void *stream);
 
 #ifdef __cplusplus
 }

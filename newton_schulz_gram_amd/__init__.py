@@ -13,14 +13,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libnsg.so")
 
-NSG_F16, NSG_BF16, NSG_F32 = 0, 1, 2
+NSG_F16, NSG_BF16, NSG_F32, NSG_F8E4M3, NSG_F8E5M2 = 0, 1, 2, 3, 4
 NSG_STANDARD, NSG_GRAM = 0, 1
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)  # "muon" kernel card, "How it works"
 
@@ -28,6 +28,7 @@ _DT = {torch.float16: NSG_F16, torch.bfloat16: NSG_BF16, torch.float32: NSG_F32}
 _DT_NAMES = {"f16": NSG_F16, "fp16": NSG_F16, "float16": NSG_F16,
              "bf16": NSG_BF16, "bfloat16": NSG_BF16,
              "f32": NSG_F32, "fp32": NSG_F32, "float32": NSG_F32}
+_F8 = {torch.float8_e4m3fn: NSG_F8E4M3, torch.float8_e5m2: NSG_F8E5M2}
 _MODES = {"standard": NSG_STANDARD, "gram": NSG_GRAM}
 KIND_NAMES = {0: "norm_reduce", 1: "scale_cast_transpose", 2: "gemm_nt", 3: "gemm_nt_sym"}
 
@@ -82,7 +83,10 @@ EXPORTS = ("ns_default_params", "ns_workspace_size", "ns_orthogonalize", "ns_sta
            "ns_flops", "ns_plan", "ns_timing_enable", "ns_timing_collect", "nsg_copy",
            "nsg_gemm_nt", "ns_select_workspace_size", "ns_orthogonalize_selected",
            "nsg_l1_workspace_size", "nsg_l1_norms", "nsg_topk", "ns_muon_momentum", "ns_muon_update",
-           "ns_muon_workspace_size", "ns_muon_step", "ns_select_count", "ns_orthogonalize_noalloc")
+           "ns_muon_workspace_size", "ns_muon_step", "ns_select_count", "ns_orthogonalize_noalloc",
+           "nsg_expert_sort_workspace_size", "nsg_expert_sort", "nsg_expert_dispatch", "nsg_expert_combine",
+           "nsg_expert_combine_backward", "nsg_quantize_fp8", "nsg_fp8_columns", "nsg_quantize_fp8_columns",
+           "nsg_gemm_fp8_nt", "nsg_expert_gemm_fp8", "nsg_expert_wgrad_fp8")
 SELECT_ROWS, SELECT_COLS, SELECT_SMALLER = 0, 1, -1
 
 _lib = None
@@ -144,6 +148,29 @@ def lib() -> ctypes.CDLL:
     L.ns_muon_step.argtypes = [vp, i32, vp, i32, vp, i32, i64, i64, i64, f32, f64, f64, f64, i32, u64, u64, P,
                                vp, sz, vp, vp]
     L.ns_muon_step.restype = i32
+    psz = ctypes.POINTER(sz)
+    L.nsg_expert_sort_workspace_size.argtypes = [i64, i64, i64, psz]
+    L.nsg_expert_sort_workspace_size.restype = i32
+    L.nsg_expert_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.nsg_expert_sort.restype = i32
+    L.nsg_expert_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp]
+    L.nsg_expert_dispatch.restype = i32
+    L.nsg_expert_combine.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, vp]
+    L.nsg_expert_combine.restype = i32
+    L.nsg_expert_combine_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp]
+    L.nsg_expert_combine_backward.restype = i32
+    L.nsg_quantize_fp8.argtypes = [vp, i32, i64, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp]
+    L.nsg_quantize_fp8.restype = i32
+    L.nsg_fp8_columns.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    L.nsg_fp8_columns.restype = i32
+    L.nsg_quantize_fp8_columns.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, vp, vp]
+    L.nsg_quantize_fp8_columns.restype = i32
+    L.nsg_gemm_fp8_nt.argtypes = [i32, i32, i32, i64, i64, i64, i64, vp, vp, i32, vp, vp, i32, vp, vp]
+    L.nsg_gemm_fp8_nt.restype = i32
+    L.nsg_expert_gemm_fp8.argtypes = [i32, i32, i32, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    L.nsg_expert_gemm_fp8.restype = i32
+    L.nsg_expert_wgrad_fp8.argtypes = [i32, i32, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+    L.nsg_expert_wgrad_fp8.restype = i32
     _lib = L
     return L
 
@@ -545,3 +572,330 @@ def muon_step(W: torch.Tensor, M: torch.Tensor, G: torch.Tensor, mu: float, lr: 
             ctypes.c_void_p(status.data_ptr()) if status is not None else None,
             ctypes.c_void_p(_stream_handle(Ws.device))), "ns_muon_step")
     return W, M
+
+
+# ---------------------------------------------------------------------------
+# The expert layer around the Muon step: tokens sorted by expert and back, 8-bit
+# operands with one scale for each block of 128, their products
+# ---------------------------------------------------------------------------
+
+class ExpertPlan(NamedTuple):
+    """Where expert_sort puts the T x k choices of a router.
+
+    offsets [E + 1] int32: sorted rows offsets[e] .. offsets[e + 1] - 1 are expert
+    e's; rows [T, k] int32: the sorted row of each choice, -1 if it was dropped;
+    tokens [T k] int32: the token in each sorted row, -1 behind offsets[E]."""
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    tokens: torch.Tensor
+
+
+def _launch(device, what: str, fn, *args):
+    """Call a C entry point on `device`, with its current stream as the last argument."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_handle(device)), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_handle(device)), what)
+
+
+def _gpu(t: torch.Tensor, what: str):
+    if not t.is_cuda:
+        raise ValueError(f"{what} needs GPU tensors (no CPU path)")
+    return t.device
+
+
+def _ints(t: torch.Tensor, shape, name: str, device):
+    """An int32 plan array of this shape (None: any), contiguous, on the device."""
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a contiguous int32 tensor{'' if shape is None else ' of shape %s' % (tuple(shape),)}"
+                         " on the input's device")
+
+
+def _matrix(t: torch.Tensor, name: str, device=None):
+    """Rows of a 2-D tensor with unit column stride: their pitch in elements."""
+    if t.dim() != 2 or t.dtype not in _DT:
+        raise ValueError(f"{name} must be a 2-D float16, bfloat16 or float32 tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on the input's device")
+    return _pitch(t, name)
+
+
+def _pitch(t: torch.Tensor, name: str) -> int:
+    """Distance of the rows of t [..., R, C]; its rows must be packed and not overlap."""
+    R, C = t.shape[-2:]
+    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs unit column stride")
+    ld = t.stride(-2) if R > 1 else C
+    if ld < C:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def _router_weights(weights: Optional[torch.Tensor], rows: torch.Tensor):
+    if weights is None:
+        return None
+    if weights.dtype != torch.float32 or weights.shape != rows.shape or not weights.is_contiguous() or \
+            weights.device != rows.device:
+        raise ValueError("weights must be a contiguous float32 [T, k] tensor on the input's device")
+    return weights.data_ptr()
+
+
+def _plan_rows(plan: ExpertPlan, device):
+    if plan.rows.dim() != 2:
+        raise ValueError("plan.rows must be [T, k]")
+    _ints(plan.rows, None, "plan.rows", device)
+    return plan.rows.shape
+
+
+def expert_sort(ids: torch.Tensor, num_experts: int, workspace: Optional[torch.Tensor] = None) -> ExpertPlan:
+    """Sort the choices ids [T, k] (int32 or int64) of a router by expert, stably.
+
+    An id outside 0 .. num_experts - 1 is dropped.  `workspace`: a uint8 tensor
+    of expert_sort_workspace_size(T, k, num_experts) bytes (allocated if not given)."""
+    device = _gpu(ids, "expert_sort")
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous [T, k] int32 or int64 tensor")
+    T, k = ids.shape
+    E = int(num_experts)
+    need = expert_sort_workspace_size(T, k, E)
+    if need and (workspace is None or nbytes(workspace) < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        check_workspace(workspace, device)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+    rows = torch.empty((T, k), dtype=torch.int32, device=device)
+    tokens = torch.empty(T * k, dtype=torch.int32, device=device)
+    _launch(device, "nsg_expert_sort", lib().nsg_expert_sort, ids.data_ptr(), 8 * ids.element_size(), T, k, E,
+            offsets.data_ptr(), rows.data_ptr(), tokens.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None, nbytes(workspace) if workspace is not None else 0)
+    return ExpertPlan(offsets, rows, tokens)
+
+
+def expert_sort_workspace_size(T: int, k: int, num_experts: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().nsg_expert_sort_workspace_size(T, k, num_experts, ctypes.byref(out)), "nsg_expert_sort_workspace_size")
+    return out.value
+
+
+def expert_dispatch(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
+    """The sorted rows [T k, C] of tokens x [T, C]: row r is x[plan.tokens[r]],
+    zeros behind the last expert's.  Its gradient is expert_combine without weights."""
+    device = _gpu(x, "expert_dispatch")
+    ld = _matrix(x, "x")
+    _ints(plan.tokens, None, "plan.tokens", device)
+    T, C = x.shape
+    P = plan.tokens.numel()
+    out = torch.empty((P, C), dtype=x.dtype, device=device)
+    _launch(device, "nsg_expert_dispatch", lib().nsg_expert_dispatch, x.data_ptr(), _DT[x.dtype], T, C, ld,
+            plan.tokens.data_ptr(), P, out.data_ptr())
+    return out
+
+
+def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Bring sorted rows y [T k, C] back: out[t] = sum_j weights[t, j] y[plan.rows[t, j]]
+    (fp32 sums, rounded once; dropped choices are left out).  weights: float32
+    [T, k], or None for all 1, which is the gradient of expert_dispatch."""
+    device = _gpu(y, "expert_combine")
+    ld = _matrix(y, "y")
+    T, k = _plan_rows(plan, device)
+    P, C = y.shape
+    if P != T * k:
+        raise ValueError(f"y has {P} rows, the plan {T * k}")
+    out = torch.empty((T, C), dtype=y.dtype, device=device)
+    _launch(device, "nsg_expert_combine", lib().nsg_expert_combine, y.data_ptr(), _DT[y.dtype], P, C, ld,
+            plan.rows.data_ptr(), T, k, _router_weights(weights, plan.rows), out.data_ptr())
+    return out
+
+
+def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
+                            weights: Optional[torch.Tensor] = None):
+    """The gradient of expert_combine: (dy [T k, C], dw [T, k] float32) for dout [T, C].
+    dy is zero in the rows behind the last expert's, dw for a dropped choice."""
+    device = _gpu(dout, "expert_combine_backward")
+    lddo, ldy = _matrix(dout, "dout"), _matrix(y, "y", device)
+    T, k = _plan_rows(plan, device)
+    P, C = y.shape
+    _ints(plan.offsets, None, "plan.offsets", device)
+    if P != T * k or dout.shape != (T, C) or dout.dtype != y.dtype:
+        raise ValueError("dout must be [T, C] and y [T k, C] of the plan, of one dtype")
+    dy = torch.empty((P, C), dtype=y.dtype, device=device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=device)
+    _launch(device, "nsg_expert_combine_backward", lib().nsg_expert_combine_backward, dout.data_ptr(), lddo, y.data_ptr(),
+            ldy, _DT[y.dtype], P, C, plan.offsets.data_ptr(), plan.offsets.numel() - 1, plan.rows.data_ptr(), T, k,
+            _router_weights(weights, plan.rows), dy.data_ptr(), dw.data_ptr())
+    return dy, dw
+
+
+FP8_BLOCK = 128
+_BLOCKS = {"row": 0, "tile": 1}
+
+
+def _up128(n: int) -> int:
+    return -(-n // FP8_BLOCK) * FP8_BLOCK
+
+
+def _f8_code(dtype) -> int:
+    if dtype not in _F8:
+        raise TypeError(f"unsupported 8-bit dtype {dtype}")
+    return _F8[dtype]
+
+
+def quantize_fp8(x: torch.Tensor, block: str = "row", dtype=torch.float8_e4m3fn, transposed: bool = False):
+    """Quantise x [R, C] or [B, R, C] to 8 bits with one fp32 scale for 128 elements
+    of a row ("row") or a 128 x 128 tile ("tile").
+
+    Returns (q, scale): q [(B,) R, Cp] with Cp = C rounded up to 128 and zeros
+    behind C, scale [(B,) Cp/128, R] or [(B,) Cp/128, ceil(R/128)]; x ~ q * scale
+    with scale = max(amax / F, 2^-126).  With `transposed` (tiles) also the
+    operand of the transposed matrix, (q, scale, qt, scale_t), with the same
+    numbers.  Infinities and NaN do not change their block's scale and become NaN
+    (an infinity stays one in float8_e5m2)."""
+    device = _gpu(x, "quantize_fp8")
+    xs = x.unsqueeze(0) if x.dim() == 2 else x
+    if xs.dim() != 3 or x.dtype not in _DT:
+        raise ValueError("expected a float16, bfloat16 or float32 tensor [R, C] or [B, R, C]")
+    if block not in _BLOCKS:
+        raise ValueError("block must be 'row' or 'tile'")
+    if transposed and block != "tile":
+        raise ValueError("transposed needs block='tile'")
+    f8 = _f8_code(dtype)
+    ld = _pitch(xs, "x")
+    B, R, C = xs.shape
+    if B > 1 and xs.stride(0) != R * ld:
+        raise ValueError("x needs packed batches")
+    Rp, Cp = _up128(R), _up128(C)
+    lead = () if x.dim() == 2 else (B,)
+    q = torch.empty((*lead, R, Cp), dtype=dtype, device=device)
+    s = torch.empty((*lead, Cp // 128, R if block == "row" else Rp // 128), dtype=torch.float32, device=device)
+    qt = st = None
+    if transposed:
+        qt = torch.empty((*lead, C, Rp), dtype=dtype, device=device)
+        st = torch.empty((*lead, Rp // 128, Cp // 128), dtype=torch.float32, device=device)
+    _launch(device, "nsg_quantize_fp8", lib().nsg_quantize_fp8, xs.data_ptr(), _DT[x.dtype], B, R, C, ld, _BLOCKS[block],
+            f8, q.data_ptr(), s.data_ptr(), qt.data_ptr() if transposed else None, st.data_ptr() if transposed else None)
+    return (q, s, qt, st) if transposed else (q, s)
+
+
+def fp8_columns(P: int, num_experts: int) -> int:
+    """Columns of the layout of quantize_fp8_columns: 128 (floor(P / 128) + num_experts)."""
+    out = ctypes.c_int64(0)
+    _check(lib().nsg_fp8_columns(P, num_experts, ctypes.byref(out)), "nsg_fp8_columns")
+    return out.value
+
+
+def quantize_fp8_columns(x: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                         dtype=torch.float8_e4m3fn):
+    """Quantise sorted rows along the rows, transposed, as expert_wgrad_fp8 takes them.
+
+    offsets [E + 1]: the experts' rows.  Sorted row r is x[r], or x[rows[r]] with
+    rows (plan.tokens).  Returns (qt [C, cap], scale [cap/128, C]) with
+    cap = fp8_columns(P, E); each expert's rows start at a multiple of 128, the
+    columns that are no row hold zeros."""
+    device = _gpu(x, "quantize_fp8_columns")
+    ld = _matrix(x, "x")
+    f8 = _f8_code(dtype)
+    _ints(offsets, None, "offsets", device)
+    if rows is not None:
+        _ints(rows, None, "rows", device)
+    R, C = x.shape
+    P = R if rows is None else rows.numel()
+    E = offsets.numel() - 1
+    cap = fp8_columns(P, E)
+    qt = torch.empty((C, cap), dtype=dtype, device=device)
+    s = torch.empty((cap // 128, C), dtype=torch.float32, device=device)
+    _launch(device, "nsg_quantize_fp8_columns", lib().nsg_quantize_fp8_columns, x.data_ptr(), _DT[x.dtype], R, C, ld,
+            offsets.data_ptr(), E, rows.data_ptr() if rows is not None else None, P, f8, qt.data_ptr(), s.data_ptr())
+    return qt, s
+
+
+def _operand(q: torch.Tensor, s: torch.Tensor, name: str, dims: int, device, kinds=("row", "tile")) -> int:
+    """Check an operand of quantize_fp8's layout; its block code."""
+    if q.dim() != dims or q.dtype not in _F8 or not q.is_contiguous() or q.device != device:
+        raise ValueError(f"{name} must be a contiguous {dims}-D float8_e4m3fn or float8_e5m2 tensor on one device")
+    R, K = q.shape[-2:]
+    if K % FP8_BLOCK:
+        raise ValueError(f"{name} needs rows padded to a multiple of {FP8_BLOCK}")
+    if s.dtype != torch.float32 or not s.is_contiguous() or s.device != device or s.dim() != dims or \
+            s.shape[:-1] != (*q.shape[:-2], K // FP8_BLOCK):
+        raise ValueError(f"the scales of {name} must be a contiguous float32 tensor [..., K/128, rows or tiles]")
+    n = s.shape[-1]
+    if "row" in kinds and n == R:
+        return 0
+    if "tile" in kinds and n == -(-R // FP8_BLOCK):
+        return 1
+    raise ValueError(f"the scales of {name} fit neither its rows nor its tiles")
+
+
+def _product_out(out: Optional[torch.Tensor], shape, out_dtype, device):
+    if out is None:
+        if out_dtype not in _DT:
+            raise TypeError(f"unsupported dtype {out_dtype}")
+        return torch.empty(shape, dtype=out_dtype, device=device)
+    if out.shape != shape or out.dtype not in _DT or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous float tensor of shape {tuple(shape)} on the operands' device")
+    return out
+
+
+def gemm_fp8_nt(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, out_dtype=torch.bfloat16,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A B^T of two 8-bit operands as quantize_fp8 returns them: qa [M, K] and qb
+    [N, K], or batches [b, M, K] and [b, N, K]; either may have row or tile
+    scales.  fp32 sums, one rounding to out_dtype."""
+    device = _gpu(qa, "gemm_fp8_nt")
+    ab = _operand(qa, sa, "qa", 2 if qa.dim() == 2 else 3, device)
+    bb = _operand(qb, sb, "qb", qa.dim(), device)
+    if qa.shape[-1] != qb.shape[-1] or qa.shape[:-2] != qb.shape[:-2]:
+        raise ValueError(f"operands {tuple(qa.shape)} and {tuple(qb.shape)} do not fit")
+    M, K = qa.shape[-2:]
+    N = qb.shape[-2]
+    out = _product_out(out, (*qa.shape[:-2], M, N), out_dtype, device)
+    _launch(device, "nsg_gemm_fp8_nt", lib().nsg_gemm_fp8_nt, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype],
+            qa.shape[0] if qa.dim() == 3 else 1, M, N, K, qa.data_ptr(), sa.data_ptr(), ab, qb.data_ptr(), sb.data_ptr(),
+            bb, out.data_ptr())
+    return out
+
+
+def expert_gemm_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                    rows: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each expert's product: out[r] = A[rows[r]] B_e^T for the sorted rows r of
+    expert e (A[r] without rows), zeros behind offsets[E].  qa [T, K] with row
+    scales, qb [E, N, K]; offsets and rows: a plan's offsets and tokens."""
+    device = _gpu(qa, "expert_gemm_fp8")
+    _operand(qa, sa, "qa", 2, device, ("row",))
+    bb = _operand(qb, sb, "qb", 3, device)
+    T, K = qa.shape
+    E, N, Kb = qb.shape
+    _ints(offsets, (E + 1,), "offsets", device)
+    if rows is not None:
+        _ints(rows, None, "rows", device)
+    if K != Kb:
+        raise ValueError(f"operands {tuple(qa.shape)} and {tuple(qb.shape)} do not fit")
+    P = T if rows is None else rows.numel()
+    out = _product_out(out, (P, N), out_dtype, device)
+    _launch(device, "nsg_expert_gemm_fp8", lib().nsg_expert_gemm_fp8, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype], T, P,
+            E, N, K, qa.data_ptr(), sa.data_ptr(), rows.data_ptr() if rows is not None else None, qb.data_ptr(),
+            sb.data_ptr(), bb, offsets.data_ptr(), out.data_ptr())
+    return out
+
+
+def expert_wgrad_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                     out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' weight gradients [E, N, K], the bucket muon_step takes: out[e]
+    = dy_e^T x_e over expert e's rows, zeros for one without.  (qa [N, cap], sa)
+    and (qb [K, cap], sb) are quantize_fp8_columns of dy and x with these offsets."""
+    device = _gpu(qa, "expert_wgrad_fp8")
+    _operand(qa, sa, "qa", 2, device, ("row",))
+    _operand(qb, sb, "qb", 2, device, ("row",))
+    _ints(offsets, None, "offsets", device)
+    E = offsets.numel() - 1
+    (N, cap), K = qa.shape, qb.shape[0]
+    P = cap - FP8_BLOCK * E  # any number of rows from here on to P + 127 has this layout
+    if qb.shape[1] != cap or P < 0:
+        raise ValueError(f"operands {tuple(qa.shape)} and {tuple(qb.shape)} do not fit {E} experts")
+    out = _product_out(out, (E, N, K), out_dtype, device)
+    _launch(device, "nsg_expert_wgrad_fp8", lib().nsg_expert_wgrad_fp8, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype],
+            P + FP8_BLOCK - 1, E, N, K, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), offsets.data_ptr(),
+            out.data_ptr())
+    return out

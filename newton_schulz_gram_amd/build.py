@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnsg.so")
 
-SOURCES = ["nsg_api.cpp", "nsg_kernels.hip", "nsg_select.hip", "nsg_muon.hip"]
+SOURCES = ["nsg_api.cpp", "nsg_kernels.hip", "nsg_select.hip", "nsg_muon.hip",
+           "nsg_expert_api.cpp", "nsg_expert.hip", "nsg_fp8.hip", "nsg_fp8_gemm.hip"]
 # per-source flags: the Muon-step kernels round every fp32 operation on its own
 # (hipcc's default contraction would fuse multiply-adds and ignore pragmas)
 EXTRA = {"nsg_muon.hip": ["-ffp-contract=off"]}

@@ -1,0 +1,348 @@
+// Tokens sorted by expert and back, on gfx950.
+//
+//   sort      a stable counting sort of the P = T k choices by expert:
+//             offsets[e] = choices of the experts below e; rows[p] = offsets[id]
+//             + earlier choices of the same expert, -1 for an id outside 0 .. E-1;
+//             tokens[rows[p]] = p / k, -1 behind offsets[E].
+//   dispatch  out[r] = x[tokens[r]], 0 where tokens[r] is no row of x
+//   combine   out[t] = sum_j w[t, j] y[rows[t, j]] (w = 1 where not given, which
+//             is dispatch's gradient), in fp32, j in order, rounded once
+//   combine's gradient  dy[rows[t, j]] = w[t, j] dout[t],
+//             dw[t, j] = <dout[t], y[rows[t, j]]> in fp32
+//
+// The sort touches 16 bytes a choice and is bound by latency; the others are
+// streaming passes, bound by HBM.  No atomics on memory: counts are integers,
+// sums have a fixed order, so every result is reproducible bit for bit.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "nsg_expert.h"
+#include "nsg_segments.h"
+
+namespace nsg {
+
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+static_assert(NSG_MAX_EXPERTS <= kSortThreads, "thread e scans expert e");
+constexpr int kSortMinChunk = 4096;  // choices of one workgroup, at least
+constexpr int kSortMaxChunks = 128;  // every workgroup of the second pass reads the whole table
+
+static int64_t sort_chunk(int64_t P) {
+  int64_t c = (P + kSortMaxChunks - 1) / kSortMaxChunks;
+  if (c < kSortMinChunk) c = kSortMinChunk;
+  return (c + kSortThreads - 1) / kSortThreads * kSortThreads;
+}
+int expert_sort_chunks(int64_t P) { return P == 0 ? 1 : (int)((P + sort_chunk(P) - 1) / sort_chunk(P)); }
+
+// the expert of choice i, or -1
+template <typename TI> __device__ __forceinline__ int expert_of(const TI *ids, int64_t i, int E) {
+  const TI v = ids[i];
+  return v >= 0 && v < (TI)E ? (int)v : -1;
+}
+
+// choices of each expert in each chunk
+template <typename TI>
+__global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const TI *__restrict__ ids, int64_t P, int64_t chunk,
+                                                                    int E, int32_t *__restrict__ table) {
+  __shared__ int count[NSG_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < E; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min(P, i0 + chunk);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
+    const int e = expert_of(ids, i, E);
+    if (e >= 0) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kSortThreads) table[(size_t)blockIdx.x * E + e] = count[e];
+}
+
+// Place the choices of chunk blockIdx.x.  at[w][e]: where the next choice of
+// expert e in wave w's part of the chunk goes.  A wave takes its part 64 choices
+// at a time: the lanes with the same expert find each other by ballots over the
+// bits of the id, so their order is that of the choices.
+template <typename TI>
+__global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const TI *__restrict__ ids, int64_t P, int64_t chunk,
+                                                                    int chunks, int k, int E, int bits,
+                                                                    const int32_t *__restrict__ table,
+                                                                    int32_t *__restrict__ offsets,
+                                                                    int32_t *__restrict__ rows,
+                                                                    int32_t *__restrict__ tokens) {
+  __shared__ int at[kSortWaves * NSG_MAX_EXPERTS];
+  __shared__ int sh[kSortWaves + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min(P, i0 + chunk);
+  const int64_t part = chunk / kSortWaves;  // a multiple of 64
+  const int64_t w0 = i0 + wave * part, w1 = min(i1, w0 + part);
+  for (int i = threadIdx.x; i < kSortWaves * E; i += kSortThreads) at[i] = 0;
+  __syncthreads();
+  for (int64_t i = w0 + lane; i < w1; i += 64) {
+    const int e = expert_of(ids, i, E);
+    if (e >= 0) atomicAdd(&at[wave * E + e], 1);
+  }
+  __syncthreads();
+  // thread e: all of expert e's choices, and those before this chunk
+  const int e = threadIdx.x;
+  int total = 0, before = 0;
+  if (e < E) {
+    if (chunks == 1) {
+      for (int w = 0; w < kSortWaves; ++w) total += at[w * E + e];
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const int n = table[(size_t)c * E + e];
+        total += n;
+        before += c < (int)blockIdx.x ? n : 0;
+      }
+    }
+  }
+  int all;
+  const int first = block_before<kSortThreads>(total, sh, all);
+  if (e < E) {
+    int next = first + before;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = at[w * E + e];
+      at[w * E + e] = next;
+      next += n;
+    }
+    if (blockIdx.x == 0) {
+      offsets[e] = first;
+      if (e == E - 1) offsets[E] = all;
+    }
+  }
+  __syncthreads();
+  volatile int *mine = at + wave * E;
+  for (int64_t i = w0; i < w1; i += 64) {
+    const int64_t p = i + lane;
+    const int id = p < w1 ? expert_of(ids, p, E) : -1;
+    uint64_t same = __ballot(id >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot((id >> b) & 1);
+      same &= (id >> b) & 1 ? one : ~one;
+    }
+    if (id >= 0) {
+      const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
+      const int base = mine[id];
+      __builtin_amdgcn_wave_barrier();
+      if (rank == n - 1) mine[id] = base + n;
+      rows[p] = base + rank;
+      tokens[base + rank] = (int32_t)((uint32_t)p / (uint32_t)k);
+    } else if (p < w1) {
+      rows[p] = -1;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  for (int64_t p = i0 + threadIdx.x; p < i1; p += kSortThreads)
+    if (p >= all) tokens[p] = -1;
+}
+
+template <typename TI>
+static hipError_t sort_t(const void *ids, int64_t P, int k, int E, int32_t *offsets, int32_t *rows, int32_t *tokens,
+                         int32_t *table, hipStream_t s) {
+  const int64_t chunk = sort_chunk(P);
+  const int chunks = expert_sort_chunks(P);
+  int bits = 0;
+  while ((1 << bits) < E) ++bits;
+  if (chunks > 1) {
+    hipLaunchKernelGGL(expert_count_kernel<TI>, dim3((unsigned)chunks), dim3(kSortThreads), 0, s,
+                       (const TI *)ids, P, chunk, E, table);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(expert_place_kernel<TI>, dim3((unsigned)chunks), dim3(kSortThreads), 0, s, (const TI *)ids, P, chunk, chunks, k, E, bits,
+                     (const int32_t *)table, offsets, rows, tokens);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_sort(const void *ids, int wide, int64_t P, int k, int E, int32_t *offsets, int32_t *rows,
+                              int32_t *tokens, int32_t *table, hipStream_t s) {
+  return wide ? sort_t<int64_t>(ids, P, k, E, offsets, rows, tokens, table, s)
+              : sort_t<int32_t>(ids, P, k, E, offsets, rows, tokens, table, s);
+}
+
+// ---------------------------------------------------------------------------
+// dispatch: one wave per row, 16 bytes a lane.  Elements are moved as they are,
+// so only their size matters.
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename V>
+__global__ void __launch_bounds__(256) expert_dispatch_kernel(const V *__restrict__ x, int64_t T, int64_t n, int64_t ldx,
+                                                              const int32_t *__restrict__ tokens, int64_t P,
+                                                              V *__restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= P) return;
+  const int64_t t = tokens[r];
+  V *dst = out + r * n;
+  if (t < 0 || t >= T) {
+    for (int64_t c = lane; c < n; c += 64) dst[c] = V(0);
+    return;
+  }
+  const V *src = x + t * ldx;
+#pragma unroll 4
+  for (int64_t c = lane; c < n; c += 64) dst[c] = src[c];
+}
+
+static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C, int64_t ldx, const int32_t *tokens,
+                                  int64_t P, void *out, hipStream_t s) {
+  const dim3 grid((unsigned)((P + 3) / 4));
+  const int64_t per = 16 / elem;
+  if (aligned16(x) && aligned16(out) && C % per == 0 && ldx % per == 0)
+    hipLaunchKernelGGL(expert_dispatch_kernel<u32x4>, grid, dim3(256), 0, s, (const u32x4 *)x, T, C / per, ldx / per,
+                       tokens, P, (u32x4 *)out);
+  else if (elem == 4)
+    hipLaunchKernelGGL(expert_dispatch_kernel<uint32_t>, grid, dim3(256), 0, s, (const uint32_t *)x, T, C, ldx, tokens, P,
+                       (uint32_t *)out);
+  else
+    hipLaunchKernelGGL(expert_dispatch_kernel<uint16_t>, grid, dim3(256), 0, s, (const uint16_t *)x, T, C, ldx, tokens, P,
+                       (uint16_t *)out);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// combine and its gradient.  A lane owns V consecutive elements of a row: 16
+// bytes of them, or one element where rows do not take 16-byte accesses.
+// ---------------------------------------------------------------------------
+template <typename T, int V> struct Row {
+  typedef T vec __attribute__((ext_vector_type(V)));
+  static __device__ __forceinline__ void load(const T *p, float (&f)[V]) {
+    const vec x = *reinterpret_cast<const vec *>(p);
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = (float)x[v];
+  }
+  static __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
+    vec x;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = (T)f[v];
+    *reinterpret_cast<vec *>(p) = x;
+  }
+};
+template <typename T> struct Row<T, 1> {
+  static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = (float)*p; }
+  static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = (T)f[0]; }
+};
+
+// One wave per 64 V elements of a token (part blockIdx.y of 4 tokens).
+template <typename T, int V>
+__global__ void __launch_bounds__(256) expert_combine_kernel(const T *__restrict__ y, int64_t P, int64_t C, int64_t ldy,
+                                                             const int32_t *__restrict__ rows, int64_t ntok, int k,
+                                                             const float *__restrict__ w, T *__restrict__ out) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * V;
+  if (t >= ntok || c >= C) return;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = rows[t * k + j];
+    if (r < 0 || r >= P) continue;
+    const float g = w ? w[t * k + j] : 1.f;
+    float f[V];
+    Row<T, V>::load(y + r * ldy + c, f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(g, f[v], acc[v]);
+  }
+  Row<T, V>::store(out + t * C + c, acc);
+}
+
+// One wave per token: dout stays in cache over the choices.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) expert_combine_backward_kernel(
+    const T *__restrict__ dout, int64_t lddo, const T *__restrict__ y, int64_t ldy, int64_t P, int64_t C,
+    const int32_t *__restrict__ offsets, int E, const int32_t *__restrict__ rows, int64_t ntok, int k,
+    const float *__restrict__ w, T *__restrict__ dy, float *__restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= ntok) return;
+  const int64_t all = seg_clamp(offsets[E], 0, (int)P);
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = t * k + j;
+    const int64_t r = rows[p];
+    const bool there = r >= 0 && r < P;
+    const float g = w ? w[p] : 1.f;
+    float dot = 0.f;
+    if (there) {
+      for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) {
+        float d[V], f[V];
+        Row<T, V>::load(dout + t * lddo + c, d);
+        Row<T, V>::load(y + r * ldy + c, f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          dot = fmaf(d[v], f[v], dot);
+          d[v] *= g;
+        }
+        Row<T, V>::store(dy + r * C + c, d);
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
+    if (lane == 0) dw[p] = there ? dot : 0.f;
+    if (p >= all && p < P) {  // a row behind the last expert's
+      float z[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) z[v] = 0.f;
+      for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) Row<T, V>::store(dy + p * C + c, z);
+    }
+  }
+}
+
+template <typename T, int V>
+static hipError_t combine_v(const void *y, int64_t P, int64_t C, int64_t ldy, const int32_t *rows, int64_t ntok, int k,
+                            const float *w, void *out, hipStream_t s) {
+  const int64_t parts = (C + 64 * V - 1) / (64 * V);
+  hipLaunchKernelGGL((expert_combine_kernel<T, V>), dim3((unsigned)((ntok + 3) / 4), (unsigned)parts), dim3(256), 0, s,
+                     (const T *)y, P, C, ldy, rows, ntok, k, w, (T *)out);
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t combine_t(const void *y, int64_t P, int64_t C, int64_t ldy, const int32_t *rows, int64_t ntok, int k,
+                            const float *w, void *out, hipStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (aligned16(y) && aligned16(out) && C % V == 0 && ldy % V == 0)
+    return combine_v<T, V>(y, P, C, ldy, rows, ntok, k, w, out, s);
+  return combine_v<T, 1>(y, P, C, ldy, rows, ntok, k, w, out, s);
+}
+
+hipError_t launch_expert_combine(const void *y, int dtype, int64_t P, int64_t C, int64_t ldy, const int32_t *rows,
+                                 int64_t T, int k, const float *w, void *out, hipStream_t s) {
+  switch (dtype) {
+    case NSG_F16: return combine_t<_Float16>(y, P, C, ldy, rows, T, k, w, out, s);
+    case NSG_BF16: return combine_t<__bf16>(y, P, C, ldy, rows, T, k, w, out, s);
+    default: return combine_t<float>(y, P, C, ldy, rows, T, k, w, out, s);
+  }
+}
+
+template <typename T>
+static hipError_t backward_t(const void *dout, int64_t lddo, const void *y, int64_t ldy, int64_t P, int64_t C,
+                             const int32_t *offsets, int E, const int32_t *rows, int64_t ntok, int k, const float *w,
+                             void *dy, float *dw, hipStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const dim3 grid((unsigned)((ntok + 3) / 4));
+  if (aligned16(dout) && aligned16(y) && aligned16(dy) && C % V == 0 && ldy % V == 0 && lddo % V == 0)
+    hipLaunchKernelGGL((expert_combine_backward_kernel<T, V>), grid, dim3(256), 0, s, (const T *)dout, lddo,
+                       (const T *)y, ldy, P, C, offsets, E, rows, ntok, k, w, (T *)dy, dw);
+  else
+    hipLaunchKernelGGL((expert_combine_backward_kernel<T, 1>), grid, dim3(256), 0, s, (const T *)dout, lddo,
+                       (const T *)y, ldy, P, C, offsets, E, rows, ntok, k, w, (T *)dy, dw);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_backward(const void *dout, int64_t lddo, const void *y, int64_t ldy, int dtype,
+                                          int64_t P, int64_t C, const int32_t *offsets, int E, const int32_t *rows,
+                                          int64_t T, int k, const float *w, void *dy, float *dw, hipStream_t s) {
+  switch (dtype) {
+    case NSG_F16: return backward_t<_Float16>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
+    case NSG_BF16: return backward_t<__bf16>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
+    default: return backward_t<float>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
+  }
+}
+
+}  // namespace nsg

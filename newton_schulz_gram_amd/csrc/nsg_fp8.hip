@@ -1,0 +1,319 @@
+// 8-bit floating point operands with one fp32 scale for each block of 128, on
+// gfx950.
+//
+//   s = max(amax / F, 2^-126),  q = RNE_8(x (1 / s)),  x ~ q s
+// with amax the largest finite |x| of the block and F the type's largest value
+// (448 for e4m3, 57344 for e5m2); amax / F, 1 / s and the product are one fp32
+// operation each.  |x| (1 / s) exceeds F by 2^-22 relative at most, far less
+// than half a step, so nothing saturates.  An infinity or NaN does not take
+// part in amax: it becomes NaN (in e5m2 an infinity stays one) and reaches only
+// the products it takes part in, while the rest of its block keeps its scale.
+//
+// A block is 128 elements of a row (activations, as the product contracts
+// them), a 128 x 128 tile (weights: the same numbers then serve the product
+// with the matrix and with its transpose, which is written in the same pass),
+// or 128 rows of a column (operands of the weight gradients, which contract
+// over rows; written transposed, each expert's rows starting at a multiple of
+// 128 columns).  Rows of q are padded with zeros to a multiple of 128; scales
+// are stored block index first, so that a product's tile reads consecutive ones.
+//
+// All three are bound by HBM: x read once, q (1 byte) and s (1/32 byte) written.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "nsg_expert.h"
+#include "nsg_segments.h"
+
+namespace nsg {
+
+__device__ __forceinline__ float f8_top(int f8) { return f8 == NSG_F8E4M3 ? 448.f : 57344.f; }
+__device__ __forceinline__ float f8_scale(float amax, float top) { return fmaxf(amax / top, 0x1p-126f); }
+// |v|, or 0 for an infinity or NaN
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = __builtin_fabsf(v);
+  return a < __builtin_inff() ? a : 0.f;
+}
+// four values to four bytes, rounded to nearest even
+template <bool E4M3> __device__ __forceinline__ uint32_t f8_pack(float a, float b, float c, float d) {
+  int w = 0;
+  if constexpr (E4M3) {
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  } else {
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+  }
+  return (uint32_t)w;
+}
+
+// Elements c .. c + 7 of a row of C (zeros behind it).  VEC: rows take 16-byte
+// loads and C is a multiple of 8.
+template <typename T, bool VEC> __device__ __forceinline__ void load8(const T *row, int64_t c, int64_t C, float (&f)[8]) {
+  if constexpr (VEC) {
+    constexpr int V = 16 / (int)sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(V)));
+    if (c < C) {
+#pragma unroll
+      for (int h = 0; h < 8 / V; ++h) {
+        const vec x = *reinterpret_cast<const vec *>(row + c + h * V);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[h * V + v] = (float)x[v];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) f[v] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) f[v] = c + v < C ? (float)row[c + v] : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows: 16 lanes per block of 128, 8 elements each; a workgroup takes 16 rows
+// (so the scales of one block index leave as 64 bytes) and kRowBlocks blocks.
+// ---------------------------------------------------------------------------
+constexpr int kRowBlocks = 8;
+
+template <typename T, bool VEC, bool E4M3>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
+  const int l = threadIdx.x & 15;
+  const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t g = blockIdx.z;
+  if (r >= a.R) return;
+  const int64_t Cp = up128(a.C), nb = Cp / kF8Block;
+  const T *row = (const T *)a.x + (g * a.R + r) * a.ldx;
+  uint8_t *q = (uint8_t *)a.q + (g * a.R + r) * Cp;
+  const int64_t b0 = (int64_t)blockIdx.y * kRowBlocks;
+#pragma unroll 4
+  for (int i = 0; i < kRowBlocks; ++i) {
+    const int64_t b = b0 + i;
+    if (b >= nb) break;
+    const int64_t c = b * kF8Block + l * 8;
+    float f[8];
+    load8<T, VEC>(row, c, a.C, f);
+    float m = 0.f;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) m = fmaxf(m, finite_abs(f[v]));
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
+    const float s = f8_scale(m, E4M3 ? 448.f : 57344.f), inv = 1.f / s;
+    uint2 w;
+    w.x = f8_pack<E4M3>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+    w.y = f8_pack<E4M3>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+    *reinterpret_cast<uint2 *>(q + c) = w;
+    if (l == 0) a.s[(g * nb + b) * a.R + r] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles and columns: a workgroup takes a 128 x 128 tile; thread (rg, cc) =
+// (t / 16, t % 16) holds rows 8 rg .. + 7 and columns 8 cc .. + 7.  The tile's
+// transposed copy goes through LDS (one row of 128 bytes per column, 144 apart
+// so that rows keep 16-byte alignment).
+// ---------------------------------------------------------------------------
+constexpr int kTurnPitch = 144;
+
+// w[i]: the 8 bytes of row 8 rg + i; afterwards o[v]: the 8 bytes of column 8 cc + v
+__device__ __forceinline__ void turn8x8(const uint2 (&w)[8], uint2 (&o)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {      // columns 4 h .. 4 h + 3
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {    // rows 4 u .. 4 u + 3
+      const uint32_t r0 = h ? w[4 * u].y : w[4 * u].x, r1 = h ? w[4 * u + 1].y : w[4 * u + 1].x;
+      const uint32_t r2 = h ? w[4 * u + 2].y : w[4 * u + 2].x, r3 = h ? w[4 * u + 3].y : w[4 * u + 3].x;
+      // v_perm_b32 selects bytes of {first, second}: 0-3 the second's, 4-7 the first's
+      const uint32_t a01 = __builtin_amdgcn_perm(r1, r0, 0x05010400u);  // r0.0 r1.0 r0.1 r1.1
+      const uint32_t b01 = __builtin_amdgcn_perm(r1, r0, 0x07030602u);  // r0.2 r1.2 r0.3 r1.3
+      const uint32_t a23 = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
+      const uint32_t b23 = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
+      const uint32_t c0 = __builtin_amdgcn_perm(a23, a01, 0x05040100u), c1 = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+      const uint32_t c2 = __builtin_amdgcn_perm(b23, b01, 0x05040100u), c3 = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+      if (u == 0) {
+        o[4 * h].x = c0; o[4 * h + 1].x = c1; o[4 * h + 2].x = c2; o[4 * h + 3].x = c3;
+      } else {
+        o[4 * h].y = c0; o[4 * h + 1].y = c1; o[4 * h + 2].y = c2; o[4 * h + 3].y = c3;
+      }
+    }
+  }
+}
+
+// this thread's 8 x 8 bytes into LDS, column by column; then row c of the
+// turned tile goes to dst + c ld for the `cols` columns that there are
+__device__ __forceinline__ void store_turned(const uint2 (&w)[8], unsigned char *lds, uint8_t *dst, int64_t ld, int cols) {
+  const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  uint2 o[8];
+  turn8x8(w, o);
+#pragma unroll
+  for (int v = 0; v < 8; ++v) *reinterpret_cast<uint2 *>(lds + (8 * cc + v) * kTurnPitch + 8 * rg) = o[v];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // 8 lanes per row, 16 bytes each
+    const int c = i * 32 + (threadIdx.x >> 3), part = threadIdx.x & 7;
+    if (c < cols)
+      *reinterpret_cast<uint4 *>(dst + c * ld + 16 * part) = *reinterpret_cast<const uint4 *>(lds + c * kTurnPitch + 16 * part);
+  }
+}
+
+template <typename T, bool VEC, bool E4M3>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) unsigned char lds[128 * kTurnPitch];
+  __shared__ float wmax[4];
+  const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  const int64_t tc = blockIdx.x, tr = blockIdx.y, g = blockIdx.z;
+  const int64_t Cp = up128(a.C), Rp = up128(a.R), nbc = Cp / kF8Block, nbr = Rp / kF8Block;
+  const int64_t r0 = tr * 128 + rg * 8, c = tc * 128 + cc * 8;
+  const T *x = (const T *)a.x + g * a.R * a.ldx;
+  float f[8][8];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + i < a.R) {
+      load8<T, VEC>(x + (r0 + i) * a.ldx, c, a.C, f[i]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) f[i][v] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int v = 0; v < 8; ++v) m = fmaxf(m, finite_abs(f[i][v]));
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  const float s = f8_scale(m, E4M3 ? 448.f : 57344.f), inv = 1.f / s;
+  uint2 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i].x = f8_pack<E4M3>(f[i][0] * inv, f[i][1] * inv, f[i][2] * inv, f[i][3] * inv);
+    w[i].y = f8_pack<E4M3>(f[i][4] * inv, f[i][5] * inv, f[i][6] * inv, f[i][7] * inv);
+    if (r0 + i < a.R) *reinterpret_cast<uint2 *>((uint8_t *)a.q + (g * a.R + r0 + i) * Cp + c) = w[i];
+  }
+  if (threadIdx.x == 0) {
+    a.s[(g * nbc + tc) * nbr + tr] = s;
+    if (a.qt) a.st[(g * nbr + tr) * nbc + tc] = s;
+  }
+  if (a.qt) {
+    const int64_t left = a.C - tc * 128;
+    store_turned(w, lds, (uint8_t *)a.qt + (g * a.C + tc * 128) * Rp + tr * 128, Rp, left < 128 ? (int)left : 128);
+  }
+}
+
+// Columns: workgroup (x, y) takes block x of all experts' blocks of 128 rows
+// and the column tiles y, y + gridDim.y, ...; blocks behind the last expert's
+// are written as zeros with the smallest scale, as an expert's unused places are.
+template <typename T, bool VEC, bool E4M3>
+__global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) unsigned char lds[128 * kTurnPitch];
+  __shared__ float cmax[4][128];
+  __shared__ int sh[8];
+  const Segment seg = find_unit<256>(a.offsets, a.E, (int)a.P, kF8Block, (int)blockIdx.x, sh);
+  const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  const int64_t cap = kF8Block * (int64_t)gridDim.x;
+  const int64_t tiles = (a.C + 127) / 128;
+  const int left = seg.expert < 0 ? 0 : seg.len - seg.unit * kF8Block;  // rows of this block
+  int64_t row[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    row[i] = -1;
+    if (rg * 8 + i < left) {
+      row[i] = seg.begin + seg.unit * kF8Block + rg * 8 + i;
+      if (a.tokens) row[i] = a.tokens[row[i]];
+      if (row[i] >= a.R) row[i] = -1;
+    }
+  }
+  for (int64_t tc = blockIdx.y; tc < tiles; tc += gridDim.y) {
+    const int64_t c = tc * 128 + cc * 8;
+    float f[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (row[i] >= 0) {
+        load8<T, VEC>((const T *)a.x + row[i] * a.ldx, c, a.C, f[i]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) f[i][v] = 0.f;
+      }
+    }
+    float m[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      m[v] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[v] = fmaxf(m[v], finite_abs(f[i][v]));
+      m[v] = fmaxf(m[v], __shfl_xor(m[v], 16, 64));
+      m[v] = fmaxf(m[v], __shfl_xor(m[v], 32, 64));
+    }
+    if ((threadIdx.x & 63) < 16) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) cmax[wave][cc * 8 + v] = m[v];
+    }
+    __syncthreads();  // also: the previous tile's turned rows have left LDS
+    float inv[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int k = cc * 8 + v;
+      const float s = f8_scale(fmaxf(fmaxf(cmax[0][k], cmax[1][k]), fmaxf(cmax[2][k], cmax[3][k])),
+                               E4M3 ? 448.f : 57344.f);
+      inv[v] = 1.f / s;
+      if (rg == 0 && c + v < a.C) a.st[(int64_t)blockIdx.x * a.C + c + v] = s;
+    }
+    uint2 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i].x = f8_pack<E4M3>(f[i][0] * inv[0], f[i][1] * inv[1], f[i][2] * inv[2], f[i][3] * inv[3]);
+      w[i].y = f8_pack<E4M3>(f[i][4] * inv[4], f[i][5] * inv[5], f[i][6] * inv[6], f[i][7] * inv[7]);
+    }
+    const int64_t cols = a.C - tc * 128;
+    store_turned(w, lds, (uint8_t *)a.qt + tc * 128 * cap + (int64_t)blockIdx.x * kF8Block, cap, cols < 128 ? (int)cols : 128);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+// 8 elements of every row take 16-byte loads
+static bool vec8(const QuantArgs &a) {
+  const int64_t per = a.x_dtype == NSG_F32 ? 4 : 8;
+  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % per == 0 && a.C % 8 == 0;
+}
+
+#define NSG_QUANT(KERNEL, grid)                                                                            \
+  do {                                                                                                     \
+    const bool vec = vec8(a), e4 = a.f8 == NSG_F8E4M3;                                                     \
+    switch (a.x_dtype) {                                                                                   \
+      case NSG_F16: NSG_QUANT_T(KERNEL, grid, _Float16); break;                                            \
+      case NSG_BF16: NSG_QUANT_T(KERNEL, grid, __bf16); break;                                             \
+      default: NSG_QUANT_T(KERNEL, grid, float); break;                                                    \
+    }                                                                                                      \
+  } while (0)
+#define NSG_QUANT_T(KERNEL, grid, T)                                                                       \
+  if (vec && e4) hipLaunchKernelGGL((KERNEL<T, true, true>), grid, dim3(256), 0, s, a);                    \
+  else if (vec) hipLaunchKernelGGL((KERNEL<T, true, false>), grid, dim3(256), 0, s, a);                    \
+  else if (e4) hipLaunchKernelGGL((KERNEL<T, false, true>), grid, dim3(256), 0, s, a);                     \
+  else hipLaunchKernelGGL((KERNEL<T, false, false>), grid, dim3(256), 0, s, a)
+
+hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t s) {
+  const int64_t nb = up128(a.C) / kF8Block;
+  const dim3 grid((unsigned)((a.R + 15) / 16), (unsigned)((nb + kRowBlocks - 1) / kRowBlocks), (unsigned)a.B);
+  NSG_QUANT(quantize_rows_kernel, grid);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_tiles(const QuantArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)(up128(a.C) / 128), (unsigned)(up128(a.R) / 128), (unsigned)a.B);
+  NSG_QUANT(quantize_tiles_kernel, grid);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_columns(const QuantArgs &a, hipStream_t s) {
+  const int64_t tiles = (a.C + 127) / 128;
+  const dim3 grid((unsigned)(a.P / kF8Block + a.E), (unsigned)(tiles < 4 ? tiles : 4));
+  NSG_QUANT(quantize_columns_kernel, grid);
+  return hipGetLastError();
+}
+
+}  // namespace nsg
