@@ -591,12 +591,18 @@ class ExpertPlan(NamedTuple):
 
 
 def _launch(device, what: str, fn, *args):
-    """Call a C entry point on `device`, with its current stream as the last argument."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream_handle(device)), what)
+    """Call a C entry point on `device`, with its current stream as the last argument.
+
+    Both lookups are torch's raw ones: the public forms (torch.cuda.current_stream,
+    torch.cuda.device) cost 2 us of a call of 10."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream_handle(device)), what)
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        raise NSGError(code, what)
 
 
 def _gpu(t: torch.Tensor, what: str):
@@ -811,15 +817,16 @@ def quantize_fp8_columns(x: torch.Tensor, offsets: torch.Tensor, rows: Optional[
 
 def _operand(q: torch.Tensor, s: torch.Tensor, name: str, dims: int, device, kinds=("row", "tile")) -> int:
     """Check an operand of quantize_fp8's layout; its block code."""
-    if q.dim() != dims or q.dtype not in _F8 or not q.is_contiguous() or q.device != device:
+    qs, ss = q.shape, s.shape
+    if len(qs) != dims or q.dtype not in _F8 or not q.is_contiguous() or q.device != device:
         raise ValueError(f"{name} must be a contiguous {dims}-D float8_e4m3fn or float8_e5m2 tensor on one device")
-    R, K = q.shape[-2:]
+    R, K = qs[-2], qs[-1]
     if K % FP8_BLOCK:
         raise ValueError(f"{name} needs rows padded to a multiple of {FP8_BLOCK}")
-    if s.dtype != torch.float32 or not s.is_contiguous() or s.device != device or s.dim() != dims or \
-            s.shape[:-1] != (*q.shape[:-2], K // FP8_BLOCK):
+    if s.dtype is not torch.float32 or not s.is_contiguous() or s.device != device or len(ss) != dims or \
+            ss[-2] * FP8_BLOCK != K or (dims == 3 and ss[0] != qs[0]):
         raise ValueError(f"the scales of {name} must be a contiguous float32 tensor [..., K/128, rows or tiles]")
-    n = s.shape[-1]
+    n = ss[-1]
     if "row" in kinds and n == R:
         return 0
     if "tile" in kinds and n == -(-R // FP8_BLOCK):
