@@ -31,6 +31,7 @@
 namespace nsg {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -43,13 +44,23 @@ typedef __attribute__((address_space(3))) unsigned char *lds_u8_t;
 // `lds`: byte address in LDS, the same in every lane; nothing is loaded where `on`
 // is 0.  The branch is inside the assembly so that the main loop stays one basic
 // block, whose instruction order the scheduling barriers keep.
-__device__ __forceinline__ void dma16(const void *src, unsigned lds, int on) {
-  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off\n.Lno%=:"
-               ::"v"(src), "s"(lds), "s"(on) : "memory", "scc");
-}
-__device__ __forceinline__ void dma4(const void *src, unsigned lds, int on) {
-  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off\n.Lno%=:"
-               ::"v"(src), "s"(lds), "s"(on) : "memory", "scc");
+// The source is a 64-bit address in every lane, or a 32-bit offset to a base.
+#define NSG_DMA(WIDTH)                                                                                           \
+  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_" WIDTH       \
+               " %0, off\n.Lno%=:" ::"v"(src), "s"(lds), "s"(on) : "memory", "scc")
+#define NSG_DMA_BASE(WIDTH)                                                                                      \
+  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_" WIDTH       \
+               " %0, %3\n.Lno%=:" ::"v"(off), "s"(lds), "s"(on), "s"(base) : "memory", "scc")
+__device__ __forceinline__ void dma16(const void *src, unsigned lds, int on) { NSG_DMA("dwordx4"); }
+__device__ __forceinline__ void dma16(uint64_t base, unsigned off, unsigned lds, int on) { NSG_DMA_BASE("dwordx4"); }
+__device__ __forceinline__ void dma4(uint64_t base, unsigned off, unsigned lds, int on) { NSG_DMA_BASE("dword"); }
+#undef NSG_DMA
+#undef NSG_DMA_BASE
+// an address that is the same in every lane, in scalar registers
+__device__ __forceinline__ uint64_t uniform(const void *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)(v >> 32)) << 32 |
+         (unsigned)__builtin_amdgcn_readfirstlane((unsigned)v);
 }
 // All but the last N of this wave's loads have landed (all of them where `on` is
 // 0) and its LDS reads have returned; then every other wave's too.
@@ -95,14 +106,13 @@ template <int FA, int FB> __device__ __forceinline__ f32x4 mma(const Frag<FB, tr
   return d;
 }
 
-// 16 consecutive elements of an output row, of which the first `cols` exist
-template <typename T>
-__device__ __forceinline__ void store16(T *dst, const float (&v)[16], int64_t cols, bool vec) {
+// 8 consecutive elements of an output row, of which the first `cols` exist
+template <typename T> __device__ __forceinline__ void store8(T *dst, const float (&v)[8], int64_t cols, bool vec) {
   constexpr int V = 16 / (int)sizeof(T);
   typedef T vec_t __attribute__((ext_vector_type(V)));
-  if (vec && cols >= 16) {
+  if (vec && cols >= 8) {
 #pragma unroll
-    for (int h = 0; h < 16 / V; ++h) {
+    for (int h = 0; h < 8 / V; ++h) {
       vec_t x;
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = (T)v[h * V + i];
@@ -110,14 +120,22 @@ __device__ __forceinline__ void store16(T *dst, const float (&v)[16], int64_t co
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (i < cols) dst[i] = (T)v[i];
   }
 }
-__device__ __forceinline__ void store16(void *out, int dtype, int64_t at, const float (&v)[16], int64_t cols, bool vec) {
-  if (dtype == NSG_BF16) store16((__bf16 *)out + at, v, cols, vec);
-  else if (dtype == NSG_F16) store16((_Float16 *)out + at, v, cols, vec);
-  else store16((float *)out + at, v, cols, vec);
+__device__ __forceinline__ void store8(void *out, int dtype, int64_t at, const float (&v)[8], int64_t cols, bool vec) {
+  if (dtype == NSG_BF16) store8((__bf16 *)out + at, v, cols, vec);
+  else if (dtype == NSG_F16) store8((_Float16 *)out + at, v, cols, vec);
+  else store8((float *)out + at, v, cols, vec);
+}
+
+template <typename T> __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  typedef T vec_t __attribute__((ext_vector_type(8)));
+  vec_t x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
+  return __builtin_bit_cast(u32x4, x);
 }
 
 // 4 consecutive elements, likewise
@@ -234,8 +252,8 @@ __device__ __forceinline__ int64_t row_of_a(const F8GemmArgs &p, int64_t m, bool
 // LDS in stages of one block (128 bytes of each row), in two slots, with their
 // scales, in three.  LDS rows are 128 bytes; chunk c (16 bytes) of row r sits at
 // c ^ ((r >> 1) & 7), so that the 16 rows of a fragment read fall on distinct
-// banks.  Row 16 f + r of 64 LDS rows of B holds n = 16 (r / 4) + 4 f + r % 4 of
-// those 64.
+// banks.  Row 16 f + r of 32 LDS rows of B holds n = 8 (r / 4) + 4 f + r % 4 of
+// those 32.
 //
 // A wave keeps A's fragments of a stage in registers and takes B's one by one
 // (row i of its NF x MF fragments), each read a row ahead.  The multiply-adds of
@@ -251,7 +269,7 @@ __device__ __forceinline__ int64_t row_of_a(const F8GemmArgs &p, int64_t m, bool
 //                  are read under this row's MFMAs
 // with a barrier each, so that every load has about 1.5 stages to land.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WGM, int WGN, int FA, int FB, bool WIDE, bool B_TILE>
+template <int BM, int BN, int WGM, int WGN, int FA, int FB, bool WIDE, bool B_TILE, bool FAR>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8GemmArgs p) {
   constexpr int NW = WGM * WGN, NT = NW * 64;
   constexpr int MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
@@ -268,32 +286,39 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WGN, wn = wave % WGN;
 
-  // direct-load sources; rows outside the output re-read its last row
+  // direct-load sources; rows outside the output re-read its last row.  FAR: as
+  // addresses, else as offsets to a base that moves from stage to stage.
   const uint8_t *srcA[LA], *srcB[LB];
+  unsigned offA[LA], offB[LB];
   bool there = true;
+  const int64_t firstA = p.mode == kExperts ? 0 : w.m0;
 #pragma unroll
   for (int i = 0; i < LA; ++i) {
-    const int r = (wave + NW * i) * 8 + (lane >> 3);
+    const int r = (wave + NW * i) * 8 + (lane >> 3), c = ((lane & 7) ^ ((r >> 1) & 7)) << 4;
     const int64_t row = row_of_a(p, min(w.m0 + r, w.m1 - 1), there);
-    srcA[i] = w.A + row * p.K + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    if (FAR) srcA[i] = w.A + row * p.K + c;
+    else offA[i] = (unsigned)((row - firstA) * p.K + c);
   }
 #pragma unroll
   for (int i = 0; i < LB; ++i) {
-    const int r = (wave + NW * i) * 8 + (lane >> 3);
-    const int n = (r & ~63) + 16 * ((r & 15) >> 2) + 4 * ((r >> 4) & 3) + (r & 3);
-    srcB[i] = w.B + min(w.n0 + n, p.N - 1) * p.K + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    const int r = (wave + NW * i) * 8 + (lane >> 3), c = ((lane & 7) ^ ((r >> 1) & 7)) << 4;
+    const int n = (r & ~31) + 8 * ((r & 15) >> 2) + 4 * ((r >> 4) & 1) + (r & 3);
+    const int64_t row = min(w.n0 + n, p.N - 1);
+    if (FAR) srcB[i] = w.B + row * p.K + c;
+    else offB[i] = (unsigned)((row - w.n0) * p.K + c);
   }
-  const float *srcS;
-  int64_t stepS;
+  uint64_t baseA = uniform(w.A + firstA * p.K), baseB = uniform(w.B + w.n0 * p.K);
+  // the wave's 64 scales of a stage: A's, or B's
+  unsigned offS;
   if (wave < BM / 64) {
     const int64_t row = row_of_a(p, min(w.m0 + wave * 64 + lane, w.m1 - 1), there);
-    srcS = w.sa + (p.a_tile ? row >> 7 : row);
-    stepS = w.ka;
+    offS = (unsigned)(p.a_tile ? row >> 7 : row) * 4;
   } else {
     const int64_t n = min(w.n0 + (wave - BM / 64) * 64 + lane, p.N - 1);
-    srcS = w.sb + (p.b_tile ? n >> 7 : n);
-    stepS = w.kb;
+    offS = (unsigned)(p.b_tile ? n >> 7 : n) * 4;
   }
+  uint64_t baseS = uniform(wave < BM / 64 ? w.sa : w.sb);
+  const uint64_t stepS = uniform(reinterpret_cast<const void *>(4 * (wave < BM / 64 ? w.ka : w.kb)));
   const unsigned lds0 = (unsigned)(size_t)(lds_u8_t)lds;
   // load q of a stage, where `on`, into slot `slot` (scales: `sslot`).  In order:
   // A 0-3, scales 4, the first halves of B's rows 5-6, the second ones 7-8 (a
@@ -302,15 +327,21 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
   auto load = [&](int q, int slot, int sslot, int on) {
     const unsigned at = lds0 + slot * STAGE;
     if (q < 4) {
-      dma16(srcA[q], at + (wave + NW * q) * 1024, on);
-      srcA[q] += kF8Block;
+      const unsigned to = at + (wave + NW * q) * 1024;
+      if (FAR) dma16(srcA[q], to, on);
+      else dma16(baseA, offA[q], to, on);
+      if (FAR) srcA[q] += kF8Block;
+      else if (q == 3) baseA += kF8Block;
     } else if (q == 4) {
-      dma4(srcS, lds0 + 2 * STAGE + sslot * SCALES + wave * 256, on);
-      srcS += stepS;
+      dma4(baseS, offS, lds0 + 2 * STAGE + sslot * SCALES + wave * 256, on);
+      baseS += stepS;
     } else {
       const int i = (q == 5 || q == 7 ? 0 : 2) + (q >= 7 ? 1 : 0);
-      dma16(srcB[i], at + BM * 128 + (wave + NW * i) * 1024, on);
-      srcB[i] += kF8Block;
+      const unsigned to = at + BM * 128 + (wave + NW * i) * 1024;
+      if (FAR) dma16(srcB[i], to, on);
+      else dma16(baseB, offB[i], to, on);
+      if (FAR) srcB[i] += kF8Block;
+      else if (q == 8) baseB += kF8Block;
     }
   };
   auto flag = [](bool v) { return __builtin_amdgcn_readfirstlane(v ? 1 : 0); };
@@ -321,17 +352,19 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
   const int c0 = (g ^ swz) << 4, c1 = ((4 + g) ^ swz) << 4;
   Frag<FA, WIDE> a[MF];
   Frag<FB, WIDE> b[2];
-  f32x4 t[4];             // B's scales of a row of fragments (row scales)
+  f32x4 t[2];             // B's scales of a row of fragments (row scales)
   float s[MF], sn[MF], tile = 1.f;  // A's scales (times B's, for a tile scale); the next stage's
   auto read_a = [&](const unsigned char *st, int j) {
     const unsigned char *row = st + (rA + 16 * j) * 128;
     a[j].set(*reinterpret_cast<const i32x4 *>(row + c0), *reinterpret_cast<const i32x4 *>(row + c1));
   };
-  auto read_b = [&](const unsigned char *st, const unsigned char *sc, int i) {
+  auto read_b = [&](const unsigned char *st, int i) {
     const unsigned char *row = st + BM * 128 + (rB + 16 * i) * 128;
     b[i & 1].set(*reinterpret_cast<const i32x4 *>(row + c0), *reinterpret_cast<const i32x4 *>(row + c1));
-    if (!B_TILE)
-      t[i & 3] = *reinterpret_cast<const f32x4 *>(sc + (BM + wn * NF * 16 + (i >> 2) * 64 + 16 * g + 4 * (i & 3)) * 4);
+  };
+  // (read when the previous row's last multiply-adds, three MFMAs late, are done)
+  auto read_t = [&](const unsigned char *sc, int i) {
+    if (!B_TILE) t[i & 1] = *reinterpret_cast<const f32x4 *>(sc + (BM + wn * NF * 16 + (i >> 1) * 32 + 8 * g + 4 * (i & 1)) * 4);
   };
   auto read_s = [&](const unsigned char *sc) {
     const float *f = reinterpret_cast<const float *>(sc);
@@ -350,12 +383,13 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
   f32x4 d[4];  // block sums in flight: MFMA number q of a stage writes d[q % 4]
 #pragma unroll
   for (int v = 0; v < 4; ++v) d[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < MF; ++j) s[j] = 0.f;
   // multiply-adds of MFMA (i, j) with A's scale x
   auto add = [&](int i, int j, float x) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[j][v], B_TILE ? x : x * t[i & 3][v], acc[i][j][v]);
+    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[j][v], B_TILE ? x : x * t[i & 1][v], acc[i][j][v]);
   };
-  float last[3] = {0.f, 0.f, 0.f};  // A's scales of the previous stage's last three MFMAs
   constexpr int ROW_A = 1, ROW_H = NF / 2 - 1, ROW_Z = NF - 1;
   static_assert(ROW_A <= ROW_H && ROW_H < ROW_Z, "the order of the loads");
   const unsigned char *scales = lds + 2 * STAGE;
@@ -368,9 +402,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
     landed_barrier<11>(two);  // stage 0 but for the second halves
 #pragma unroll
     for (int j = 0; j < MF; ++j) read_a(lds, j);
-    read_b(lds, scales, 0);
+    read_b(lds, 0);
+    read_t(scales, 0);
     read_s(scales);
-    t[3] = f32x4{0.f, 0.f, 0.f, 0.f};
+    t[1] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   int s0 = 0;  // kt % 3
   for (int kt = 0; kt < w.nkb; ++kt) {
@@ -378,8 +413,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
     const unsigned char *st = lds + slot * STAGE, *nst = lds + (slot ^ 1) * STAGE;
     const unsigned char *sc = scales + s0 * SCALES, *nsc = scales + s1 * SCALES;
     const int on1 = flag(kt + 1 < w.nkb), on2 = flag(kt + 2 < w.nkb);
-#pragma unroll
-    for (int j = 0; j < MF; ++j) s[j] = sn[j] * tile;
+    s[0] = sn[0] * tile;  // the others once the previous stage's last multiply-adds are done
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       // the second halves of kt were followed by the 9 loads of kt + 1 and, where
@@ -394,9 +428,9 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
         landed_barrier<9>(on2);
       }
       if (i + 1 < NF) {
-        read_b(st, sc, i + 1);
+        read_b(st, i + 1);
       } else {  // (after the last stage: what is read here is not used)
-        read_b(nst, nsc, 0);
+        read_b(nst, 0);
         read_s(nsc);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -412,33 +446,68 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
           if (after >= 0 && after < 7) load(after, slot, s2, on2);
         }
         if (i == ROW_Z && j < 2) load(7 + j, slot, s2, on2);
-        if (j == 3) add(i, 0, s[0]);
-        else if (i > 0) add(i - 1, j + 1, s[j + 1]);
-        else add(NF - 1, j + 1, last[j]);
+        if (j == 3) {
+          if (i + 1 < NF) read_t(sc, i + 1);
+          else read_t(nsc, 0);
+          add(i, 0, s[0]);
+        } else if (i > 0) {
+          add(i - 1, j + 1, s[j + 1]);
+        } else {
+          add(NF - 1, j + 1, s[j + 1]);
+          s[j + 1] = sn[j + 1] * tile;
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-#pragma unroll
-    for (int j = 0; j < 3; ++j) last[j] = s[j + 1];
     s0 = s1;
   }
 #pragma unroll
-  for (int j = 0; j < 3; ++j) add(NF - 1, j + 1, last[j]);
+  for (int j = 0; j < 3; ++j) add(NF - 1, j + 1, s[j + 1]);
 
   const bool vec = (p.N * (p.out_dtype == NSG_F32 ? 4 : 2)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  if (vec && p.out_dtype != NSG_F32 && w.n0 + BN <= p.N) {
+    // lanes of neighbouring tokens swap halves of 64 n, so that a store fills
+    // whole 128-byte lines: first the even tokens', then the odd ones'
+    const bool odd = r16 & 1;
+    uint16_t *base = (uint16_t *)p.out + w.out + w.n0 + wn * NF * 16 + 8 * g + (odd ? 32 : 0);
 #pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int64_t m = w.m0 + rA + 16 * j;
-    if (m >= w.m1) continue;
-    there = true;
-    if (!w.zero) row_of_a(p, m, there);
+    for (int j = 0; j < MF; ++j) {
+      const int64_t m = w.m0 + rA + 16 * j, me = m - odd, mo = me + 1;
+      bool there = true;
+      if (!w.zero && m < w.m1) row_of_a(p, m, there);
 #pragma unroll
-    for (int i = 0; i < NF; i += 4) {
-      const int64_t n = w.n0 + wn * NF * 16 + i * 16 + 16 * g;
-      float v[16];
+      for (int i = 0; i < NF; i += 4) {
+        u32x4 h[2];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = there ? acc[i + (k >> 2)][j][k & 3] : 0.f;
-      store16(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
+        for (int k = 0; k < 2; ++k) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = there ? acc[i + 2 * k + (e >> 2)][j][e & 3] : 0.f;
+          h[k] = p.out_dtype == NSG_BF16 ? pack8<__bf16>(v) : pack8<_Float16>(v);
+        }
+        u32x4 get;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // from lane ^ 1
+          get[e] = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h[0][e] : h[1][e]), 0xB1, 0xF, 0xF, true);
+        if (me < w.m1) *reinterpret_cast<u32x4 *>(base + me * p.N + i * 16) = odd ? get : h[0];
+        if (mo < w.m1) *reinterpret_cast<u32x4 *>(base + mo * p.N + i * 16) = odd ? h[1] : get;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int64_t m = w.m0 + rA + 16 * j;
+      if (m >= w.m1) continue;
+      bool there = true;
+      if (!w.zero) row_of_a(p, m, there);
+#pragma unroll
+      for (int i = 0; i < NF; i += 2) {
+        const int64_t n = w.n0 + wn * NF * 16 + i * 16 + 8 * g;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = there ? acc[i + (k >> 2)][j][k & 3] : 0.f;
+        store8(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
+      }
     }
   }
 }
@@ -586,9 +655,16 @@ template <typename L> static hipError_t by_type(const F8GemmArgs &a, int64_t gri
 template <int BM, int BN, int WGM, int WGN, bool WIDE> static hipError_t launch_tile(const F8GemmArgs &a, hipStream_t s) {
   constexpr int NT = WGM * WGN * 64;
   const int64_t grid = grid_of<BM, BN>(a);
+  // rows of a tile, or (gathered) of A, within 32-bit offsets
+  const int64_t span = a.mode == kExperts && a.T > BN ? a.T : (BM > BN ? BM : BN);
+  const bool far = span * a.K > 0xFFFFFFFFll;
   return by_type(a, grid, NT, [&](auto fa, auto fb, auto tile) {
-    hipLaunchKernelGGL((gemm_f8_tile_kernel<BM, BN, WGM, WGN, fa(), fb(), WIDE, tile() != 0>), dim3((unsigned)grid), dim3(NT),
-                       0, s, a);
+    if (far)
+      hipLaunchKernelGGL((gemm_f8_tile_kernel<BM, BN, WGM, WGN, fa(), fb(), WIDE, tile() != 0, true>), dim3((unsigned)grid),
+                         dim3(NT), 0, s, a);
+    else
+      hipLaunchKernelGGL((gemm_f8_tile_kernel<BM, BN, WGM, WGN, fa(), fb(), WIDE, tile() != 0, false>), dim3((unsigned)grid),
+                         dim3(NT), 0, s, a);
   });
 }
 
@@ -600,19 +676,28 @@ template <int MF, int NF, int NW, int U, bool WIDE> static hipError_t launch_row
   });
 }
 
+// Which kernel.  The choice never changes a tile's sums (both tile sizes add the
+// blocks in order); the kernel for few rows adds them in another order.
 template <bool WIDE> static hipError_t launch_any(const F8GemmArgs &a, hipStream_t s) {
+  // few rows: 16 x 4096 x 4096 in 6.8 us against the tile kernel's 28, 64 rows in 15 against 23
   if (a.mode == kDense && a.M <= 64) {
     if (a.M <= 16) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
     if (a.M <= 32) return launch_rows<2, 1, 8, 2, WIDE>(a, s);
     return launch_rows<4, 2, 8, 1, WIDE>(a, s);
   }
-  // one token's experts; with more the tile kernel streams the weights faster
-  // (2 x 8 rows of N = 512: 9.5 against 16.7 us, 8 x 8: 30 against 20 us)
+  // one or two tokens' experts: with more of them the tile kernel streams the
+  // weights faster (K = 2048: 2 x 8 rows of N = 512 in 9.5 against 16.7 us, 8 x 8
+  // in 30 against 20)
   if (a.mode == kExperts && a.M * a.N <= 16384) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
+  // 256 x 256 tiles (8-bit instructions only: their registers are full) need most of
+  // the chip's compute units busy, one workgroup each, and mostly full tiles:
+  //   1024 x 11008 x 4096 (172 tiles) in 49 us against 61 with 128 x 128 tiles,
+  //   2048 x 4096 x 4096 (128) in 46 against 40; experts with 256 rows on average
+  //   (2048 x 8 over 64, N = K = 2048) in 120 against 143, with 128 rows in 107 against 92;
+  //   weight gradients of 512 experts of 2048 x 512 in 492 against 613
   if constexpr (!WIDE) {
-    const int64_t tiles = (a.mode == kDense ? a.batch : 1) * (a.M / 256) * ((a.N + 255) / 256);
-    if (a.mode != kWgrad && tiles >= 160 && (a.mode == kDense || a.M >= 192 * a.E))
-      return launch_tile<256, 256, 4, 2, false>(a, s);
+    const int64_t full = (a.M / 256) * (a.N / 256) * (a.mode == kDense ? a.batch : a.mode == kWgrad ? a.E : 1);
+    if (full >= 160 && (a.mode != kExperts || a.M >= 192 * (int64_t)a.E)) return launch_tile<256, 256, 4, 2, false>(a, s);
   }
   return launch_tile<128, 128, 2, 2, WIDE>(a, s);
 }

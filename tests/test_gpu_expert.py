@@ -481,6 +481,12 @@ def test_offsets_past_32_bits():
     out = nsg.expert_gemm_fp8(q, s, b[0][None], b[1][None], off, rows=rows, out_dtype=torch.float32)
     exp = product(ref.values(eq, es), bv)
     check_product(out[[0, 3, 2]], *exp, K=C)
+    many = rows.repeat(100)  # as many rows as take the tile kernel
+    for dt in (torch.float32, torch.bfloat16):
+        tiled = nsg.expert_gemm_fp8(q, s, b[0][None], b[1][None], torch.tensor([0, 400], dtype=torch.int32).cuda(), rows=many,
+                                    out_dtype=dt)
+        check_product(tiled[[396, 399, 398]], *exp, K=C)
+        assert torch.equal(tiled[:4], tiled[396:]) and not tiled[1].any()
     full = nsg.gemm_fp8_nt(q, s, *b, out_dtype=torch.float32)
     check_product(full[-3:], *exp, K=C)
     assert not full[:-3].any()
@@ -490,6 +496,27 @@ def test_offsets_past_32_bits():
     rows_all = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).reshape(T, 1).contiguous()
     back = nsg.expert_combine(x, nsg.ExpertPlan(off, rows_all, rows))
     assert torch.equal(back[:3].cpu(), last.flip(0)) and not back[3:].any()
+
+
+def test_wgrad_of_very_many_rows():
+    """More than 2^24 rows: the rows of a tile are over 2^32 bytes apart."""
+    P = (1 << 24) + 1000
+    o = torch.tensor([0, 300, P - 200, P], dtype=torch.int32).cuda()
+    x = torch.zeros((P, 300), dtype=torch.bfloat16, device="cuda")
+    ends = normal((500, 300), "bf16", 170)
+    x[:300], x[-200:] = ends[:300].cuda(), ends[300:].cuda()
+    x[5000] = 1.0
+    q, s = nsg.quantize_fp8_columns(x, o)
+    del x
+    for dt in (torch.float32, torch.bfloat16):
+        out = nsg.expert_wgrad_fp8(q[:300], s, q[:300], s, o, out_dtype=dt)
+        for e, part in ((0, ends[:300]), (2, ends[300:])):
+            eq, es = ref.quantize_columns(part.float().numpy(), [0, len(part)], "e4m3")
+            v = ref.values(eq[:, :ref.up128(len(part))], es[:ref.up128(len(part)) // 128])
+            check_product(out[e], *product(v, v), K=ref.up128(len(part)))
+        # 1 is 448 times the scale 1 / 448, which is rounded (1 + u), once in each operand; the
+        # scales' product and the multiply-add round once more: (1 + u)^4, which in bf16 is 1
+        assert (out[1].float() - 1).abs().max() <= (5 * U if dt == torch.float32 else 0)
 
 
 def layer(x, ids, w, W, dout, E):
