@@ -412,10 +412,13 @@ nsg_status_t nsg_expert_sort(const void *ids, int32_t id_bits, int64_t T, int64_
                              int32_t *offsets, int32_t *rows, int32_t *tokens,
                              void *workspace, size_t workspace_bytes, void *stream);
 
-/* out[r] = x[tokens[r]] for r < P, zeros where tokens[r] is no row of x.
- * x [T][C] (ldx), out [P][C]; dtype F16, BF16 or F32. */
+/* Bring tokens x [T][C] (ldx) into the sorted order: out[rows[t][j]] = x[t] in
+ * out [P][C], P = T k, and zeros behind offsets[E].  rows and offsets as
+ * nsg_expert_sort gives them (every row below offsets[E] once); dtype F16, BF16 or
+ * F32. */
 nsg_status_t nsg_expert_dispatch(const void *x, int32_t dtype, int64_t T, int64_t C, int64_t ldx,
-                                 const int32_t *tokens, int64_t P, void *out, void *stream);
+                                 const int32_t *offsets, int64_t E, const int32_t *rows, int64_t k,
+                                 void *out, void *stream);
 
 /* out[t] = sum_j weights[t][j] y[rows[t][j]], summed in fp32 in the order of j
  * and rounded once; choices that are no row of y are left out, and a token with

@@ -153,7 +153,7 @@ def lib() -> ctypes.CDLL:
     L.nsg_expert_sort_workspace_size.restype = i32
     L.nsg_expert_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]
     L.nsg_expert_sort.restype = i32
-    L.nsg_expert_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp]
+    L.nsg_expert_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, vp]
     L.nsg_expert_dispatch.restype = i32
     L.nsg_expert_combine.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, vp]
     L.nsg_expert_combine.restype = i32
@@ -685,16 +685,18 @@ def expert_sort_workspace_size(T: int, k: int, num_experts: int) -> int:
 
 
 def expert_dispatch(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
-    """The sorted rows [T k, C] of tokens x [T, C]: row r is x[plan.tokens[r]],
+    """The sorted rows [T k, C] of tokens x [T, C]: x[t] in the rows plan.rows[t],
     zeros behind the last expert's.  Its gradient is expert_combine without weights."""
     device = _gpu(x, "expert_dispatch")
     ld = _matrix(x, "x")
-    _ints(plan.tokens, None, "plan.tokens", device)
-    T, C = x.shape
-    P = plan.tokens.numel()
-    out = torch.empty((P, C), dtype=x.dtype, device=device)
+    T, k = _plan_rows(plan, device)
+    _ints(plan.offsets, None, "plan.offsets", device)
+    C = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, the plan {T} tokens")
+    out = torch.empty((T * k, C), dtype=x.dtype, device=device)
     _launch(device, "nsg_expert_dispatch", lib().nsg_expert_dispatch, x.data_ptr(), _DT[x.dtype], T, C, ld,
-            plan.tokens.data_ptr(), P, out.data_ptr())
+            plan.offsets.data_ptr(), plan.offsets.numel() - 1, plan.rows.data_ptr(), k, out.data_ptr())
     return out
 
 

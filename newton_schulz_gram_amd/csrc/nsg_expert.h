@@ -21,8 +21,8 @@ inline __host__ __device__ int64_t up128(int64_t n) { return (n + kF8Block - 1) 
 int expert_sort_chunks(int64_t P);  // workgroups of the sort; above 1 it needs a table [chunks][E]
 hipError_t launch_expert_sort(const void *ids, int wide, int64_t P, int k, int E, int32_t *offsets, int32_t *rows,
                               int32_t *tokens, int32_t *table, hipStream_t s);
-hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C, int64_t ldx, const int32_t *tokens,
-                                  int64_t P, void *out, hipStream_t s);
+hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C, int64_t ldx, const int32_t *offsets, int E,
+                                  const int32_t *rows, int k, void *out, hipStream_t s);
 hipError_t launch_expert_combine(const void *y, int dtype, int64_t P, int64_t C, int64_t ldy, const int32_t *rows,
                                  int64_t T, int k, const float *w, void *out, hipStream_t s);
 hipError_t launch_expert_combine_backward(const void *dout, int64_t lddo, const void *y, int64_t ldy, int dtype,
@@ -43,6 +43,8 @@ struct QuantArgs {
   const int32_t *offsets = nullptr, *tokens = nullptr;
   int E = 0;
   int64_t P = 0;
+  // by the launchers.  Rows: blocks of a workgroup; columns: all blocks of 128 rows
+  int64_t blocks = 0;
 };
 hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t s);
 hipError_t launch_quantize_tiles(const QuantArgs &a, hipStream_t s);

@@ -4,7 +4,7 @@
 //             offsets[e] = choices of the experts below e; rows[p] = offsets[id]
 //             + earlier choices of the same expert, -1 for an id outside 0 .. E-1;
 //             tokens[rows[p]] = p / k, -1 behind offsets[E].
-//   dispatch  out[r] = x[tokens[r]], 0 where tokens[r] is no row of x
+//   dispatch  out[rows[t, j]] = x[t], 0 behind offsets[E]
 //   combine   out[t] = sum_j w[t, j] y[rows[t, j]] (w = 1 where not given, which
 //             is dispatch's gradient), in fp32, j in order, rounded once
 //   combine's gradient  dy[rows[t, j]] = w[t, j] dout[t],
@@ -28,13 +28,24 @@ namespace nsg {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 static_assert(NSG_MAX_EXPERTS <= kSortThreads, "thread e scans expert e");
-constexpr int kSortMinChunk = 4096;  // choices of one workgroup, at least
+constexpr int kSortKept = 4;         // steps of 64 choices whose experts a wave keeps in registers
+constexpr int kSortChunk = kSortThreads * kSortKept;  // choices of one workgroup, then
 constexpr int kSortMaxChunks = 128;  // every workgroup of the second pass reads the whole table
 
+// Choices of one workgroup, a multiple of 1024: up to kSortChunk choices take one
+// workgroup and one launch; more, about 64 workgroups (4099 x 8 choices of 512
+// experts: 9.0 us, with workgroups of kSortChunk 11.2) until they are of kSortChunk,
+// then workgroups of that until there are kSortMaxChunks, which grow from there on
+// (and read the ids twice).
 static int64_t sort_chunk(int64_t P) {
-  int64_t c = (P + kSortMaxChunks - 1) / kSortMaxChunks;
-  if (c < kSortMinChunk) c = kSortMinChunk;
-  return (c + kSortThreads - 1) / kSortThreads * kSortThreads;
+  int64_t c = P;
+  if (P > kSortChunk) {
+    c = (P + 63) / 64;
+    if (c > kSortChunk) c = kSortChunk;
+    const int64_t least = (P + kSortMaxChunks - 1) / kSortMaxChunks;
+    if (c < least) c = least;
+  }
+  return c == 0 ? kSortThreads : (c + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 int expert_sort_chunks(int64_t P) { return P == 0 ? 1 : (int)((P + sort_chunk(P) - 1) / sort_chunk(P)); }
 
@@ -64,7 +75,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const TI *__
 // expert e in wave w's part of the chunk goes.  A wave takes its part 64 choices
 // at a time: the lanes with the same expert find each other by ballots over the
 // bits of the id, so their order is that of the choices.
-template <typename TI>
+template <typename TI, bool KEPT>
 __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const TI *__restrict__ ids, int64_t P, int64_t chunk,
                                                                     int chunks, int k, int E, int bits,
                                                                     const int32_t *__restrict__ table,
@@ -77,11 +88,25 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const TI *__
   const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min(P, i0 + chunk);
   const int64_t part = chunk / kSortWaves;  // a multiple of 64
   const int64_t w0 = i0 + wave * part, w1 = min(i1, w0 + part);
+  int kept[kSortKept];
+  if (KEPT) {
+#pragma unroll
+    for (int u = 0; u < kSortKept; ++u) {
+      const int64_t p = w0 + u * 64 + lane;
+      kept[u] = p < w1 ? expert_of(ids, p, E) : -1;
+    }
+  }
   for (int i = threadIdx.x; i < kSortWaves * E; i += kSortThreads) at[i] = 0;
   __syncthreads();
-  for (int64_t i = w0 + lane; i < w1; i += 64) {
-    const int e = expert_of(ids, i, E);
-    if (e >= 0) atomicAdd(&at[wave * E + e], 1);
+  if (KEPT) {
+#pragma unroll
+    for (int u = 0; u < kSortKept; ++u)
+      if (kept[u] >= 0) atomicAdd(&at[wave * E + kept[u]], 1);
+  } else {
+    for (int64_t i = w0 + lane; i < w1; i += 64) {
+      const int e = expert_of(ids, i, E);
+      if (e >= 0) atomicAdd(&at[wave * E + e], 1);
+    }
   }
   __syncthreads();
   // thread e: all of expert e's choices, and those before this chunk
@@ -115,9 +140,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const TI *__
   }
   __syncthreads();
   volatile int *mine = at + wave * E;
-  for (int64_t i = w0; i < w1; i += 64) {
-    const int64_t p = i + lane;
-    const int id = p < w1 ? expert_of(ids, p, E) : -1;
+  auto place = [&](int64_t p, int id) {
     uint64_t same = __ballot(id >= 0);
     for (int b = 0; b < bits; ++b) {
       const uint64_t one = __ballot((id >> b) & 1);
@@ -134,6 +157,13 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const TI *__
       rows[p] = -1;
     }
     __builtin_amdgcn_wave_barrier();
+  };
+  if (KEPT) {
+#pragma unroll
+    for (int u = 0; u < kSortKept; ++u)
+      if (w0 + u * 64 < w1) place(w0 + u * 64 + lane, kept[u]);
+  } else {
+    for (int64_t i = w0; i < w1; i += 64) place(i + lane, i + lane < w1 ? expert_of(ids, i + lane, E) : -1);
   }
   for (int64_t p = i0 + threadIdx.x; p < i1; p += kSortThreads)
     if (p >= all) tokens[p] = -1;
@@ -152,8 +182,12 @@ static hipError_t sort_t(const void *ids, int64_t P, int k, int E, int32_t *offs
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(expert_place_kernel<TI>, dim3((unsigned)chunks), dim3(kSortThreads), 0, s, (const TI *)ids, P, chunk, chunks, k, E, bits,
-                     (const int32_t *)table, offsets, rows, tokens);
+  if (chunk <= kSortChunk)
+    hipLaunchKernelGGL((expert_place_kernel<TI, true>), dim3((unsigned)chunks), dim3(kSortThreads), 0, s, (const TI *)ids, P,
+                       chunk, chunks, k, E, bits, (const int32_t *)table, offsets, rows, tokens);
+  else
+    hipLaunchKernelGGL((expert_place_kernel<TI, false>), dim3((unsigned)chunks), dim3(kSortThreads), 0, s, (const TI *)ids, P,
+                       chunk, chunks, k, E, bits, (const int32_t *)table, offsets, rows, tokens);
   return hipGetLastError();
 }
 
@@ -164,45 +198,60 @@ hipError_t launch_expert_sort(const void *ids, int wide, int64_t P, int k, int E
 }
 
 // ---------------------------------------------------------------------------
-// dispatch: one wave per row, 16 bytes a lane.  Elements are moved as they are,
-// so only their size matters.
+// dispatch: one wave per 64 x 16 bytes of a token (part blockIdx.y of 4 tokens),
+// read once and stored to the rows of the token's choices; rows behind the last
+// expert's are cleared by the choices of the same numbers.  Elements are moved as
+// they are, so only their size matters.
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Outputs up to this size (the last-level cache holds 256 MB) stay there for what
+// reads them next; larger ones are streamed past it: 134 MB in 25 us kept and 36
+// streamed, 197 MB in 47 and 54, 268 MB in 78 and 75, 537 MB in 180 and 153.
+constexpr int64_t kDispatchKept = 224 << 20;
 
-template <typename V>
+template <typename V, bool STREAM>
 __global__ void __launch_bounds__(256) expert_dispatch_kernel(const V *__restrict__ x, int64_t T, int64_t n, int64_t ldx,
-                                                              const int32_t *__restrict__ tokens, int64_t P,
+                                                              const int32_t *__restrict__ offsets, int E,
+                                                              const int32_t *__restrict__ rows, int k,
                                                               V *__restrict__ out) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= P) return;
-  const int64_t t = tokens[r];
-  V *dst = out + r * n;
-  if (t < 0 || t >= T) {
-    for (int64_t c = lane; c < n; c += 64) dst[c] = V(0);
-    return;
-  }
-  const V *src = x + t * ldx;
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c = (int64_t)blockIdx.y * 64 + (threadIdx.x & 63);
+  if (t >= T || c >= n) return;
+  const int64_t P = T * k, all = seg_clamp(offsets[E], 0, (int)P);
+  const V v = x[t * ldx + c];
 #pragma unroll 4
-  for (int64_t c = lane; c < n; c += 64) dst[c] = src[c];
+  for (int64_t p = t * k; p < (t + 1) * k; ++p) {
+    const int64_t r = rows[p];
+    if (r >= 0 && r < P) {
+      if (STREAM) __builtin_nontemporal_store(v, out + r * n + c);
+      else out[r * n + c] = v;
+    }
+    if (p >= all) out[p * n + c] = V(0);
+  }
 }
 
 static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C, int64_t ldx, const int32_t *tokens,
-                                  int64_t P, void *out, hipStream_t s) {
-  const dim3 grid((unsigned)((P + 3) / 4));
+template <typename V>
+static hipError_t dispatch_t(const void *x, int64_t T, int64_t n, int64_t ldx, const int32_t *offsets, int E,
+                             const int32_t *rows, int k, void *out, hipStream_t s) {
+  const dim3 grid((unsigned)((T + 3) / 4), (unsigned)((n + 63) / 64));
+  if (T * k * n * (int64_t)sizeof(V) > kDispatchKept)
+    hipLaunchKernelGGL((expert_dispatch_kernel<V, true>), grid, dim3(256), 0, s, (const V *)x, T, n, ldx, offsets, E, rows, k,
+                       (V *)out);
+  else
+    hipLaunchKernelGGL((expert_dispatch_kernel<V, false>), grid, dim3(256), 0, s, (const V *)x, T, n, ldx, offsets, E, rows, k,
+                       (V *)out);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C, int64_t ldx, const int32_t *offsets, int E,
+                                  const int32_t *rows, int k, void *out, hipStream_t s) {
   const int64_t per = 16 / elem;
   if (aligned16(x) && aligned16(out) && C % per == 0 && ldx % per == 0)
-    hipLaunchKernelGGL(expert_dispatch_kernel<u32x4>, grid, dim3(256), 0, s, (const u32x4 *)x, T, C / per, ldx / per,
-                       tokens, P, (u32x4 *)out);
-  else if (elem == 4)
-    hipLaunchKernelGGL(expert_dispatch_kernel<uint32_t>, grid, dim3(256), 0, s, (const uint32_t *)x, T, C, ldx, tokens, P,
-                       (uint32_t *)out);
-  else
-    hipLaunchKernelGGL(expert_dispatch_kernel<uint16_t>, grid, dim3(256), 0, s, (const uint16_t *)x, T, C, ldx, tokens, P,
-                       (uint16_t *)out);
-  return hipGetLastError();
+    return dispatch_t<u32x4>(x, T, C / per, ldx / per, offsets, E, rows, k, out, s);
+  if (elem == 4) return dispatch_t<uint32_t>(x, T, C, ldx, offsets, E, rows, k, out, s);
+  return dispatch_t<uint16_t>(x, T, C, ldx, offsets, E, rows, k, out, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -252,44 +301,45 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const T *__restrict
   Row<T, V>::store(out + t * C + c, acc);
 }
 
-// One wave per token: dout stays in cache over the choices.
+// One wave per choice; a token's choices are neighbours, so dout comes from cache
+// for all but one.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) expert_combine_backward_kernel(
     const T *__restrict__ dout, int64_t lddo, const T *__restrict__ y, int64_t ldy, int64_t P, int64_t C,
-    const int32_t *__restrict__ offsets, int E, const int32_t *__restrict__ rows, int64_t ntok, int k,
-    const float *__restrict__ w, T *__restrict__ dy, float *__restrict__ dw) {
+    const int32_t *__restrict__ offsets, int E, const int32_t *__restrict__ rows, int k, const float *__restrict__ w,
+    T *__restrict__ dy, float *__restrict__ dw) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= ntok) return;
-  const int64_t all = seg_clamp(offsets[E], 0, (int)P);
-  for (int j = 0; j < k; ++j) {
-    const int64_t p = t * k + j;
-    const int64_t r = rows[p];
-    const bool there = r >= 0 && r < P;
+  const int64_t p = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (p >= P) return;
+  const int64_t t = (uint32_t)p / (uint32_t)k;
+  const int64_t r = rows[p];
+  const bool there = r >= 0 && r < P;
+  float dot = 0.f;
+  if (there) {
     const float g = w ? w[p] : 1.f;
-    float dot = 0.f;
-    if (there) {
-      for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) {
-        float d[V], f[V];
-        Row<T, V>::load(dout + t * lddo + c, d);
-        Row<T, V>::load(y + r * ldy + c, f);
+    const T *d = dout + t * lddo, *f = y + r * ldy;
+    T *out = dy + r * C;
+#pragma unroll 4
+    for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) {
+      float u[V], v[V];
+      Row<T, V>::load(d + c, u);
+      Row<T, V>::load(f + c, v);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          dot = fmaf(d[v], f[v], dot);
-          d[v] *= g;
-        }
-        Row<T, V>::store(dy + r * C + c, d);
+      for (int i = 0; i < V; ++i) {
+        dot = fmaf(u[i], v[i], dot);
+        u[i] *= g;
       }
+      Row<T, V>::store(out + c, u);
     }
+  }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
-    if (lane == 0) dw[p] = there ? dot : 0.f;
-    if (p >= all && p < P) {  // a row behind the last expert's
-      float z[V];
+  for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
+  if (lane == 0) dw[p] = there ? dot : 0.f;
+  if (p >= seg_clamp(offsets[E], 0, (int)P)) {  // a row behind the last expert's
+    float z[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[v] = 0.f;
-      for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) Row<T, V>::store(dy + p * C + c, z);
-    }
+    for (int i = 0; i < V; ++i) z[i] = 0.f;
+    for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) Row<T, V>::store(dy + p * C + c, z);
   }
 }
 
@@ -322,16 +372,16 @@ hipError_t launch_expert_combine(const void *y, int dtype, int64_t P, int64_t C,
 
 template <typename T>
 static hipError_t backward_t(const void *dout, int64_t lddo, const void *y, int64_t ldy, int64_t P, int64_t C,
-                             const int32_t *offsets, int E, const int32_t *rows, int64_t ntok, int k, const float *w,
-                             void *dy, float *dw, hipStream_t s) {
+                             const int32_t *offsets, int E, const int32_t *rows, int k, const float *w, void *dy,
+                             float *dw, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
-  const dim3 grid((unsigned)((ntok + 3) / 4));
+  const dim3 grid((unsigned)((P + 3) / 4));
   if (aligned16(dout) && aligned16(y) && aligned16(dy) && C % V == 0 && ldy % V == 0 && lddo % V == 0)
     hipLaunchKernelGGL((expert_combine_backward_kernel<T, V>), grid, dim3(256), 0, s, (const T *)dout, lddo,
-                       (const T *)y, ldy, P, C, offsets, E, rows, ntok, k, w, (T *)dy, dw);
+                       (const T *)y, ldy, P, C, offsets, E, rows, k, w, (T *)dy, dw);
   else
     hipLaunchKernelGGL((expert_combine_backward_kernel<T, 1>), grid, dim3(256), 0, s, (const T *)dout, lddo,
-                       (const T *)y, ldy, P, C, offsets, E, rows, ntok, k, w, (T *)dy, dw);
+                       (const T *)y, ldy, P, C, offsets, E, rows, k, w, (T *)dy, dw);
   return hipGetLastError();
 }
 
@@ -339,9 +389,9 @@ hipError_t launch_expert_combine_backward(const void *dout, int64_t lddo, const 
                                           int64_t P, int64_t C, const int32_t *offsets, int E, const int32_t *rows,
                                           int64_t T, int k, const float *w, void *dy, float *dw, hipStream_t s) {
   switch (dtype) {
-    case NSG_F16: return backward_t<_Float16>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
-    case NSG_BF16: return backward_t<__bf16>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
-    default: return backward_t<float>(dout, lddo, y, ldy, P, C, offsets, E, rows, T, k, w, dy, dw, s);
+    case NSG_F16: return backward_t<_Float16>(dout, lddo, y, ldy, P, C, offsets, E, rows, k, w, dy, dw, s);
+    case NSG_BF16: return backward_t<__bf16>(dout, lddo, y, ldy, P, C, offsets, E, rows, k, w, dy, dw, s);
+    default: return backward_t<float>(dout, lddo, y, ldy, P, C, offsets, E, rows, k, w, dy, dw, s);
   }
 }
 

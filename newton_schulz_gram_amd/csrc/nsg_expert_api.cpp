@@ -66,16 +66,17 @@ nsg_status_t nsg_expert_sort(const void *ids, int32_t id_bits, int64_t T, int64_
                                  reinterpret_cast<int32_t *>(workspace), hs(stream)));
 }
 
-nsg_status_t nsg_expert_dispatch(const void *x, int32_t dtype, int64_t T, int64_t C, int64_t ldx, const int32_t *tokens,
-                                 int64_t P, void *out, void *stream) {
+nsg_status_t nsg_expert_dispatch(const void *x, int32_t dtype, int64_t T, int64_t C, int64_t ldx, const int32_t *offsets,
+                                 int64_t E, const int32_t *rows, int64_t k, void *out, void *stream) {
   if (!float_dtype(dtype)) return NSG_ERR_UNSUPPORTED_DTYPE;
-  const nsg_status_t st = check_rows(T, C, ldx);
+  nsg_status_t st = check_choices(T, k, E);
+  if (st == NSG_OK) st = check_rows(T, C, ldx);
   if (st != NSG_OK) return st;
-  if (P < 0 || P > kMaxRows) return NSG_ERR_SHAPE;
-  if (P == 0 || C == 0) return NSG_OK;
-  if (tokens == nullptr || out == nullptr || (T > 0 && x == nullptr)) return NSG_ERR_INVALID_ARG;
-  if (!rows_aligned(x, dtype) || !rows_aligned(out, dtype) || !aligned(tokens, 4)) return NSG_ERR_INVALID_ARG;
-  return done(launch_expert_dispatch(x, (int)elem_size(dtype), T, C, ldx, tokens, P, out, hs(stream)));
+  if (T == 0 || C == 0) return NSG_OK;
+  if (x == nullptr || offsets == nullptr || rows == nullptr || out == nullptr) return NSG_ERR_INVALID_ARG;
+  if (!rows_aligned(x, dtype) || !rows_aligned(out, dtype) || !aligned(offsets, 4) || !aligned(rows, 4))
+    return NSG_ERR_INVALID_ARG;
+  return done(launch_expert_dispatch(x, (int)elem_size(dtype), T, C, ldx, offsets, (int)E, rows, (int)k, out, hs(stream)));
 }
 
 nsg_status_t nsg_expert_combine(const void *y, int32_t dtype, int64_t P, int64_t C, int64_t ldy, const int32_t *rows,

@@ -36,14 +36,15 @@ def test_sort_workspace_size():
     assert nsg.lib().nsg_expert_sort_workspace_size(1, 1, 1, None) == ARG
 
 
-def dispatch(x=P16, dt=1, T=4, C=8, ld=8, tokens=P16, P=8, out=P16):
-    return nsg.lib().nsg_expert_dispatch(x, dt, T, C, ld, tokens, P, out, None)
+def dispatch(x=P16, dt=1, T=4, C=8, ld=8, offsets=P16, E=3, rows=P16, k=2, out=P16):
+    return nsg.lib().nsg_expert_dispatch(x, dt, T, C, ld, offsets, E, rows, k, out, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=3), DTYPE), (dict(dt=-1), DTYPE), (dict(T=-1), SHAPE), (dict(C=70000, ld=70000), SHAPE), (dict(ld=7), SHAPE),
-    (dict(P=-1), SHAPE), (dict(P=(1 << 26) + 1), SHAPE), (dict(x=None), ARG), (dict(tokens=None), ARG), (dict(out=None), ARG),
-    (dict(x=P16 + 1), ARG), (dict(out=P16 + 1), ARG), (dict(P=0), OK), (dict(C=0, ld=0), OK),
+    (dict(k=0), SHAPE), (dict(T=1 << 26, k=2), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(x=None), ARG),
+    (dict(offsets=None), ARG), (dict(rows=None), ARG), (dict(out=None), ARG), (dict(x=P16 + 1), ARG), (dict(out=P16 + 1), ARG),
+    (dict(rows=P16 + 2), ARG), (dict(T=0), OK), (dict(C=0, ld=0), OK),
 ])
 def test_dispatch_refusals(kw, code):
     assert dispatch(**kw) == code
