@@ -513,6 +513,132 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
 }
 
 // ---------------------------------------------------------------------------
+// Kernel for few tiles: 64 x 64 outputs, four waves of 32 x 32.  With fewer tiles
+// than compute units what counts is how long a tile takes, which in the tile kernel
+// is a load's latency for every stage; here NS - 1 of the NS slots are in flight,
+// and a stage's fragments are read under the MFMAs of the one before.  Layouts as in
+// the tile kernel.
+// ---------------------------------------------------------------------------
+template <int NS, int FA, int FB, bool WIDE, bool B_TILE>
+__global__ void __launch_bounds__(256, 2) gemm_f8_deep_kernel(const F8GemmArgs p) {
+  constexpr int BM = 64, BN = 64, STAGE = (BM + BN) * 128 + (BM + BN) * 4;
+  constexpr int LOADS = 5;  // of a wave and stage: two of each operand, one of scales
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * STAGE];
+  __shared__ int sh[8];
+  Work w;
+  if (!find_work<BM, BN, 256>(p, sh, w)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+
+  unsigned offA[2], offB[2], offS;
+  bool there = true;
+  const int64_t firstA = p.mode == kExperts ? 0 : w.m0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (wave + 4 * i) * 8 + (lane >> 3), c = ((lane & 7) ^ ((r >> 1) & 7)) << 4;
+    const int64_t row = row_of_a(p, min(w.m0 + r, w.m1 - 1), there);
+    offA[i] = (unsigned)((row - firstA) * p.K + c);
+    const int n = (r & ~31) + 8 * ((r & 15) >> 2) + 4 * ((r >> 4) & 1) + (r & 3);
+    offB[i] = (unsigned)((min(w.n0 + n, p.N - 1) - w.n0) * p.K + c);
+  }
+  uint64_t baseA = uniform(w.A + firstA * p.K), baseB = uniform(w.B + w.n0 * p.K);
+  // waves 0 and 2 load A's 64 scales (twice the same), 1 and 3 B's
+  if (wn == 0) {
+    const int64_t row = row_of_a(p, min(w.m0 + lane, w.m1 - 1), there);
+    offS = (unsigned)(p.a_tile ? row >> 7 : row) * 4;
+  } else {
+    const int64_t n = min(w.n0 + lane, p.N - 1);
+    offS = (unsigned)(p.b_tile ? n >> 7 : n) * 4;
+  }
+  uint64_t baseS = uniform(wn == 0 ? w.sa : w.sb);
+  const uint64_t stepS = uniform(reinterpret_cast<const void *>(4 * (wn == 0 ? w.ka : w.kb)));
+  const unsigned lds0 = (unsigned)(size_t)(lds_u8_t)lds;
+  auto load = [&](int slot, bool some) {
+    const int on = __builtin_amdgcn_readfirstlane(some ? 1 : 0);
+    const unsigned at = lds0 + slot * STAGE;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      dma16(baseA, offA[i], at + (wave + 4 * i) * 1024, on);
+      dma16(baseB, offB[i], at + BM * 128 + (wave + 4 * i) * 1024, on);
+    }
+    dma4(baseS, offS, at + (BM + BN) * 128 + wn * 256, on);
+    baseA += kF8Block;
+    baseB += kF8Block;
+    baseS += stepS;
+  };
+
+  const int r16 = lane & 15, g = lane >> 4, swz = (r16 >> 1) & 7;
+  const int c0 = (g ^ swz) << 4, c1 = ((4 + g) ^ swz) << 4;
+  const int rA = wm * 32 + r16, rB = wn * 32 + r16;
+  f32x4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  Frag<FA, WIDE> a[2][2];  // of even and odd stages
+  Frag<FB, WIDE> b[2][2];
+  float s[2][2];
+  f32x4 t[2][2];
+  auto read = [&](int slot, int o) {
+    const unsigned char *st = lds + slot * STAGE;
+    const float *sA = reinterpret_cast<const float *>(st + (BM + BN) * 128), *sB = sA + BM + wn * 32;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const unsigned char *rowA = st + (rA + 16 * j) * 128, *rowB = st + BM * 128 + (rB + 16 * j) * 128;
+      a[o][j].set(*reinterpret_cast<const i32x4 *>(rowA + c0), *reinterpret_cast<const i32x4 *>(rowA + c1));
+      b[o][j].set(*reinterpret_cast<const i32x4 *>(rowB + c0), *reinterpret_cast<const i32x4 *>(rowB + c1));
+      s[o][j] = sA[rA + 16 * j];
+      t[o][j] = B_TILE ? f32x4{sB[0], 0.f, 0.f, 0.f} : *reinterpret_cast<const f32x4 *>(sB + 8 * g + 4 * j);
+    }
+  };
+  int slot = 0;  // kt % NS
+  // stage kt, whose fragments are in registers; the next one's are read
+  auto stage = [&](int kt, int o) {
+    const int next = slot + 1 == NS ? 0 : slot + 1;
+    // stage kt + 1 has landed, and every wave has read stage kt, whose slot is refilled
+    landed_barrier<LOADS *(NS - 2)>(__builtin_amdgcn_readfirstlane(kt + NS - 1 < w.nkb ? 1 : 0));
+    read(next, o ^ 1);  // (after the last stage: not used)
+    load(slot, kt + NS < w.nkb);
+    slot = next;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const f32x4 d = mma<FA, FB>(b[o][i], a[o][j]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[v], s[o][j] * t[o][i][B_TILE ? 0 : v], acc[i][j][v]);
+      }
+  };
+  if (w.nkb > 0) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) load(k, k < w.nkb);
+    landed_barrier<LOADS *(NS - 1)>(__builtin_amdgcn_readfirstlane(NS - 1 < w.nkb ? 1 : 0));
+    read(0, 0);
+  }
+  int kt = 0;
+  for (; kt + 1 < w.nkb; kt += 2) {
+    stage(kt, 0);
+    stage(kt + 1, 1);
+  }
+  if (kt < w.nkb) stage(kt, 0);
+
+  const bool vec = (p.N * (p.out_dtype == NSG_F32 ? 4 : 2)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t m = w.m0 + rA + 16 * j, n = w.n0 + wn * 32 + 8 * g;
+    if (m >= w.m1) continue;
+    there = true;
+    if (!w.zero) row_of_a(p, m, there);
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = there ? acc[k >> 2][j][k & 3] : 0.f;
+    store8(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Kernel for few rows of A: a workgroup takes 16 MF rows of A and 16 NF rows of B,
 // and its NW waves take the blocks of K in turn.  What bounds it is reading B
 // once, so nothing goes through LDS: a wave loads fragments of U blocks straight
@@ -652,12 +778,15 @@ template <typename L> static hipError_t by_type(const F8GemmArgs &a, int64_t gri
   return hipGetLastError();
 }
 
+// rows of a tile of BN (gathered: all rows of A) are within 32-bit offsets of each other
+static bool near_rows(const F8GemmArgs &a, int64_t tile) {
+  return (a.mode == kExperts && a.T > tile ? a.T : tile) * a.K <= 0xFFFFFFFFll;
+}
+
 template <int BM, int BN, int WGM, int WGN, bool WIDE> static hipError_t launch_tile(const F8GemmArgs &a, hipStream_t s) {
   constexpr int NT = WGM * WGN * 64;
   const int64_t grid = grid_of<BM, BN>(a);
-  // rows of a tile, or (gathered) of A, within 32-bit offsets
-  const int64_t span = a.mode == kExperts && a.T > BN ? a.T : (BM > BN ? BM : BN);
-  const bool far = span * a.K > 0xFFFFFFFFll;
+  const bool far = !near_rows(a, BM > BN ? BM : BN);
   return by_type(a, grid, NT, [&](auto fa, auto fb, auto tile) {
     if (far)
       hipLaunchKernelGGL((gemm_f8_tile_kernel<BM, BN, WGM, WGN, fa(), fb(), WIDE, tile() != 0, true>), dim3((unsigned)grid),
@@ -665,6 +794,13 @@ template <int BM, int BN, int WGM, int WGN, bool WIDE> static hipError_t launch_
     else
       hipLaunchKernelGGL((gemm_f8_tile_kernel<BM, BN, WGM, WGN, fa(), fb(), WIDE, tile() != 0, false>), dim3((unsigned)grid),
                          dim3(NT), 0, s, a);
+  });
+}
+
+template <bool WIDE> static hipError_t launch_deep(const F8GemmArgs &a, hipStream_t s) {
+  const int64_t grid = grid_of<64, 64>(a);
+  return by_type(a, grid, 256, [&](auto fa, auto fb, auto tile) {
+    hipLaunchKernelGGL((gemm_f8_deep_kernel<8, fa(), fb(), WIDE, tile() != 0>), dim3((unsigned)grid), dim3(256), 0, s, a);
   });
 }
 
@@ -676,19 +812,23 @@ template <int MF, int NF, int NW, int U, bool WIDE> static hipError_t launch_row
   });
 }
 
-// Which kernel.  The choice never changes a tile's sums (both tile sizes add the
-// blocks in order); the kernel for few rows adds them in another order.
+constexpr int64_t kComputeUnits = 256;  // of an MI355X
+
+// Which kernel.  All but the one for few rows add an output's blocks in the same
+// order, so that their results are the same bit for bit.
 template <bool WIDE> static hipError_t launch_any(const F8GemmArgs &a, hipStream_t s) {
-  // few rows: 16 x 4096 x 4096 in 6.8 us against the tile kernel's 28, 64 rows in 15 against 23
-  if (a.mode == kDense && a.M <= 64) {
+  // few rows: 16 x 4096 x 4096 in 6.7 us against the deep kernel's 15, 32 in 8.5 against 15
+  if (a.mode == kDense && a.M <= 32) {
     if (a.M <= 16) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
-    if (a.M <= 32) return launch_rows<2, 1, 8, 2, WIDE>(a, s);
-    return launch_rows<4, 2, 8, 1, WIDE>(a, s);
+    return launch_rows<2, 1, 8, 2, WIDE>(a, s);
   }
   // one or two tokens' experts: with more of them the tile kernel streams the
   // weights faster (K = 2048: 2 x 8 rows of N = 512 in 9.5 against 16.7 us, 8 x 8
   // in 30 against 20)
   if (a.mode == kExperts && a.M * a.N <= 16384) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
+  // no more 64 x 64 tiles than compute units: 256 x 4096 x 4096 (256 tiles) in 15.6 us
+  // against 22.8 with 128 x 128 tiles, 128 x 11008 x 4096 (344) in 29 against 23
+  if (grid_of<64, 64>(a) <= kComputeUnits && near_rows(a, 64)) return launch_deep<WIDE>(a, s);
   // 256 x 256 tiles (8-bit instructions only: their registers are full) need most of
   // the chip's compute units busy, one workgroup each, and mostly full tiles:
   //   1024 x 11008 x 4096 (172 tiles) in 49 us against 61 with 128 x 128 tiles,

@@ -348,6 +348,19 @@ def test_gemm_batched(M):
         assert torch.equal(out[i], nsg.gemm_fp8_nt(qa[i], sa[i], qb[i], sb[i], out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("how", ["row", "tile"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_gemm_tile_sizes_agree(how, out):
+    """One product alone, among 20 and among 200 runs on tiles of 64, 128 and (16-bit
+    outputs) 256: the same sums in the same order, bit for bit."""
+    (a, av), (b, bv) = operand((300, 640), "e5m2", 75), operand((290, 640), "e4m3", 76, how)
+    one = nsg.gemm_fp8_nt(*a, *b, out_dtype=DT[out])
+    check_product(one, *product(av, bv), K=640)
+    for n in (20, 200):
+        many = nsg.gemm_fp8_nt(*(t.expand(n, *t.shape).contiguous() for t in (*a, *b)), out_dtype=DT[out])
+        assert torch.equal(many, one.expand_as(many))
+
+
 def test_gemm_exact_integers():
     """Small whole numbers with power-of-two scales: every sum is exact, so the
     lane layout of both operands, the block order and the stores are pinned."""
