@@ -43,8 +43,9 @@ struct QuantArgs {
   const int32_t *offsets = nullptr, *tokens = nullptr;
   int E = 0;
   int64_t P = 0;
-  // by the launchers.  Rows: blocks of a workgroup; columns: all blocks of 128 rows
-  int64_t blocks = 0;
+  // by the launchers.  Rows: blocks of a workgroup; columns: all blocks of 128 rows,
+  // and how many workgroups share the column tiles of one
+  int64_t blocks = 0, share = 0;
 };
 hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t s);
 hipError_t launch_quantize_tiles(const QuantArgs &a, hipStream_t s);

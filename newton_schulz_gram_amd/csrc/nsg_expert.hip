@@ -198,24 +198,41 @@ hipError_t launch_expert_sort(const void *ids, int wide, int64_t P, int k, int E
 }
 
 // ---------------------------------------------------------------------------
-// dispatch: one wave per 64 x 16 bytes of a token (part blockIdx.y of 4 tokens),
-// read once and stored to the rows of the token's choices; rows behind the last
+// dispatch: one wave per 64 x 16 bytes of a token (a part; see Parts), read once and stored to the rows of the token's choices; rows behind the last
 // expert's are cleared by the choices of the same numbers.  Elements are moved as
 // they are, so only their size matters.
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Outputs up to this size (the last-level cache holds 256 MB) stay there for what
-// reads them next; larger ones are streamed past it: 134 MB in 25 us kept and 36
-// streamed, 197 MB in 47 and 54, 268 MB in 78 and 75, 537 MB in 180 and 153.
+// reads them next; larger ones are streamed past it: 134 MB in 24 us kept and 26
+// streamed, 197 MB in 39.5 both, 268 MB in 56 and 53, 537 MB in 121 and 104.
 constexpr int64_t kDispatchKept = 224 << 20;
+
+// Four waves of a workgroup take 1 << lp parts of 4 >> lp tokens: a row's parts are
+// read and written together (one token's four parts to a workgroup instead of four
+// tokens' first parts, 16384 x 8 rows of 4 KB: dispatch 153 -> 104 us, combine 155 ->
+// 120, 4.9 and 5.0 TB/s).
+struct Parts {
+  int64_t t, part;
+  __device__ __forceinline__ explicit Parts(int lp) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    t = (int64_t)blockIdx.x * (4 >> lp) + (wave >> lp);
+    part = ((int64_t)blockIdx.y << lp) + (wave & ((1 << lp) - 1));
+  }
+};
+// lp and the grid for T tokens of so many parts (HIP counts a launch's threads in 32 bits)
+static int parts_log(int64_t T, int64_t parts) { return T > (1 << 23) || parts < 2 ? 0 : parts < 4 ? 1 : 2; }
+static dim3 parts_grid(int64_t T, int64_t parts, int lp) {
+  return dim3((unsigned)((T + (4 >> lp) - 1) / (4 >> lp)), (unsigned)((parts + (1 << lp) - 1) >> lp));
+}
 
 template <typename V, bool STREAM>
 __global__ void __launch_bounds__(256) expert_dispatch_kernel(const V *__restrict__ x, int64_t T, int64_t n, int64_t ldx,
                                                               const int32_t *__restrict__ offsets, int E,
                                                               const int32_t *__restrict__ rows, int k,
-                                                              V *__restrict__ out) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = (int64_t)blockIdx.y * 64 + (threadIdx.x & 63);
+                                                              int lp, V *__restrict__ out) {
+  const Parts at(lp);
+  const int64_t t = at.t, c = at.part * 64 + (threadIdx.x & 63);
   if (t >= T || c >= n) return;
   const int64_t P = T * k, all = seg_clamp(offsets[E], 0, (int)P);
   const V v = x[t * ldx + c];
@@ -235,13 +252,15 @@ static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 1
 template <typename V>
 static hipError_t dispatch_t(const void *x, int64_t T, int64_t n, int64_t ldx, const int32_t *offsets, int E,
                              const int32_t *rows, int k, void *out, hipStream_t s) {
-  const dim3 grid((unsigned)((T + 3) / 4), (unsigned)((n + 63) / 64));
+  const int64_t parts = (n + 63) / 64;
+  const int lp = parts_log(T, parts);
+  const dim3 grid = parts_grid(T, parts, lp);
   if (T * k * n * (int64_t)sizeof(V) > kDispatchKept)
     hipLaunchKernelGGL((expert_dispatch_kernel<V, true>), grid, dim3(256), 0, s, (const V *)x, T, n, ldx, offsets, E, rows, k,
-                       (V *)out);
+                       lp, (V *)out);
   else
     hipLaunchKernelGGL((expert_dispatch_kernel<V, false>), grid, dim3(256), 0, s, (const V *)x, T, n, ldx, offsets, E, rows, k,
-                       (V *)out);
+                       lp, (V *)out);
   return hipGetLastError();
 }
 
@@ -277,13 +296,13 @@ template <typename T> struct Row<T, 1> {
   static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = (T)f[0]; }
 };
 
-// One wave per 64 V elements of a token (part blockIdx.y of 4 tokens).
+// One wave per 64 V elements of a token (a part).
 template <typename T, int V>
 __global__ void __launch_bounds__(256) expert_combine_kernel(const T *__restrict__ y, int64_t P, int64_t C, int64_t ldy,
                                                              const int32_t *__restrict__ rows, int64_t ntok, int k,
-                                                             const float *__restrict__ w, T *__restrict__ out) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * V;
+                                                             const float *__restrict__ w, int lp, T *__restrict__ out) {
+  const Parts at(lp);
+  const int64_t t = at.t, c = (at.part * 64 + (threadIdx.x & 63)) * V;
   if (t >= ntok || c >= C) return;
   float acc[V];
 #pragma unroll
@@ -347,8 +366,9 @@ template <typename T, int V>
 static hipError_t combine_v(const void *y, int64_t P, int64_t C, int64_t ldy, const int32_t *rows, int64_t ntok, int k,
                             const float *w, void *out, hipStream_t s) {
   const int64_t parts = (C + 64 * V - 1) / (64 * V);
-  hipLaunchKernelGGL((expert_combine_kernel<T, V>), dim3((unsigned)((ntok + 3) / 4), (unsigned)parts), dim3(256), 0, s,
-                     (const T *)y, P, C, ldy, rows, ntok, k, w, (T *)out);
+  const int lp = parts_log(ntok, parts);
+  hipLaunchKernelGGL((expert_combine_kernel<T, V>), parts_grid(ntok, parts, lp), dim3(256), 0, s, (const T *)y, P, C, ldy,
+                     rows, ntok, k, w, lp, (T *)out);
   return hipGetLastError();
 }
 

@@ -17,7 +17,10 @@
 // 128 columns).  Rows of q are padded with zeros to a multiple of 128; scales
 // are stored block index first, so that a product's tile reads consecutive ones.
 //
-// All three are bound by HBM: x read once, q (1 byte) and s (1/32 byte) written.
+// All three are bound by HBM: x read once, q (1 byte) and s (1/32 byte) written.  Measured
+// (bytes of the definition): rows 16384 x 11008 in 110 us, 5.0 TB/s; tiles with the
+// transposed copy 512 x 2048 x 512 in 403 us, 5.3 TB/s; columns 131072 x 2048 of 512
+// experts in 212 us, 3.8 TB/s (their 128-byte rows of q_t lie cap apart).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -138,13 +141,14 @@ constexpr int kRowBlocks = 8;  // at most
 template <typename T, bool VEC, bool E4M3>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
   const int l = threadIdx.x & 15;
-  const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int64_t g = blockIdx.z;
+  // x: parts of a row, which are read together (16384 x 11008: 110 us, 138 with the
+  // groups of rows first); y and the rest of z: groups of 16 rows
+  const int64_t g = blockIdx.z % a.B, r = (blockIdx.z / a.B * 65535 + blockIdx.y) * 16 + (threadIdx.x >> 4);
   if (r >= a.R) return;
   const int64_t Cp = up128(a.C), nb = Cp / kF8Block;
   const T *row = (const T *)a.x + (g * a.R + r) * a.ldx;
   uint8_t *q = (uint8_t *)a.q + (g * a.R + r) * Cp;
-  const int64_t b0 = (int64_t)blockIdx.y * a.blocks, b1 = b0 + a.blocks < nb ? b0 + a.blocks : nb;
+  const int64_t b0 = (int64_t)blockIdx.x * a.blocks, b1 = b0 + a.blocks < nb ? b0 + a.blocks : nb;
 #pragma unroll 4
   for (int64_t b = b0; b < b1; ++b) {
     const int64_t c = b * kF8Block + l * 8;
@@ -256,8 +260,8 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const QuantArgs a) 
   }
 }
 
-// Columns: workgroup (x, y) takes one of all experts' blocks of 128 rows and the
-// column tiles y, y + gridDim.y, ...; blocks behind the last expert's
+// Columns: a workgroup takes one of all experts' blocks of 128 rows and every
+// a.share-th of its column tiles; blocks behind the last expert's
 // are written as zeros with the smallest scale, as an expert's unused places are.
 template <typename T, bool VEC, bool E4M3>
 __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantArgs a) {
@@ -266,9 +270,10 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantArgs a
   __shared__ typename Eight<T>::reg cmax[4][16][Eight<T>::N];
   __shared__ int sh[8];
   // workgroup b runs on XCD b % 8: each XCD takes consecutive blocks, whose rows of
-  // q_t are neighbours
-  const unsigned per = (blocks + 7) / 8, block = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (block >= blocks) return;
+  // q_t are neighbours, and the workgroups that share a block's rows run together
+  const unsigned share = (unsigned)a.share, q = blockIdx.x >> 3;
+  const unsigned per = (blocks + 7) / 8, block = (blockIdx.x & 7) * per + q / share;
+  if (q / share >= per || block >= blocks) return;
   const Segment seg = find_unit<256>(a.offsets, a.E, (int)a.P, kF8Block, (int)block, sh);
   const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const int64_t cap = kF8Block * (int64_t)blocks;
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const QuantArgs a
       if (row[i] >= a.R) row[i] = -1;
     }
   }
-  for (int64_t tc = blockIdx.y; tc < tiles; tc += gridDim.y) {
+  for (int64_t tc = q % share; tc < tiles; tc += share) {
     const int64_t c = tc * 128 + cc * 8;
     Eight<T> f[8];
 #pragma unroll
@@ -354,10 +359,12 @@ static bool vec8(const QuantArgs &a) {
 hipError_t launch_quantize_rows(const QuantArgs &args, hipStream_t s) {
   QuantArgs a = args;
   const int64_t nb = up128(a.C) / kF8Block, groups = (a.R + 15) / 16 * a.B;
-  // a block each where there are few: 64 x 4096 in 3.2 us against 5.8
+  // a block each where there are few: 64 x 4096 in 2.5 us against 5.8
   a.blocks = groups * nb / 1024;
   a.blocks = a.blocks < 1 ? 1 : a.blocks > kRowBlocks ? kRowBlocks : a.blocks;
-  const dim3 grid((unsigned)((a.R + 15) / 16), (unsigned)((nb + a.blocks - 1) / a.blocks), (unsigned)a.B);
+  const int64_t rows = (a.R + 15) / 16, z = (rows + 65534) / 65535;
+  if (z * a.B > 65535) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)((nb + a.blocks - 1) / a.blocks), (unsigned)(rows < 65535 ? rows : 65535), (unsigned)(z * a.B));
   NSG_QUANT(quantize_rows_kernel, grid);
   return hipGetLastError();
 }
@@ -375,8 +382,10 @@ hipError_t launch_quantize_columns(const QuantArgs &args, hipStream_t s) {
   // 4 workgroups share a block's column tiles, more where there are few blocks: each
   // has to find its expert (1000 rows of 8 experts, C = 1024: 8.3 us with 8, 13 with 4;
   // 131072 rows of 512, C = 2048: 370 us with 16, 311 with 4)
-  const int64_t share = (2048 + a.blocks - 1) / a.blocks, y = share < 4 ? 4 : share;
-  const dim3 grid((unsigned)((a.blocks + 7) / 8 * 8), (unsigned)(tiles < y ? tiles : y));
+  const int64_t y = (2048 + a.blocks - 1) / a.blocks;
+  a.share = y < 4 ? 4 : y;
+  if (a.share > tiles) a.share = tiles;
+  const dim3 grid((unsigned)((a.blocks + 7) / 8 * 8 * a.share));
   NSG_QUANT(quantize_columns_kernel, grid);
   return hipGetLastError();
 }
