@@ -388,8 +388,8 @@ nsg_status_t ns_muon_step(void *W, int32_t w_dtype, void *M, int32_t m_dtype, co
  *     allocated, nothing waits, a bad argument is reported before anything is
  *     enqueued.  Pointers are aligned to their elements, 8-bit data to 16 bytes
  *     (else NSG_ERR_INVALID_ARG).  Outputs must not overlap inputs.
- *   - Results are reproducible bit for bit and do not depend on what else is in
- *     the batch: sums have a fixed order, no atomics on memory.
+ *   - Results are reproducible bit for bit: sums have an order that only the
+ *     sizes fix, there are no atomics on memory.
  *   - Rows are ld elements apart (ld >= their length) where a call has an ld,
  *     packed otherwise.
  *   - Index and offset arrays are device data that the host cannot check: an
@@ -398,7 +398,7 @@ nsg_status_t ns_muon_step(void *W, int32_t w_dtype, void *M, int32_t m_dtype, co
  *   - Limits: E <= NSG_MAX_EXPERTS, at most NSG_MAX_ROWS tokens or sorted rows, other
  *     sides at most NSG_MAX_SIDE; beyond them NSG_ERR_SHAPE. */
 #define NSG_MAX_EXPERTS 1024
-#define NSG_MAX_ROWS (1 << 26)
+#define NSG_MAX_ROWS (1 << 25)
 
 /* Sort the P = T k choices ids[t][j] (device, int32 or int64 by id_bits) by
  * expert, stably.  An id outside 0 .. E-1 is dropped (as by a capacity limit).

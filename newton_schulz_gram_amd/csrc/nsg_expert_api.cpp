@@ -165,7 +165,7 @@ nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R,
 
 static nsg_status_t check_product(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t M, int64_t N, int64_t K) {
   if (!f8_dtype(a_dtype) || !f8_dtype(b_dtype) || !float_dtype(out_dtype)) return NSG_ERR_UNSUPPORTED_DTYPE;
-  if (M < 0 || M > kMaxRows || N < 0 || N > kMaxSide || K < 0 || K > 4 * kMaxRows || K % kF8Block) return NSG_ERR_SHAPE;
+  if (M < 0 || M > kMaxRows || N < 0 || N > kMaxSide || K < 0 || K > 2 * kMaxRows || K % kF8Block) return NSG_ERR_SHAPE;
   return NSG_OK;
 }
 static nsg_status_t check_operands(const void *qa, const float *sa, const void *qb, const float *sb, const void *out,

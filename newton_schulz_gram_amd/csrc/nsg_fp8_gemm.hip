@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
 #pragma unroll
   for (int v = 0; v < 4; ++v) d[v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < MF; ++j) s[j] = 0.f;
+  for (int j = 0; j < MF; ++j) s[j] = 0.f;  // for the multiply-adds that come before any MFMA
+  t[1] = f32x4{0.f, 0.f, 0.f, 0.f};
   // multiply-adds of MFMA (i, j) with A's scale x
   auto add = [&](int i, int j, float x) {
 #pragma unroll
@@ -405,7 +406,6 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
     read_b(lds, 0);
     read_t(scales, 0);
     read_s(scales);
-    t[1] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   int s0 = 0;  // kt % 3
   for (int kt = 0; kt < w.nkb; ++kt) {

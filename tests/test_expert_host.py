@@ -20,7 +20,7 @@ def sort(ids=P16, bits=64, T=4, k=2, E=8, offsets=P16, rows=P16, tokens=P16, ws=
 
 @pytest.mark.parametrize("kw,code", [
     (dict(bits=16), DTYPE), (dict(T=-1), SHAPE), (dict(k=0), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
-    (dict(T=1 << 26, k=2), SHAPE), (dict(k=1 << 40), SHAPE), (dict(ids=None), ARG), (dict(offsets=None), ARG),
+    (dict(T=1 << 25, k=2), SHAPE), (dict(k=1 << 40), SHAPE), (dict(ids=None), ARG), (dict(offsets=None), ARG),
     (dict(rows=None), ARG), (dict(tokens=None), ARG), (dict(ids=P16 + 4), ARG), (dict(rows=P16 + 2), ARG),
     (dict(T=70000), WORKSPACE), (dict(T=70000, ws=P16, n=64), WORKSPACE), (dict(T=70000, ws=P16 + 1, n=1 << 30), WORKSPACE),
 ])
@@ -42,7 +42,7 @@ def dispatch(x=P16, dt=1, T=4, C=8, ld=8, offsets=P16, E=3, rows=P16, k=2, out=P
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=3), DTYPE), (dict(dt=-1), DTYPE), (dict(T=-1), SHAPE), (dict(C=70000, ld=70000), SHAPE), (dict(ld=7), SHAPE),
-    (dict(k=0), SHAPE), (dict(T=1 << 26, k=2), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(x=None), ARG),
+    (dict(k=0), SHAPE), (dict(T=1 << 25, k=2), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(x=None), ARG),
     (dict(offsets=None), ARG), (dict(rows=None), ARG), (dict(out=None), ARG), (dict(x=P16 + 1), ARG), (dict(out=P16 + 1), ARG),
     (dict(rows=P16 + 2), ARG), (dict(T=0), OK), (dict(C=0, ld=0), OK),
 ])
@@ -81,7 +81,7 @@ def quantize(x=P16, dt=1, B=1, R=4, C=8, ld=8, block=0, f8=3, q=P16, s=P16, qt=N
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=3), DTYPE), (dict(f8=1), DTYPE), (dict(f8=5), DTYPE), (dict(block=2), ARG), (dict(B=-1), SHAPE), (dict(B=70000), SHAPE),
-    (dict(R=-1), SHAPE), (dict(ld=7), SHAPE), (dict(R=(1 << 26) + 1), SHAPE), (dict(block=1, R=128 * 65535 + 1), SHAPE),
+    (dict(R=-1), SHAPE), (dict(ld=7), SHAPE), (dict(R=(1 << 25) + 1), SHAPE), (dict(block=1, R=128 * 65535 + 1), SHAPE),
     (dict(qt=P16, st=P16), ARG), (dict(block=1, qt=P16), ARG), (dict(block=1, st=P16), ARG), (dict(x=None), ARG), (dict(q=None), ARG),
     (dict(s=None), ARG), (dict(q=P16 + 8), ARG), (dict(block=1, qt=P16 + 8, st=P16), ARG), (dict(x=P16 + 1), ARG), (dict(B=0), OK),
     (dict(R=0), OK), (dict(C=0, ld=0), OK),
@@ -112,7 +112,7 @@ def gemm(ad=3, bd=3, od=1, batch=1, M=4, N=8, K=128, qa=P16, sa=P16, ab=0, qb=P1
     (dict(M=-1), SHAPE), (dict(N=70000), SHAPE), (dict(batch=-1), SHAPE), (dict(batch=65536), SHAPE), (dict(ab=2), ARG), (dict(bb=-1), ARG),
     (dict(qa=None), ARG), (dict(sa=None), ARG), (dict(qb=None), ARG), (dict(sb=None), ARG), (dict(out=None), ARG), (dict(qa=P16 + 8), ARG),
     (dict(qb=P16 + 8), ARG), (dict(sa=P16 + 2), ARG), (dict(out=P16 + 1), ARG), (dict(M=0), OK), (dict(N=0), OK), (dict(batch=0), OK),
-    (dict(M=1 << 26, N=65536, batch=64), SHAPE),
+    (dict(M=1 << 25, N=65536, batch=64), SHAPE),
 ])
 def test_gemm_refusals(kw, code):
     assert gemm(**kw) == code
