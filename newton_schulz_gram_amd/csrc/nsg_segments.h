@@ -11,6 +11,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include "nsg.h"
+
 namespace nsg {
 
 struct Segment {
@@ -58,38 +60,35 @@ template <int NT> __device__ __forceinline__ int block_before(int v, int *sh, in
 template <int NT>
 __device__ __forceinline__ Segment find_unit(const int32_t *offsets, int E, int P, int unit, int target, int *sh,
                                              bool tail = false) {
+  // a thread's experts, loaded once, all loads together
+  constexpr int kMost = (NSG_MAX_EXPERTS + 1 + NT - 1) / NT;
   const int all = E + (tail ? 1 : 0);
-  const int per = (all + NT - 1) / NT;
-  const int e0 = min((int)threadIdx.x * per, all), e1 = min(e0 + per, all);
-  auto bounds = [&](int e, int &b, int &n) {
-    if (e < E) {
-      seg_bounds(offsets, e, P, b, n);
-    } else {
-      b = seg_clamp(offsets[E], 0, P);
-      n = P;
+  const int per = (all + NT - 1) / NT, e0 = (int)threadIdx.x * per;
+  int begin[kMost], len[kMost], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    begin[i] = len[i] = 0;
+    if (i < per && e0 + i < all) {
+      int end = P;
+      if (e0 + i < E) seg_bounds(offsets, e0 + i, P, begin[i], end);
+      else begin[i] = seg_clamp(offsets[E], 0, P);
+      len[i] = end - begin[i];
     }
-  };
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    int b, n;
-    bounds(e, b, n);
-    mine += (n - b + unit - 1) / unit;
+    mine += (len[i] + unit - 1) / unit;
   }
   int *res = sh + NT / 64;
   if (threadIdx.x == 0) res[0] = -1;
   int total;
   int at = block_before<NT>(mine, sh, total);
   if (target >= at && target < at + mine) {
-    for (int e = e0; e < e1; ++e) {
-      int b, n;
-      bounds(e, b, n);
-      const int u = (n - b + unit - 1) / unit;
-      if (target < at + u) {
-        res[0] = e;
-        res[1] = b;
-        res[2] = n - b;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int u = (len[i] + unit - 1) / unit;
+      if (target >= at && target < at + u) {
+        res[0] = e0 + i;
+        res[1] = begin[i];
+        res[2] = len[i];
         res[3] = target - at;
-        break;
       }
       at += u;
     }
