@@ -380,8 +380,8 @@ hipError_t launch_quantize_columns(const QuantArgs &args, hipStream_t s) {
   a.blocks = a.P / kF8Block + a.E;
   const int64_t tiles = (a.C + 127) / 128;
   // 4 workgroups share a block's column tiles, more where there are few blocks: each
-  // has to find its expert (1000 rows of 8 experts, C = 1024: 8.3 us with 8, 13 with 4;
-  // 131072 rows of 512, C = 2048: 370 us with 16, 311 with 4)
+  // has to find its expert (1000 rows of 8 experts, C = 1024: 6.6 us with 8 (all), 9.6 with 4;
+  // 131072 rows of 512, C = 2048: 248 us with 16, 211 with 4)
   const int64_t y = (2048 + a.blocks - 1) / a.blocks;
   a.share = y < 4 ? 4 : y;
   if (a.share > tiles) a.share = tiles;

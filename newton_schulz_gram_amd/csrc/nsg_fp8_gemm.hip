@@ -827,24 +827,25 @@ constexpr int64_t kComputeUnits = 256;  // of an MI355X
 // Which kernel.  All but the one for few rows add an output's blocks in the same
 // order, so that their results are the same bit for bit.
 template <bool WIDE> static hipError_t launch_any(const F8GemmArgs &a, hipStream_t s) {
-  // few rows: 16 x 4096 x 4096 in 6.7 us against the deep kernel's 15, 32 in 8.5 against 15
-  if (a.mode == kDense && a.M <= 32) {
-    if (a.M <= 16) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
-    return launch_rows<2, 1, 8, 2, WIDE>(a, s);
-  }
-  // one or two tokens' experts: with more of them the tile kernel streams the
-  // weights faster (K = 2048: 2 x 8 rows of N = 512 in 9.5 against 16.7 us, 8 x 8
-  // in 30 against 20)
-  if (a.mode == kExperts && a.M * a.N <= 16384) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
-  // no more 64 x 64 tiles than compute units: 256 x 4096 x 4096 (256 tiles) in 15.6 us
-  // against 22.8 with 128 x 128 tiles, 128 x 11008 x 4096 (344) in 29 against 23
+  // few rows: 16 x 4096 x 4096 in 6.7 us against the deep kernel's 15.1, 32 in 8.5
+  // against 15.3; with more rows of B those of A are read too often: 32 x 8192 x 4096 in
+  // 13.9 against 15.3, 32 x 11008 x 4096 in 19.6 against 15.6
+  if (a.mode == kDense && a.M <= 16) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
+  if (a.mode == kDense && a.M <= 32 && a.batch * a.N <= 8192) return launch_rows<2, 1, 8, 2, WIDE>(a, s);
+  // one or two tokens' experts (K = 2048, N = 512): 1 x 8 rows in 6.2 us against the deep
+  // kernel's 10.9, 2 x 8 in 9.5 against 11.6, 4 x 8 in 16.5 against 12.4
+  if (a.mode == kExperts && a.M * a.N <= 8192) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
+  // no more 64 x 64 tiles than compute units: 256 x 4096 x 4096 (256 tiles) in 15.8 us
+  // against 23.0 with 128 x 128 tiles, 128 x 11008 x 4096 (344) in 29.5 against 23.2;
+  // weight gradients of 256 x 256 over 4096 rows (128 workgroups) in 16.4 against 28.6,
+  // two of 512 x 512 over 300 rows (512) in 9.1 against 6.3
   if (grid_of<64, 64>(a) <= kComputeUnits && near_rows(a, 64)) return launch_deep<WIDE>(a, s);
   // 256 x 256 tiles (8-bit instructions only: their registers are full) need most of
   // the chip's compute units busy, one workgroup each, and mostly full tiles:
-  //   1024 x 11008 x 4096 (172 tiles) in 49 us against 61 with 128 x 128 tiles,
-  //   2048 x 4096 x 4096 (128) in 46 against 40; experts with 256 rows on average
-  //   (2048 x 8 over 64, N = K = 2048) in 120 against 143, with 128 rows in 107 against 92;
-  //   weight gradients of 512 experts of 2048 x 512 in 492 against 613
+  //   1024 x 11008 x 4096 (172 tiles) in 48 us against 53 with 128 x 128 tiles,
+  //   2048 x 4096 x 4096 (128) in 47 against 36; experts with 256 rows on average
+  //   (2048 x 8 over 64, N = K = 2048) in 116 against 128, with 128 rows in 97 against 84;
+  //   weight gradients of 512 experts of 2048 x 512 in 458 against 611
   if constexpr (!WIDE) {
     const int64_t full = (a.M / 256) * (a.N / 256) * (a.mode == kDense ? a.batch : a.mode == kWgrad ? a.E : 1);
     if (full >= 160 && (a.mode != kExperts || a.M >= 192 * (int64_t)a.E)) return launch_tile<256, 256, 4, 2, false>(a, s);
