@@ -900,11 +900,11 @@ def expert_wgrad_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: t
     _ints(offsets, None, "offsets", device)
     E = offsets.numel() - 1
     (N, cap), K = qa.shape, qb.shape[0]
-    P = cap - FP8_BLOCK * E  # any number of rows from here on to P + 127 has this layout
+    P = cap - FP8_BLOCK * E  # P .. P + 127 rows have this layout, at most NSG_MAX_ROWS
     if qb.shape[1] != cap or P < 0:
         raise ValueError(f"operands {tuple(qa.shape)} and {tuple(qb.shape)} do not fit {E} experts")
     out = _product_out(out, (E, N, K), out_dtype, device)
     _launch(device, "nsg_expert_wgrad_fp8", lib().nsg_expert_wgrad_fp8, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype],
-            P + FP8_BLOCK - 1, E, N, K, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), offsets.data_ptr(),
+            max(P, min(P + FP8_BLOCK - 1, 1 << 25)), E, N, K, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), offsets.data_ptr(),
             out.data_ptr())
     return out

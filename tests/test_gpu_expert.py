@@ -642,3 +642,153 @@ def test_layer_graph_replay(T, E):
         torch.cuda.synchronize()
         for p, q in zip(got, layer(*fresh[i % 3], E)):
             assert torch.equal(p, q), i
+
+
+# ---------------------------------------------------------------------------
+# calls that the documentation allows and that a program may make
+# ---------------------------------------------------------------------------
+def test_two_layers_at_once():
+    """Two layers on two streams that run at the same time, each as alone."""
+    jobs = [layer_inputs(900, 4, 16, 256, 256, 210), layer_inputs(60, 8, 16, 256, 512, 220)]
+    exp = [layer(*a, 16) for a in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(layer(*jobs[i], 16))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            for p, q in zip(outs, exp[i]):
+                assert torch.equal(p, q)
+
+
+def test_two_graphs_share_a_sort_workspace():
+    """The sort's workspace holds nothing between calls: two graphs replayed in turn
+    on one stream use one."""
+    T, k, E = 5000, 4, 100
+    ws = torch.empty(nsg.expert_sort_workspace_size(T, k, E), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    ids = [torch.from_numpy(choices(T, k, E, seed=230 + i)).cuda() for i in range(2)]
+    graphs, plans = [], []
+    for i in range(2):
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            plans.append(nsg.expert_sort(ids[i], E, workspace=ws))
+    for n in range(4):
+        ws.fill_(0xFF)
+        for i in range(2):
+            ids[i].copy_(torch.from_numpy(choices(T, k, E, seed=240 + 2 * n + i)))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for got, e in zip(plans[i], ref.expert_sort(ids[i].cpu().numpy(), E)):
+                assert np.array_equal(got.cpu().numpy(), e)
+
+
+def test_one_expert_many_times_in_a_token():
+    """The same expert in every choice of a token: each choice has its own row and
+    counts on its own, in the sum and in the gradients."""
+    T, k, C = 40, 6, 72
+    ids = np.repeat(np.arange(T)[:, None] % 3, k, 1)
+    p = plan_of(ids, 3)
+    x, w = normal((T, C), "f32", 250).cuda(), normal((T, k), "f32", 251).cuda()
+    y = nsg.expert_dispatch(x, p)
+    got = f64(nsg.expert_combine(y, p, w))
+    exp = f64(w).sum(1)[:, None] * f64(x)
+    size = np.abs(f64(w)).sum(1)[:, None] * np.abs(f64(x))
+    assert np.all(np.abs(got - exp) <= (2 * k + 1) * U * size)
+    dy, dw = nsg.expert_combine_backward(x, y, p, w)
+    s = (f64(x) ** 2).sum(1)[:, None]
+    assert np.all(np.abs(f64(dw) - s) <= 2 * C * U * s)
+    for j in range(k):
+        assert torch.equal(dy[p.rows[:, j].long()], w[:, j:j + 1] * x)
+
+
+# 10 x 16 tiles of 256 x 256, of which one kernel needs 160, and 128 x 128 tiles
+@pytest.mark.parametrize("M,N", [(2600, 4100), (1000, 4100)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_large_gemm_nan_stays_in_its_row_and_column(M, N, out):
+    x, w = normal((M, 200), "bf16", 260).cuda(), normal((N, 200), "bf16", 261).cuda()
+    clean = nsg.gemm_fp8_nt(*nsg.quantize_fp8(x), *nsg.quantize_fp8(w), out_dtype=DT[out])
+    x[M - 1, 199] = float("nan")
+    w[N - 1, 3] = float("inf")
+    got = nsg.gemm_fp8_nt(*nsg.quantize_fp8(x), *nsg.quantize_fp8(w), out_dtype=DT[out])
+    assert got[M - 1].isnan().all() and not got[:, N - 1].isfinite().any()
+    assert clean.isfinite().all() and torch.equal(got[:M - 1, :N - 1], clean[:M - 1, :N - 1])
+
+
+def test_wgrad_of_the_most_rows():
+    """2^25 rows of one column, all 1.  An operand's block is 448 times its scale, which
+    is rounded (1 + u); a block's 128 equal products are summed exactly, and its
+    multiply-add rounds once: 2^18 blocks in order, (2^18 + 4) u of 2^25 in all."""
+    P = 1 << 25
+    x = torch.ones((P, 1), dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    q = nsg.quantize_fp8_columns(x, o)
+    out = nsg.expert_wgrad_fp8(*q, *q, o, out_dtype=torch.float32)
+    assert abs(out.item() - P) <= ((1 << 18) + 4) * U * P
+
+
+# ---------------------------------------------------------------------------
+# refusals of GPU tensors: checked on the host, before any launch
+# ---------------------------------------------------------------------------
+def test_refusals():
+    T, k, E, C = 10, 2, 4, 256
+    p = plan_of(choices(T, k, E, seed=270), E)
+    x, y = torch.zeros((T, C), device="cuda"), torch.zeros((T * k, C), device="cuda")
+    w = torch.zeros((T, k), device="cuda")
+    q, s = nsg.quantize_fp8(x)
+    W = torch.zeros((E, 64, C), device="cuda")
+    wq, ws = nsg.quantize_fp8(W, block="tile")
+    c = nsg.quantize_fp8_columns(y, p.offsets)
+    wide = torch.zeros((T, k, 2), dtype=torch.int64, device="cuda")
+    shifted = torch.zeros(T * C + 16, dtype=torch.uint8, device="cuda")[1:T * C + 1].view(torch.float8_e4m3fn).view(T, C)
+    one = torch.zeros((1, C), device="cuda")
+    cases = [
+        lambda: nsg.expert_sort(wide[..., 0], E),                                  # strided ids
+        lambda: nsg.expert_sort(w, E),                                             # ids of floats
+        lambda: nsg.expert_sort(wide[..., 0].contiguous(), 0),
+        lambda: nsg.expert_sort(wide[..., 0].contiguous(), 1025),
+        lambda: nsg.expert_dispatch(one.expand(T, C), p),                          # rows that overlap
+        lambda: nsg.expert_dispatch(x.t(), p),
+        lambda: nsg.expert_dispatch(y, p),                                         # not the plan's tokens
+        lambda: nsg.expert_dispatch(x.double(), p),
+        lambda: nsg.expert_dispatch(x, p._replace(offsets=p.offsets.cpu())),
+        lambda: nsg.expert_dispatch(x, p._replace(rows=p.rows.long())),
+        lambda: nsg.expert_dispatch(x, p._replace(offsets=p.offsets[:0])),
+        lambda: nsg.expert_combine(x, p, w),
+        lambda: nsg.expert_combine(y, p, w.bfloat16()),
+        lambda: nsg.expert_combine(y, p, w.t().contiguous().t()),
+        lambda: nsg.expert_combine(y, p, w[:, :1].contiguous()),
+        lambda: nsg.expert_combine_backward(x.bfloat16(), y, p, w),                # two dtypes
+        lambda: nsg.expert_combine_backward(x[:, :8], y, p, w),
+        lambda: nsg.quantize_fp8(x, block="column"),
+        lambda: nsg.quantize_fp8(x, transposed=True),
+        lambda: nsg.quantize_fp8(x, dtype=torch.bfloat16),
+        lambda: nsg.quantize_fp8(W[:, ::2].transpose(0, 1)),                       # batches not behind each other
+        lambda: nsg.quantize_fp8_columns(y, p.offsets.long()),
+        lambda: nsg.quantize_fp8_columns(y, p.offsets, rows=p.tokens.cpu()),
+        lambda: nsg.gemm_fp8_nt(q, s, wq[0], ws),                                  # scales of the batch
+        lambda: nsg.gemm_fp8_nt(q, s, wq, ws),
+        lambda: nsg.gemm_fp8_nt(q, s.t(), wq[0], ws[0]),
+        lambda: nsg.gemm_fp8_nt(q, s.bfloat16(), wq[0], ws[0]),
+        lambda: nsg.gemm_fp8_nt(q[:, :128], s[:1], wq[0], ws[0]),                  # a slice of its rows
+        lambda: nsg.gemm_fp8_nt(q[:, :128].contiguous(), s[:1], wq[0], ws[0]),     # another K
+        lambda: nsg.gemm_fp8_nt(shifted, s, wq[0], ws[0]),                         # not at 16 bytes
+        lambda: nsg.gemm_fp8_nt(q, s, wq[0], ws[0], out_dtype=torch.float64),
+        lambda: nsg.gemm_fp8_nt(q, s, wq[0], ws[0], out=torch.zeros((64, T), device="cuda")),
+        lambda: nsg.expert_gemm_fp8(*nsg.quantize_fp8(torch.zeros((300, C), device="cuda"), block="tile"), wq, ws, p.offsets),
+        lambda: nsg.expert_gemm_fp8(q, s, wq, ws, p.offsets[:-1], rows=p.tokens),
+        lambda: nsg.expert_gemm_fp8(q, s, wq, ws, p.offsets, rows=p.tokens.long()),
+        lambda: nsg.expert_wgrad_fp8(*c, *nsg.quantize_fp8_columns(torch.zeros((300, C), device="cuda"), p.offsets), p.offsets),
+        lambda: nsg.expert_wgrad_fp8(q, s, q, s, p.offsets),                       # fewer columns than 128 E
+    ]
+    for i, call in enumerate(cases):
+        with pytest.raises((ValueError, TypeError, nsg.NSGError)):
+            call()
+            pytest.fail(f"case {i} was not refused")
+    torch.cuda.synchronize()
