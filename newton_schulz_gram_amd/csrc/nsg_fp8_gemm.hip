@@ -45,12 +45,14 @@ typedef __attribute__((address_space(3))) unsigned char *lds_u8_t;
 // is 0.  The branch is inside the assembly so that the main loop stays one basic
 // block, whose instruction order the scheduling barriers keep.
 // The source is a 64-bit address in every lane, or a 32-bit offset to a base.
+// The two instructions between the write of m0 and the load are the wait state that
+// an LDS load needs there; the compiler adds none inside assembly.
 #define NSG_DMA(WIDTH)                                                                                           \
-  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_" WIDTH       \
-               " %0, off\n.Lno%=:" ::"v"(src), "s"(lds), "s"(on) : "memory", "scc")
+  asm volatile("s_mov_b32 m0, %1\n\ts_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\tglobal_load_lds_" WIDTH       \
+               " %0, off\n.Lno%=:" ::"v"(src), "s"(lds), "s"(on) : "memory", "scc", "m0")
 #define NSG_DMA_BASE(WIDTH)                                                                                      \
-  asm volatile("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_" WIDTH       \
-               " %0, %3\n.Lno%=:" ::"v"(off), "s"(lds), "s"(on), "s"(base) : "memory", "scc")
+  asm volatile("s_mov_b32 m0, %1\n\ts_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lno%=\n\tglobal_load_lds_" WIDTH       \
+               " %0, %3\n.Lno%=:" ::"v"(off), "s"(lds), "s"(on), "s"(base) : "memory", "scc", "m0")
 __device__ __forceinline__ void dma16(const void *src, unsigned lds, int on) { NSG_DMA("dwordx4"); }
 __device__ __forceinline__ void dma16(uint64_t base, unsigned off, unsigned lds, int on) { NSG_DMA_BASE("dwordx4"); }
 __device__ __forceinline__ void dma4(uint64_t base, unsigned off, unsigned lds, int on) { NSG_DMA_BASE("dword"); }
