@@ -409,60 +409,81 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
     read_t(scales, 0);
     read_s(scales);
   }
-  int s0 = 0;  // kt % 3
-  for (int kt = 0; kt < w.nkb; ++kt) {
-    const int slot = kt & 1, s1 = s0 == 2 ? 0 : s0 + 1, s2 = s1 == 2 ? 0 : s1 + 1;
-    const unsigned char *st = lds + slot * STAGE, *nst = lds + (slot ^ 1) * STAGE;
-    const unsigned char *sc = scales + s0 * SCALES, *nsc = scales + s1 * SCALES;
-    const int on1 = flag(kt + 1 < w.nkb), on2 = flag(kt + 2 < w.nkb);
-    s[0] = sn[0] * tile;  // the others once the previous stage's last multiply-adds are done
+  // the stages of a wave: IDLE where none of its rows or columns is in the output, which
+  // then loads and waits like the others and leaves the matrix cores to them
+  auto stages = [&](auto idle) {
+    constexpr bool IDLE = decltype(idle)::value;
+    int s0 = 0;  // kt % 3
+    for (int kt = 0; kt < w.nkb; ++kt) {
+      const int slot = kt & 1, s1 = s0 == 2 ? 0 : s0 + 1, s2 = s1 == 2 ? 0 : s1 + 1;
+      const unsigned char *st = lds + slot * STAGE, *nst = lds + (slot ^ 1) * STAGE;
+      const unsigned char *sc = scales + s0 * SCALES, *nsc = scales + s1 * SCALES;
+      const int on1 = flag(kt + 1 < w.nkb), on2 = flag(kt + 2 < w.nkb);
+      if (!IDLE) s[0] = sn[0] * tile;  // the others once the previous stage's last multiply-adds are done
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      // the second halves of kt were followed by the 9 loads of kt + 1 and, where
-      // A's row is an earlier one, 5 of kt + 2; those of kt + 1 up to its first
-      // halves by 2 of its own and 7 of kt + 2
-      if (i == ROW_H) {
-        if (ROW_A < ROW_H) landed_barrier<14>(on2);
-        else landed_barrier<9>(on1);
-      } else if (i == ROW_A) {
-        read_barrier();
-      } else if (i == ROW_Z) {
-        landed_barrier<9>(on2);
-      }
-      if (i + 1 < NF) {
-        read_b(st, i + 1);
-      } else {  // (after the last stage: what is read here is not used)
-        read_b(nst, 0);
-        read_s(nsc);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < MF; ++j) {
-        d[j] = mma<FA, FB>(b[i & 1], a[j]);
-        if (i + 1 == NF) read_a(nst, j);
-        const int after = (i - ROW_A) * MF + j;  // MFMAs since A's row
-        if (ROW_A < ROW_H) {
-          if (after >= 0 && after < 5) load(after, slot, s2, on2);
-          if (i == ROW_H && j < 2) load(5 + j, slot, s2, on2);
-        } else {
-          if (after >= 0 && after < 7) load(after, slot, s2, on2);
+      for (int i = 0; i < NF; ++i) {
+        // the second halves of kt were followed by the 9 loads of kt + 1 and, where
+        // A's row is an earlier one, 5 of kt + 2; those of kt + 1 up to its first
+        // halves by 2 of its own and 7 of kt + 2
+        if (i == ROW_H) {
+          if (ROW_A < ROW_H) landed_barrier<14>(on2);
+          else landed_barrier<9>(on1);
+        } else if (i == ROW_A) {
+          read_barrier();
+        } else if (i == ROW_Z) {
+          landed_barrier<9>(on2);
         }
-        if (i == ROW_Z && j < 2) load(7 + j, slot, s2, on2);
-        if (j == 3) {
-          if (i + 1 < NF) read_t(sc, i + 1);
-          else read_t(nsc, 0);
-          add(i, 0, s[0]);
-        } else if (i > 0) {
-          add(i - 1, j + 1, s[j + 1]);
-        } else {
-          add(NF - 1, j + 1, s[j + 1]);
-          s[j + 1] = sn[j + 1] * tile;
+        if (!IDLE) {
+          if (i + 1 < NF) {
+            read_b(st, i + 1);
+          } else {  // (after the last stage: what is read here is not used)
+            read_b(nst, 0);
+            read_s(nsc);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+          if (!IDLE) {
+            d[j] = mma<FA, FB>(b[i & 1], a[j]);
+            if (i + 1 == NF) read_a(nst, j);
+          }
+          const int after = (i - ROW_A) * MF + j;  // MFMAs since A's row
+          if (ROW_A < ROW_H) {
+            if (after >= 0 && after < 5) load(after, slot, s2, on2);
+            if (i == ROW_H && j < 2) load(5 + j, slot, s2, on2);
+          } else {
+            if (after >= 0 && after < 7) load(after, slot, s2, on2);
+          }
+          if (i == ROW_Z && j < 2) load(7 + j, slot, s2, on2);
+          if (!IDLE) {
+            if (j == 3) {
+              if (i + 1 < NF) read_t(sc, i + 1);
+              else read_t(nsc, 0);
+              add(i, 0, s[0]);
+            } else if (i > 0) {
+              add(i - 1, j + 1, s[j + 1]);
+            } else {
+              add(NF - 1, j + 1, s[j + 1]);
+              s[j + 1] = sn[j + 1] * tile;
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+      s0 = s1;
     }
-    s0 = s1;
+  };
+  // only with tile scales of B (weights by expert: 16384 x 8 rows over 512 experts 238 ->
+  // 223 us, 2048 x 8 over 64 115 -> 107): with row scales, which weight gradients have,
+  // whose tiles are mostly full, the second loop cost 456 -> 467
+  if constexpr (B_TILE) {
+    if (flag(w.m0 + wm * MF * 16 >= w.m1 || w.n0 + wn * NF * 16 >= p.N)) {
+      stages(std::true_type{});
+      return;
+    }
   }
+  stages(std::false_type{});
 #pragma unroll
   for (int j = 0; j < 3; ++j) add(NF - 1, j + 1, s[j + 1]);
 
@@ -845,12 +866,14 @@ template <bool WIDE> static hipError_t launch_any(const F8GemmArgs &a, hipStream
   // 256 x 256 tiles (8-bit instructions only: their registers are full) need most of
   // the chip's compute units busy, one workgroup each, and mostly full tiles:
   //   1024 x 11008 x 4096 (172 tiles) in 48 us against 53 with 128 x 128 tiles,
-  //   2048 x 4096 x 4096 (128) in 47 against 36; experts with 256 rows on average
-  //   (2048 x 8 over 64, N = K = 2048) in 116 against 128, with 128 rows in 97 against 84;
-  //   weight gradients of 512 experts of 2048 x 512 in 458 against 611
+  //   2048 x 4096 x 4096 (128) in 47 against 36; experts with tile scales, whose empty
+  //   parts of a tile cost least, with 128 rows on average (8192 x 8 over 512, N = 512,
+  //   K = 2048) in 155 against 168, with 64 (512 x 8 over 64, N = K = 2048) in 66 against
+  //   67; with row scales and 256 rows (2048 x 8 over 64) in 116 against 128, with 128
+  //   in 97 against 84; weight gradients of 512 experts of 2048 x 512 in 458 against 611
   if constexpr (!WIDE) {
     const int64_t full = (a.M / 256) * (a.N / 256) * (a.mode == kDense ? a.batch : a.mode == kWgrad ? a.E : 1);
-    if (full >= 160 && (a.mode != kExperts || a.M >= 192 * (int64_t)a.E)) return launch_tile<256, 256, 4, 2, false>(a, s);
+    if (full >= 160 && (a.mode != kExperts || a.M >= (a.b_tile ? 96 : 192) * (int64_t)a.E)) return launch_tile<256, 256, 4, 2, false>(a, s);
   }
   return launch_tile<128, 128, 2, 2, WIDE>(a, s);
 }

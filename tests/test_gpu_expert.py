@@ -792,3 +792,31 @@ def test_refusals():
             call()
             pytest.fail(f"case {i} was not refused")
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("how", ["row", "tile"])
+def test_partly_filled_large_tiles(how):
+    """256 x 256 tiles of which an expert's rows, or the last rows and columns of a
+    matrix, fill a part: the same bits as each expert's product alone, which takes
+    smaller tiles and adds in the same order (above 32 rows; fewer go to the kernel that
+    splits K)."""
+    E, K, N, P = 40, 264, 1100, 10300
+    g = np.random.default_rng(280)
+    cuts = np.sort(g.integers(0, P - 77, size=E - 1))
+    o = np.concatenate([[0], cuts, [P - 77]])
+    x, W = normal((P, K), "bf16", 281).cuda(), normal((E, N, K), "bf16", 282).cuda()
+    q, s = nsg.quantize_fp8(x)
+    wq, ws = nsg.quantize_fp8(W, block=how)
+    out = nsg.expert_gemm_fp8(q, s, wq, ws, torch.from_numpy(o.astype(np.int32)).cuda())
+    some = 0
+    for e in range(E):
+        b, n = o[e], o[e + 1] - o[e]
+        if n > 32:
+            alone = nsg.gemm_fp8_nt(q[b:b + n].contiguous(), s[:, b:b + n].contiguous(), wq[e], ws[e])
+            assert torch.equal(out[b:b + n], alone), e
+            some += 1
+    assert some > 20 and not out[P - 77:].any()
+    whole = nsg.gemm_fp8_nt(q, s, wq[3], ws[3])
+    for b in range(0, P, 1000):
+        part = nsg.gemm_fp8_nt(q[b:b + 1000].contiguous(), s[:, b:b + 1000].contiguous(), wq[3], ws[3])
+        assert torch.equal(whole[b:b + 1000], part)
