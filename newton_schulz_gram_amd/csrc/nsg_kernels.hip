@@ -352,10 +352,12 @@ __device__ __forceinline__ int lds_slice_off(int r, int c) { return r * 128 + ((
 // base + voff (bytes) and writes LDS bytes [lds + 16 l, lds + 16 l + 16).
 // Issued as inline assembly so that the compiler does not add waits for it
 // before unrelated LDS reads; the kernel waits (vmcnt) and synchronizes itself
-// before reading a stage.
+// before reading a stage.  The s_nop is the wait state that an LDS load needs
+// behind a write of m0; the compiler adds none inside assembly.
 __device__ __forceinline__ void lds_dma16(const void *base, unsigned voff, const void *lds) {
   const unsigned m0v = (unsigned)(size_t)(lds_ptr_t)lds;
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0v) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0v)
+               : "memory", "m0");
 }
 
 // s_waitcnt vmcnt(n) with expcnt / lgkmcnt left unconstrained (gfx9 encoding).
@@ -367,7 +369,7 @@ template <int N> __device__ __forceinline__ void wait_vmcnt() {
 // used only to pull lines into the caches ahead of the direct loads.
 __device__ __forceinline__ void lds_touch4(const void *addr, const void *lds) {
   const unsigned m0v = (unsigned)(size_t)(lds_ptr_t)lds;
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(addr), "s"(m0v) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(addr), "s"(m0v) : "memory", "m0");
 }
 // All of this wave's LDS reads have returned their data.
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
