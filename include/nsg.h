@@ -476,7 +476,8 @@ nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R,
  * out_dtype the 8-bit matrix instructions are used, which cut the products of 8
  * consecutive k off at 2^-13 of the largest one's power of two before they are
  * summed (about 1e-5 relative, far below that rounding); with F32 the products are
- * exact. */
+ * exact.  batch <= 65535, and NSG_ERR_SHAPE from about 2^24 tiles of 128 x 128
+ * outputs on, which one launch does not hold. */
 nsg_status_t nsg_gemm_fp8_nt(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t batch,
                              int64_t M, int64_t N, int64_t K, const void *qa, const float *sa,
                              int32_t a_block, const void *qb, const float *sb, int32_t b_block,

@@ -799,9 +799,12 @@ template <int BM, int BN> static int64_t grid_of(const F8GemmArgs &a) {
   return ((int64_t)a.E + 7) / 8 * 8 * ((a.M + BM - 1) / BM) * tn;
 }
 
+// HIP counts a launch's threads in 32 bits
+static bool launchable(int64_t grid, int threads) { return grid * threads <= 0xFFFFFFFFll; }
+
 // Calls launch<FA, FB, B_TILE>() for the types and scales of `a`.
 template <typename L> static hipError_t by_type(const F8GemmArgs &a, int64_t grid, int threads, L launch) {
-  if (grid * threads > 0xFFFFFFFFll) return hipErrorInvalidConfiguration;  // HIP counts a launch's threads in 32 bits
+  if (!launchable(grid, threads)) return hipErrorInvalidConfiguration;
   using one = std::integral_constant<int, 1>;
   using zero = std::integral_constant<int, 0>;
   auto scales = [&](auto fa, auto fb) { a.b_tile ? launch(fa, fb, one{}) : launch(fa, fb, zero{}); };
@@ -837,6 +840,13 @@ template <bool WIDE> static hipError_t launch_deep(const F8GemmArgs &a, hipStrea
   });
 }
 
+// whether a launch holds the few-rows kernel's workgroups, 16 NF columns of B each: for
+// batches of more than about 2^27 columns in all it does not, and the tile kernel's
+// (128 columns for 256 threads) it does
+template <int MF, int NF, int NW> static bool rows_launchable(const F8GemmArgs &a) {
+  return launchable(grid_of<16 * MF, 16 * NF>(a), NW * 64);
+}
+
 template <int MF, int NF, int NW, int U, bool WIDE> static hipError_t launch_rows(const F8GemmArgs &a, hipStream_t s) {
   const int64_t grid = grid_of<16 * MF, 16 * NF>(a);
   return by_type(a, grid, NW * 64, [&](auto fa, auto fb, auto tile) {
@@ -853,7 +863,7 @@ template <bool WIDE> static hipError_t launch_any(const F8GemmArgs &a, hipStream
   // few rows: 16 x 4096 x 4096 in 6.7 us against the deep kernel's 15.1, 32 in 8.5
   // against 15.3; with more rows of B those of A are read too often: 32 x 8192 x 4096 in
   // 13.9 against 15.3, 32 x 11008 x 4096 in 19.6 against 15.6
-  if (a.mode == kDense && a.M <= 16) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
+  if (a.mode == kDense && a.M <= 16 && rows_launchable<1, 1, 8>(a)) return launch_rows<1, 1, 8, 4, WIDE>(a, s);
   if (a.mode == kDense && a.M <= 32 && a.batch * a.N <= 8192) return launch_rows<2, 1, 8, 2, WIDE>(a, s);
   // one or two tokens' experts (K = 2048, N = 512): 1 x 8 rows in 6.2 us against the deep
   // kernel's 10.9, 2 x 8 in 9.5 against 11.6, 4 x 8 in 16.5 against 12.4
