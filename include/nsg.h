@@ -476,8 +476,10 @@ nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R,
  * out_dtype the 8-bit matrix instructions are used, which cut the products of 8
  * consecutive k off at 2^-13 of the largest one's power of two before they are
  * summed (about 1e-5 relative, far below that rounding); with F32 the products are
- * exact.  batch <= 65535, and NSG_ERR_SHAPE from about 2^24 tiles of 128 x 128
- * outputs on, which one launch does not hold. */
+ * exact.
+ * NSG_ERR_SHAPE also for a batch above 65535, a K that is no multiple of 128, K = 0
+ * (an empty sum: the zeros are left to the caller) and from about 2^24 tiles of
+ * 128 x 128 outputs on, which one launch does not hold. */
 nsg_status_t nsg_gemm_fp8_nt(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t batch,
                              int64_t M, int64_t N, int64_t K, const void *qa, const float *sa,
                              int32_t a_block, const void *qb, const float *sb, int32_t b_block,
@@ -485,7 +487,9 @@ nsg_status_t nsg_gemm_fp8_nt(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype
 
 /* The experts' products: out [P][N], out[r] = A[tokens[r]] B_e^T for the sorted
  * rows r of expert e (tokens NULL: A[r], T == P), zeros where tokens[r] is no
- * row of A and behind offsets[E].  qa [T][K] with row scales, qb [E][N][K]. */
+ * row of A and behind offsets[E].  qa [T][K] with row scales, qb [E][N][K].
+ * NSG_ERR_SHAPE also for K = 0 and T = 0 where there are outputs: those zeros are
+ * left to the caller. */
 nsg_status_t nsg_expert_gemm_fp8(int32_t a_dtype, int32_t b_dtype, int32_t out_dtype, int64_t T,
                                  int64_t P, int64_t E, int64_t N, int64_t K, const void *qa,
                                  const float *sa, const int32_t *tokens, const void *qb,

@@ -850,7 +850,7 @@ def gemm_fp8_nt(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A B^T of two 8-bit operands as quantize_fp8 returns them: qa [M, K] and qb
     [N, K], or batches [b, M, K] and [b, N, K]; either may have row or tile
-    scales.  fp32 sums, one rounding to out_dtype."""
+    scales.  fp32 sums, one rounding to out_dtype; zeros for K = 0."""
     device = _gpu(qa, "gemm_fp8_nt")
     ab = _operand(qa, sa, "qa", 2 if qa.dim() == 2 else 3, device)
     bb = _operand(qb, sb, "qb", qa.dim(), device)
@@ -859,6 +859,8 @@ def gemm_fp8_nt(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.
     M, K = qa.shape[-2:]
     N = qb.shape[-2]
     out = _product_out(out, (*qa.shape[:-2], M, N), out_dtype, device)
+    if K == 0:  # an empty sum, which the C entry point leaves to its caller
+        return out.zero_()
     _launch(device, "nsg_gemm_fp8_nt", lib().nsg_gemm_fp8_nt, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype],
             qa.shape[0] if qa.dim() == 3 else 1, M, N, K, qa.data_ptr(), sa.data_ptr(), ab, qb.data_ptr(), sb.data_ptr(),
             bb, out.data_ptr())
@@ -869,8 +871,9 @@ def expert_gemm_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: to
                     rows: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Each expert's product: out[r] = A[rows[r]] B_e^T for the sorted rows r of
-    expert e (A[r] without rows), zeros behind offsets[E].  qa [T, K] with row
-    scales, qb [E, N, K]; offsets and rows: a plan's offsets and tokens."""
+    expert e (A[r] without rows), zeros behind offsets[E], where rows[r] is no row
+    of A, and for K = 0.  qa [T, K] with row scales, qb [E, N, K]; offsets and
+    rows: a plan's offsets and tokens."""
     device = _gpu(qa, "expert_gemm_fp8")
     _operand(qa, sa, "qa", 2, device, ("row",))
     bb = _operand(qb, sb, "qb", 3, device)
@@ -883,6 +886,8 @@ def expert_gemm_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: to
         raise ValueError(f"operands {tuple(qa.shape)} and {tuple(qb.shape)} do not fit")
     P = T if rows is None else rows.numel()
     out = _product_out(out, (P, N), out_dtype, device)
+    if K == 0 or T == 0:  # empty sums, which the C entry point leaves to its caller
+        return out.zero_()
     _launch(device, "nsg_expert_gemm_fp8", lib().nsg_expert_gemm_fp8, _F8[qa.dtype], _F8[qb.dtype], _DT[out.dtype], T, P,
             E, N, K, qa.data_ptr(), sa.data_ptr(), rows.data_ptr() if rows is not None else None, qb.data_ptr(),
             sb.data_ptr(), bb, offsets.data_ptr(), out.data_ptr())

@@ -31,3 +31,32 @@ def test_the_largest_batch_of_few_rows(M, out):
     for r in range(some):
         exp = (a[r::some].double() * sa[r::some].double().transpose(1, 2)).flatten(0, 1) @ base[r].double().t() * scale
         assert torch.equal(got[r::some].flatten(0, 1), exp.to(out)), r
+
+
+# ---------------------------------------------------------------------------
+# empty sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("block", ["row", "tile"])
+def test_products_of_rows_without_elements_are_zero(out, block):
+    """quantize_fp8 takes rows of no elements; their products are empty sums."""
+    x, w = torch.zeros((200, 0), device="cuda"), torch.zeros((3, 140, 0), device="cuda")
+    a, b = nsg.quantize_fp8(x), nsg.quantize_fp8(w, block=block)
+    assert a[0].shape == (200, 0) and b[0].shape == (3, 140, 0)
+    for got, shape in ((nsg.gemm_fp8_nt(*a, b[0][0], b[1][0], out_dtype=out), (200, 140)),
+                       (nsg.gemm_fp8_nt(*b, *b, out_dtype=out), (3, 140, 140))):
+        assert got.dtype == out and got.shape == shape and not got.any()
+    used = torch.full((200, 140), float("nan"), dtype=out, device="cuda")
+    assert nsg.gemm_fp8_nt(*a, b[0][0], b[1][0], out=used) is used and not used.any()
+    plan = nsg.expert_sort(torch.arange(400, device="cuda").view(200, 2) % 4, 3)
+    got = nsg.expert_gemm_fp8(*a, *b, plan.offsets, rows=plan.tokens, out_dtype=out)
+    assert got.shape == (400, 140) and not got.any()
+
+
+def test_expert_product_of_no_tokens_is_zero():
+    """Rows that all point past the end of A, which has none."""
+    a = nsg.quantize_fp8(torch.zeros((0, 256), device="cuda"))
+    b = nsg.quantize_fp8(torch.ones((2, 64, 256), device="cuda"), block="tile")
+    offsets = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    got = nsg.expert_gemm_fp8(*a, *b, offsets, rows=torch.tensor([0, 1, -1, 7, 0], dtype=torch.int32, device="cuda"))
+    assert got.shape == (5, 64) and not got.any()
