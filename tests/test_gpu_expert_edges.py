@@ -60,3 +60,141 @@ def test_expert_product_of_no_tokens_is_zero():
     offsets = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
     got = nsg.expert_gemm_fp8(*a, *b, offsets, rows=torch.tensor([0, 1, -1, 7, 0], dtype=torch.int32, device="cuda"))
     assert got.shape == (5, 64) and not got.any()
+
+
+# ---------------------------------------------------------------------------
+# whole-line stores: 16-bit outputs whose rows take 16-byte stores, in whole column
+# tiles, leave by lanes that swap halves.  Tiles of 256 x 256 are taken from 160 full
+# ones on (with experts only from 96 rows per expert on, 192 with row scales), tiles of
+# 128 x 128 below that, from 257 of 64 x 64 on.  All sums are exact, so the results are
+# the exact ones rounded once, whatever the order.
+# ---------------------------------------------------------------------------
+def operand(shape, seed, f8, how="row"):
+    """An operand [..., R, K] of whole numbers with power-of-two scales, and its values."""
+    R, K = shape[-2:]
+    q = whole(shape, seed).float().to(f8)
+    n = R if how == "row" else -(-R // 128)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    s = torch.exp2(torch.randint(-1, 2, (*shape[:-2], K // 128, n), generator=g, device="cuda").float())
+    each = s if how == "row" else s.repeat_interleave(128, -1)[..., :R]
+    return (q, s), q.double() * each.transpose(-1, -2).repeat_interleave(128, -1).double()
+
+
+# 256 x 256 tiles: 14 matrices with 3 x 4 full ones, and 10 x 16; 128 x 128: the others
+@pytest.mark.parametrize("batch,M,N,K", [(1, 901, 1096, 384), (14, 901, 1096, 128), (1, 2601, 4104, 256), (1, 1100, 1024, 128)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("kinds", [("row", "tile"), ("row", "row"), ("tile", "tile")])
+def test_whole_line_stores(batch, M, N, K, out, kinds):
+    (a, av), (b, bv) = operand((batch, M, K), 10, E4M3, kinds[0]), operand((batch, N, K), 20, E5M2, kinds[1])
+    got = nsg.gemm_fp8_nt(*a, *b, out_dtype=out)
+    for i in range(batch):
+        assert torch.equal(got[i], (av[i] @ bv[i].t()).to(out)), i
+
+
+def segments(P, E, seed, tail):
+    """Offsets of E experts in P rows: odd starts and lengths, an expert without rows,
+    `tail` rows behind the last."""
+    g = torch.Generator().manual_seed(seed)
+    cut = torch.sort(torch.randint(0, P - tail + 1, (E - 1,), generator=g)).values
+    cut[1] = cut[0]
+    return torch.cat([torch.zeros(1, dtype=torch.long), cut, torch.tensor([P - tail])]).to(torch.int32).cuda()
+
+
+# 256 x 256 tiles: 40 x 4 full ones; 128 x 128
+@pytest.mark.parametrize("P,E", [(10300, 40), (1501, 12)])
+@pytest.mark.parametrize("N", [1096, 1024])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("how", ["row", "tile"])
+def test_whole_line_stores_of_experts(P, E, N, out, how):
+    T, K = 1200, 256
+    (a, av), (b, bv) = operand((T, K), 30, E5M2), operand((E, N, K), 40, E4M3, how)
+    o = segments(P, E, 50, tail=77)
+    g = torch.Generator(device="cuda").manual_seed(60)
+    rows = torch.randint(-20, T + 20, (P,), generator=g, device="cuda", dtype=torch.int32)  # some are no rows of A
+    got = nsg.expert_gemm_fp8(*a, *b, o, rows=rows, out_dtype=out)
+    there = (rows >= 0) & (rows < T)
+    x = torch.where(there[:, None], av[rows.clamp(0, T - 1).long()], 0.0)
+    for e in range(E):
+        s = slice(int(o[e]), int(o[e + 1]))
+        assert torch.equal(got[s], (x[s] @ bv[e].t()).to(out)), e
+    assert not got[int(o[-1]):].any()
+
+
+def columns(P, o, C, seed, f8):
+    """Columns-layout operand of whole numbers [C, cap] with scales by block, and its values."""
+    E = o.numel() - 1
+    cap = nsg.fp8_columns(P, E)
+    n = o.diff().long().cpu()
+    start = torch.cat([torch.zeros(1, dtype=torch.long), ((n + 127) // 128 * 128).cumsum(0)])
+    used = torch.zeros(cap, device="cuda")
+    for e in range(E):
+        used[start[e]:start[e] + n[e]] = 1
+    (q, s), _ = operand((C, cap), seed, f8)
+    q = (q.float() * used).to(f8)
+    return (q, s), q.double() * s.t().repeat_interleave(128, -1).double(), start
+
+
+# 256 x 256 tiles: 2 x 4 full ones for each of 20 experts; 128 x 128
+@pytest.mark.parametrize("P,E", [(3001, 20), (1003, 5)])
+@pytest.mark.parametrize("N,K", [(520, 1096), (519, 1024)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+def test_whole_line_stores_of_weight_gradients(P, E, N, K, out):
+    o = segments(P, E, 70, tail=0)
+    (a, av, start), (b, bv, _) = columns(P, o, N, 80, E5M2), columns(P, o, K, 90, E4M3)
+    got = nsg.expert_wgrad_fp8(*a, *b, o, out_dtype=out)
+    for e in range(E):
+        s = slice(int(start[e]), int(start[e + 1]))
+        assert torch.equal(got[e], (av[:, s] @ bv[:, s].t()).to(out)), e
+
+
+# ---------------------------------------------------------------------------
+# operands whose rows lie past 32-bit offsets, in every kernel that takes them
+# ---------------------------------------------------------------------------
+# T rows of 4096 bytes are 4.5 GB; 256 x 256 tiles: 40 x 4 full ones; 128 x 128
+@pytest.mark.parametrize("P,E", [(10300, 40), (1501, 12)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("how", ["row", "tile"])
+def test_far_rows_of_experts(P, E, out, how):
+    T, K, N, some = 1_100_000, 4096, 1096, 500
+    (few, fs), fv = operand((2 * some, K), 100, E4M3)
+    q = torch.zeros((T, K), dtype=torch.uint8, device="cuda").view(E4M3)
+    s = torch.ones((K // 128, T), device="cuda")
+    at = torch.cat([torch.arange(some), torch.arange(T - some, T)]).cuda()
+    q.view(torch.uint8)[at] = few.view(torch.uint8)
+    s[:, at] = fs
+    (b, bv) = operand((E, N, K), 110, E4M3, how)
+    o = segments(P, E, 120, tail=9)
+    g = torch.Generator(device="cuda").manual_seed(130)
+    pick = torch.randint(0, 2 * some, (P,), generator=g, device="cuda")
+    got = nsg.expert_gemm_fp8(q, s, *b, o, rows=at[pick].to(torch.int32), out_dtype=out)
+    for e in range(E):
+        r = slice(int(o[e]), int(o[e + 1]))
+        assert torch.equal(got[r], (fv[pick[r]] @ bv[e].t()).to(out)), e
+    assert not got[int(o[-1]):].any()
+
+
+# rows are P bytes: 256 of them from P = 2^24 on, 128 from 2^25 on are more than 2^32.
+# 256 x 256 tiles: 2 x 2 full ones for each of 40 experts; 128 x 128
+@pytest.mark.parametrize("P,N,K,out", [((1 << 24) + 1000, 512, 520, torch.bfloat16), (1 << 25, 264, 272, torch.bfloat16),
+                                       (1 << 25, 264, 272, torch.float32)])
+def test_far_rows_of_weight_gradients(P, N, K, out):
+    E, each = 40, 150
+    n = torch.full((E,), each)
+    n[20] = P - (E - 1) * each  # one expert has nearly all rows, the others lie on both sides
+    o = torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)]).to(torch.int32).cuda()
+    cap = nsg.fp8_columns(P, E)
+    start = torch.cat([torch.zeros(1, dtype=torch.long), ((n + 127) // 128 * 128).cumsum(0)])
+    q = torch.zeros((K, cap), dtype=torch.uint8, device="cuda").view(E4M3)
+    s = torch.ones((cap // 128, K), device="cuda")
+    values = []  # 256 columns of each expert hold numbers: its rows, or its last ones
+    for e in range(E):
+        (v, vs), _ = operand((K, 256), 140 + e, E4M3)
+        v[:, each if e != 20 else 256 - int(-n[e] % 128):] = 0  # columns that are no row
+        c = int(start[e]) if e != 20 else int(start[21]) - 256
+        q.view(torch.uint8)[:, c:c + 256] = v.view(torch.uint8)
+        s[c // 128:c // 128 + 2] = vs
+        values.append(v.double() * vs.t().repeat_interleave(128, -1).double())
+    qa, sa = q[K - N:], s[:, K - N:].contiguous()
+    got = nsg.expert_wgrad_fp8(qa, sa, q, s, o, out_dtype=out)
+    for e in range(E):
+        assert torch.equal(got[e], (values[e][K - N:] @ values[e].t()).to(out)), e
