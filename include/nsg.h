@@ -472,7 +472,9 @@ nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R,
  * q s of operands as nsg_quantize_fp8 lays them out (qa [batch][M][K], qb
  * [batch][N][K], K their padded length; a_block, b_block say which scales they
  * have).  Products of a block of 128 are summed in fp32, blocks in fp32, and
- * the result is rounded once to out_dtype (F16, BF16 or F32).  With a 16-bit
+ * the result is rounded once to out_dtype (F16, BF16 or F32).  Scales may be any fp32
+ * numbers, also where the product of two is past fp32's largest; a product below
+ * 2^-126 is rounded to a multiple of 2^-149.  With a 16-bit
  * out_dtype the 8-bit matrix instructions are used, which cut the products of 8
  * consecutive k off at 2^-13 of the largest one's power of two before they are
  * summed (about 1e-5 relative, far below that rounding); with F32 the products are

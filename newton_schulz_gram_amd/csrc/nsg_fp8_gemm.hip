@@ -4,7 +4,8 @@
 //
 // A holds tokens (or output gradients), B weights (or activations).  The outer
 // sum is one fp32 fused multiply-add per block and element, on the VALU, while
-// the matrix cores run the next block.  Scales may be any fp32 numbers.
+// the matrix cores run the next block.  Scales may be any fp32 numbers; what is done
+// where the product of two leaves fp32's range stands at not_finite below.
 //
 // The inner sum of a block starts from zero, in one of two ways:
 //   16-bit outputs: one v_mfma_f32_16x16x128_f8f6f4.  Its sums are fp32, but
@@ -250,6 +251,95 @@ __device__ __forceinline__ int64_t row_of_a(const F8GemmArgs &p, int64_t m, bool
 }
 
 // ---------------------------------------------------------------------------
+// Scales whose product is past the largest fp32 number.  The kernels below multiply a
+// block's sum d by sa sb, formed first: one product serves a row of a tile, and a large
+// scale with a small one stays in range.  Where both are so large that sa sb is
+// infinite, d = 0 gives NaN and a small d infinity, whatever the result; the output is
+// not finite then in any case, since no later block brings it back.  So each kernel
+// looks at its outputs once at the end (not_finite), and where one is not finite and
+// the scales can be the cause, the wave computes its outputs again with (d sa) sb:
+// both factors are above 1 there, so d sa is infinite only where the result is.
+// (The looks cost the weight gradients of 512 experts 459 -> 463 us, the others nothing.
+// The loops below are not unrolled: they hardly ever run, and unrolled they changed the
+// registers of the kernels around them, 256 x 4096 x 4096 15.6 -> 15.8 us.)
+// A product sa sb below 2^-126 is rounded to a multiple of 2^-149 and changes a block's
+// part of the output by at most 2^-150 |d|, below 2^-111 (e5m2) or 2^-125 (e4m3).
+// ---------------------------------------------------------------------------
+// seen = largest size of the values that it was called with, NaN where one was among
+// them (one v_maximum3 for two values)
+__device__ __forceinline__ void look_at(float a, float b, float &seen) {
+  seen = __builtin_elementwise_maximum(__builtin_elementwise_maximum(seen, __builtin_fabsf(a)), __builtin_fabsf(b));
+}
+__device__ __forceinline__ bool not_finite(float seen) { return __builtin_expect(__any(!(seen < __builtin_inff())), 0); }
+
+// Whether scales of rows m .. m + rows - 1 and n .. n + cols - 1 can have an infinite product.
+__device__ __forceinline__ bool scales_overflow(const F8GemmArgs &p, const Work &w, int64_t m, int rows, int64_t n, int cols) {
+  const int lane = threadIdx.x & 63;
+  float a = 0.f, b = 0.f;
+  bool there = true;
+  for (int r = lane; r < rows; r += 64) {
+    const int64_t row = row_of_a(p, min(m + r, w.m1 - 1), there);
+    const float *s = w.sa + (p.a_tile ? row >> 7 : row);
+#pragma unroll 1
+    for (int kb = 0; kb < w.nkb; ++kb) a = fmaxf(a, fabsf(s[kb * w.ka]));
+  }
+  for (int c = lane; c < cols; c += 64) {
+    const int64_t col = min(n + c, p.N - 1);
+    const float *s = w.sb + (p.b_tile ? col >> 7 : col);
+#pragma unroll 1
+    for (int kb = 0; kb < w.nkb; ++kb) b = fmaxf(b, fabsf(s[kb * w.kb]));
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    a = fmaxf(a, __shfl_xor(a, off, 64));
+    b = fmaxf(b, __shfl_xor(b, off, 64));
+  }
+  return a * b > 0x1.fffffep127f;
+}
+
+// The 16 x 16 outputs from row m and column n, straight from memory, block by block in
+// order as the tile and deep kernels add them.
+template <int FA, int FB, bool WIDE>
+__device__ __forceinline__ void compute_again(const F8GemmArgs &p, const Work &w, int64_t m, int64_t n) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+  bool there = true;
+  const int64_t row = row_of_a(p, min(m + r16, w.m1 - 1), there);
+  const uint8_t *a = w.A + row * p.K + 16 * g, *b = w.B + min(n + r16, p.N - 1) * p.K + 16 * g;
+  m += r16;
+  n += 4 * g;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int64_t kb = 0; kb < w.nkb; ++kb) {
+    Frag<FA, WIDE> fa;
+    Frag<FB, WIDE> fb;
+    fa.set(*reinterpret_cast<const i32x4 *>(a + kb * kF8Block), *reinterpret_cast<const i32x4 *>(a + kb * kF8Block + 64));
+    fb.set(*reinterpret_cast<const i32x4 *>(b + kb * kF8Block), *reinterpret_cast<const i32x4 *>(b + kb * kF8Block + 64));
+    const f32x4 d = mma<FA, FB>(fb, fa);
+    const float sa = w.sa[kb * w.ka + (p.a_tile ? row >> 7 : row)];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t c = min(n + v, p.N - 1);
+      const float sb = w.sb[kb * w.kb + (p.b_tile ? c >> 7 : c)], x = sa * sb;
+      const bool past = __builtin_isinf(x) && !__builtin_isinf(sa) && !__builtin_isinf(sb);
+      acc[v] = fmaf(past ? d[v] * sa : d[v], past ? sb : x, acc[v]);
+    }
+  }
+  if (m >= w.m1 || n >= p.N) return;
+  if (!there) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  store4(p.out, p.out_dtype, w.out + m * p.N + n, acc, p.N - n, false);
+}
+
+// A wave's 16 MF x 16 NF outputs from row m and column n, already stored, of which one was
+// not finite.
+template <int MF, int NF, int FA, int FB, bool WIDE>
+__device__ __forceinline__ void mend(const F8GemmArgs &p, const Work &w, int64_t m, int64_t n) {
+  if (!scales_overflow(p, w, m, 16 * MF, n, 16 * NF)) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // other lanes stored what this one stores now
+#pragma unroll 1
+  for (int f = 0; f < MF * NF; ++f) compute_again<FA, FB, WIDE>(p, w, m + 16 * (f % MF), n + 16 * (f / MF));
+}
+
+// ---------------------------------------------------------------------------
 // Tile kernel: BM x BN outputs, WGM x WGN waves.  Both operands stream through
 // LDS in stages of one block (128 bytes of each row), in two slots, with their
 // scales, in three.  LDS rows are 128 bytes; chunk c (16 bytes) of row r sits at
@@ -487,6 +577,17 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
 #pragma unroll
   for (int j = 0; j < 3; ++j) add(NF - 1, j + 1, s[j + 1]);
 
+  float seen = 0.f;
+  // row j's outputs, once they are on their way (with a tile scale of B a row has one
+  // product of scales for all columns)
+  auto look_at_row = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < (B_TILE ? 1 : NF); ++i) {
+      look_at(acc[i][j][0], acc[i][j][1], seen);
+      if (!B_TILE) look_at(acc[i][j][2], acc[i][j][3], seen);
+    }
+  };
+
   const bool vec = (p.N * (p.out_dtype == NSG_F32 ? 4 : 2)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   if (vec && p.out_dtype != NSG_F32 && w.n0 + BN <= p.N) {
     // (large products, past the caches: weight gradients of 512 experts, 1.07 GB, 467 ->
@@ -525,6 +626,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
           if (mo < w.m1) *to = vo;
         }
       }
+      look_at_row(j);
     }
   } else {
 #pragma unroll
@@ -541,8 +643,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) gemm_f8_tile_kernel(const F8
         for (int k = 0; k < 8; ++k) v[k] = there ? acc[i + (k >> 2)][j][k & 3] : 0.f;
         store8(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
       }
+      look_at_row(j);
     }
   }
+  if (not_finite(seen)) mend<MF, NF, FA, FB, WIDE>(p, w, w.m0 + wm * MF * 16, w.n0 + wn * NF * 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -658,6 +762,7 @@ __global__ void __launch_bounds__(256, 2) gemm_f8_deep_kernel(const F8GemmArgs p
   if (kt < w.nkb) stage(kt, 0);
 
   const bool vec = (p.N * (p.out_dtype == NSG_F32 ? 4 : 2)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  float seen = 0.f;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int64_t m = w.m0 + rA + 16 * j, n = w.n0 + wn * 32 + 8 * g;
@@ -667,8 +772,11 @@ __global__ void __launch_bounds__(256, 2) gemm_f8_deep_kernel(const F8GemmArgs p
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = there ? acc[k >> 2][j][k & 3] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) look_at(v[k], v[k + 1], seen);
     store8(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
   }
+  if (not_finite(seen)) mend<2, 2, FA, FB, WIDE>(p, w, w.m0 + wm * 32, w.n0 + wn * 32);
 }
 
 // ---------------------------------------------------------------------------
@@ -772,11 +880,16 @@ __global__ void __launch_bounds__(NW * 64) gemm_f8_rows_kernel(const F8GemmArgs 
 #pragma unroll
     for (int k = 1; k < NW; ++k) v += sums[k][f][lane];
     const int64_t m = w.m0 + 16 * (f % MF) + r16, n = w.n0 + 16 * (f / MF) + 4 * g;
-    if (m >= w.m1 || n >= p.N) continue;
-    there = true;
-    if (!w.zero) row_of_a(p, m, there);
-    if (!there) v = f32x4{0.f, 0.f, 0.f, 0.f};
-    store4(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
+    float seen = 0.f;
+    look_at(v[0], v[1], seen);
+    look_at(v[2], v[3], seen);
+    if (m < w.m1 && n < p.N) {
+      there = true;
+      if (!w.zero) row_of_a(p, m, there);
+      if (!there) v = f32x4{0.f, 0.f, 0.f, 0.f};
+      store4(p.out, p.out_dtype, w.out + m * p.N + n, v, p.N - n, vec);
+    }
+    if (not_finite(seen)) mend<1, 1, FA, FB, WIDE>(p, w, m - r16, n - 4 * g);
   }
 }
 

@@ -198,3 +198,101 @@ def test_far_rows_of_weight_gradients(P, N, K, out):
     got = nsg.expert_wgrad_fp8(qa, sa, q, s, o, out_dtype=out)
     for e in range(E):
         assert torch.equal(got[e], (values[e][K - N:] @ values[e].t()).to(out)), e
+
+
+# ---------------------------------------------------------------------------
+# scales whose product is past the largest fp32 number
+# ---------------------------------------------------------------------------
+def large_block(op, how, exponent, kinds):
+    """The operand with the scale 2^exponent in its second block, where row r holds only
+    its element 5, kinds[r % len(kinds)]; and its values."""
+    q, s = op[0].float(), op[1].clone()
+    R = q.shape[-2]
+    q[..., 128:256] = 0
+    q[..., 133] = torch.tensor(kinds, device="cuda")[torch.arange(R, device="cuda") % len(kinds)]
+    s[..., 1, :] = 2.0 ** exponent
+    q = q.to(op[0].dtype)
+    each = s if how == "row" else s.repeat_interleave(128, -1)[..., :R]
+    return (q, s), q.double() * each.transpose(-1, -2).repeat_interleave(128, -1).double()
+
+
+# 2^-9 is e4m3's smallest number: 2^-18 2^140 is a number, 2^-9 2^140 is infinite
+A_KINDS, B_KINDS = (0.0, 2.0 ** -9, 1.0), (0.0, 2.0 ** -9)
+
+
+# the kernels for few rows, for few tiles, tiles of 128 x 128 and 256 x 256 (16-bit outputs)
+@pytest.mark.parametrize("batch,M,N", [(1, 3, 200), (1, 20, 100), (2, 100, 200), (1, 901, 1096), (14, 901, 1096), (14, 901, 1091)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("kinds", [("row", "tile"), ("row", "row"), ("tile", "tile")])
+def test_scales_with_an_infinite_product(batch, M, N, out, kinds):
+    """A block sum of 0 adds nothing and a small one a number, as by the definition,
+    although the product of the scales alone is infinite."""
+    a, av = large_block(operand((batch, M, 384), 200, E4M3, kinds[0])[0], kinds[0], 70, A_KINDS)
+    b, bv = large_block(operand((batch, N, 384), 210, E4M3, kinds[1])[0], kinds[1], 70, B_KINDS)
+    got = nsg.gemm_fp8_nt(*a, *b, out_dtype=out)
+    for i in range(batch):
+        exp = (av[i] @ bv[i].t()).float().to(out)
+        assert torch.equal(got[i], exp), i
+        assert M < 3 or out == torch.float16 or exp[1, 1] == 2.0 ** 122 and exp[2, 1] == float("inf") and exp[2, 0].isfinite()
+
+
+@pytest.mark.parametrize("P,E,N", [(9, 3, 100), (300, 4, 200), (1501, 12, 1096), (10300, 40, 1096)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("how", ["row", "tile"])
+def test_scales_of_experts_with_an_infinite_product(P, E, N, out, how):
+    T = 1200
+    a, av = large_block(operand((T, 384), 220, E4M3)[0], "row", 70, A_KINDS)
+    b, bv = large_block(operand((E, N, 384), 230, E4M3, how)[0], how, 70, B_KINDS)
+    o = segments(P, E, 240, tail=2)
+    g = torch.Generator(device="cuda").manual_seed(250)
+    rows = torch.randint(-20, T, (P,), generator=g, device="cuda", dtype=torch.int32)
+    got = nsg.expert_gemm_fp8(*a, *b, o, rows=rows, out_dtype=out)
+    x = torch.where((rows >= 0)[:, None], av[rows.clamp(min=0).long()], 0.0)
+    for e in range(E):
+        s = slice(int(o[e]), int(o[e + 1]))
+        assert torch.equal(got[s], (x[s] @ bv[e].t()).float().to(out)), e
+    assert not got[int(o[-1]):].any()
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 100, 70), (5, 520, 1096), (20, 520, 1096)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_scales_of_weight_gradients_with_an_infinite_product(E, N, K, out):
+    P = 384 * E  # three blocks for each expert
+    o = (384 * torch.arange(E + 1)).to(torch.int32).cuda()
+    (a, _, _), (b, _, _) = columns(P, o, N, 260, E4M3), columns(P, o, K, 270, E4M3)
+    got_a, av = zip(*[large_block((a[0][:, c:c + 384], a[1][c // 128:c // 128 + 3]), "row", 70, A_KINDS) for c in range(0, P, 384)])
+    got_b, bv = zip(*[large_block((b[0][:, c:c + 384], b[1][c // 128:c // 128 + 3]), "row", 70, B_KINDS) for c in range(0, P, 384)])
+    join = lambda whole, parts: (torch.cat([p[0] for p in parts] + [whole[0][:, P:]], 1).contiguous(),  # noqa: E731
+                                 torch.cat([p[1] for p in parts] + [whole[1][P // 128:]]))
+    got = nsg.expert_wgrad_fp8(*join(a, got_a), *join(b, got_b), o, out_dtype=out)
+    for e in range(E):
+        assert torch.equal(got[e], (av[e] @ bv[e].t()).float().to(out)), e
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (100, 200), (901, 1096)])
+def test_infinite_sums_and_nan_are_not_computed_away(M, N):
+    """What is infinite or NaN by the definition stays so, also next to such scales."""
+    (a, _), (b, _) = operand((M, 384), 280, E4M3), operand((N, 384), 290, E4M3)
+    a, av = large_block(a, "row", 70, (1.0, 0.0))
+    b, bv = large_block(b, "row", 70, (1.0, -1.0, 0.0))
+    a[0][1, 300] = float("nan")
+    got = nsg.gemm_fp8_nt(*a, *b, out_dtype=torch.float32)
+    exp = (av @ bv.t()).float()
+    exp[1] = float("nan")
+    assert torch.equal(got.nan_to_num(7.0, 8.0, 9.0), exp.nan_to_num(7.0, 8.0, 9.0))
+    assert exp[0, 0] == float("inf") and exp[0, 1] == -float("inf") and exp[0, 2].isfinite()
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (100, 200), (901, 1096)])
+@pytest.mark.parametrize("f8", [E4M3, E5M2])
+def test_scales_with_a_subnormal_product(M, N, f8):
+    """sa sb is rounded to a multiple of 2^-149, so that a block of 128 products adds an
+    error of 2^-150 times their sum's size; then one rounding a block."""
+    (a, av), (b, bv) = operand((M, 384), 300, f8), operand((N, 384), 310, f8)
+    a, b = (a[0], a[1] * 1.37 * 2.0 ** -66), (b[0], b[1] * 1.19 * 2.0 ** -66)
+    av, bv = (q.double() * s.double().t().repeat_interleave(128, -1) for q, s in (a, b))
+    got = nsg.gemm_fp8_nt(*a, *b, out_dtype=torch.float32).double()
+    size = sum((a[0][:, k:k + 128].double() @ b[0][:, k:k + 128].double().t()).abs() for k in range(0, 384, 128))
+    exp = av @ bv.t()
+    assert torch.all((got - exp).abs() <= size * 2.0 ** -150 * (1 + 2.0 ** -20) + 3 * 2.0 ** -149 + 4 * 2.0 ** -24 * exp.abs())
+    assert got.abs().max() > 0
