@@ -474,11 +474,13 @@ nsg_status_t nsg_quantize_fp8_columns(const void *x, int32_t x_dtype, int64_t R,
  * have).  Products of a block of 128 are summed in fp32, blocks in fp32, and
  * the result is rounded once to out_dtype (F16, BF16 or F32).  Scales may be any fp32
  * numbers, also where the product of two is past fp32's largest; a product below
- * 2^-126 is rounded to a multiple of 2^-149.  With a 16-bit
- * out_dtype the 8-bit matrix instructions are used, which cut the products of 8
- * consecutive k off at 2^-13 of the largest one's power of two before they are
- * summed (about 1e-5 relative, far below that rounding); with F32 the products are
- * exact.
+ * 2^-126 is rounded to a multiple of 2^-149.
+ * With F32 the products are exact.  With a 16-bit out_dtype the 8-bit matrix
+ * instructions are used, which cut the products of 8 consecutive k off at 2^-13 of the
+ * largest one's power of two before they are summed: an error below 7 * 2^-13 of the
+ * largest |a b| of each 8.  On normal values that is about 1e-5 of the result, but it
+ * is relative to the products: where large ones of different groups of 8 cancel, what
+ * is left of the smaller ones beside them can be lost, and F32 is the type to take.
  * NSG_ERR_SHAPE also for a batch above 65535, a K that is no multiple of 128, K = 0
  * (an empty sum: the zeros are left to the caller) and from about 2^24 tiles of
  * 128 x 128 outputs on, which one launch does not hold. */

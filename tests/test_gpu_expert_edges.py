@@ -296,3 +296,21 @@ def test_scales_with_a_subnormal_product(M, N, f8):
     exp = av @ bv.t()
     assert torch.all((got - exp).abs() <= size * 2.0 ** -150 * (1 + 2.0 ** -20) + 3 * 2.0 ** -149 + 4 * 2.0 ** -24 * exp.abs())
     assert got.abs().max() > 0
+
+
+@pytest.mark.parametrize("M,N,batch", [(3, 200, 1), (100, 200, 1), (901, 1096, 1), (901, 1096, 14)])
+def test_large_products_that_cancel(M, N, batch):
+    """448^2 and -448^2 in different groups of 8 and numbers of 1 beside them.  fp32 outputs
+    hold the sum exactly; 16-bit outputs are off by 7 * 2^-13 of the largest product of each
+    group at most, then by one rounding (the sum of 14 is a number of both types)."""
+    a, b = torch.ones((batch, M, 128), device="cuda"), torch.zeros((batch, N, 128), device="cuda")
+    a[..., 0], a[..., 64] = 448, 448
+    b[..., 0], b[..., 64] = 448, -448
+    b[..., 1:8], b[..., 65:72] = 1, 1
+    one = torch.ones((batch, 1, M), device="cuda"), torch.ones((batch, 1, N), device="cuda")
+    args = a.to(E4M3), one[0], b.to(E4M3), one[1]
+    assert torch.all(nsg.gemm_fp8_nt(*args, out_dtype=torch.float32) == 14)
+    bound = 2 * 7 * 2.0 ** -13 * 448 ** 2
+    for out in (torch.bfloat16, torch.float16):
+        off = (nsg.gemm_fp8_nt(*args, out_dtype=out).double() - 14).abs().max()
+        assert off <= bound + torch.finfo(out).eps / 2 * (14 + bound)
