@@ -277,10 +277,12 @@ hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C,
 // combine and its gradient.  A lane owns V consecutive elements of a row: 16
 // bytes of them, or one element where rows do not take 16-byte accesses.
 // ---------------------------------------------------------------------------
-template <typename T, int V> struct Row {
+// ALIGN: bytes that the elements are aligned to (the instructions take any).
+template <typename T, int V, int ALIGN = V * (int)sizeof(T)> struct Row {
   typedef T vec __attribute__((ext_vector_type(V)));
+  typedef vec mem __attribute__((aligned(ALIGN)));
   static __device__ __forceinline__ void load(const T *p, float (&f)[V]) {
-    const vec x = *reinterpret_cast<const vec *>(p);
+    const vec x = *reinterpret_cast<const mem *>(p);
 #pragma unroll
     for (int v = 0; v < V; ++v) f[v] = (float)x[v];
   }
@@ -288,10 +290,10 @@ template <typename T, int V> struct Row {
     vec x;
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = (T)f[v];
-    *reinterpret_cast<vec *>(p) = x;
+    *reinterpret_cast<mem *>(p) = x;
   }
 };
-template <typename T> struct Row<T, 1> {
+template <typename T, int ALIGN> struct Row<T, 1, ALIGN> {
   static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = (float)*p; }
   static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = (T)f[0]; }
 };
@@ -321,7 +323,8 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const T *__restrict
 }
 
 // One wave per choice; a token's choices are neighbours, so dout comes from cache
-// for all but one.
+// for all but one.  Whether a lane takes V elements at once goes by C alone, so that
+// neither alignment nor pitch changes the order of dw's sum.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) expert_combine_backward_kernel(
     const T *__restrict__ dout, int64_t lddo, const T *__restrict__ y, int64_t ldy, int64_t P, int64_t C,
@@ -341,14 +344,14 @@ __global__ void __launch_bounds__(256) expert_combine_backward_kernel(
 #pragma unroll 4
     for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) {
       float u[V], v[V];
-      Row<T, V>::load(d + c, u);
-      Row<T, V>::load(f + c, v);
+      Row<T, V, (int)sizeof(T)>::load(d + c, u);
+      Row<T, V, (int)sizeof(T)>::load(f + c, v);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         dot = fmaf(u[i], v[i], dot);
         u[i] *= g;
       }
-      Row<T, V>::store(out + c, u);
+      Row<T, V, (int)sizeof(T)>::store(out + c, u);
     }
   }
 #pragma unroll
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(256) expert_combine_backward_kernel(
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = 0.f;
-    for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) Row<T, V>::store(dy + p * C + c, z);
+    for (int64_t c = (int64_t)lane * V; c < C; c += 64 * V) Row<T, V, (int)sizeof(T)>::store(dy + p * C + c, z);
   }
 }
 
@@ -396,7 +399,7 @@ static hipError_t backward_t(const void *dout, int64_t lddo, const void *y, int6
                              float *dw, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const dim3 grid((unsigned)((P + 3) / 4));
-  if (aligned16(dout) && aligned16(y) && aligned16(dy) && C % V == 0 && ldy % V == 0 && lddo % V == 0)
+  if (C % V == 0)
     hipLaunchKernelGGL((expert_combine_backward_kernel<T, V>), grid, dim3(256), 0, s, (const T *)dout, lddo,
                        (const T *)y, ldy, P, C, offsets, E, rows, k, w, (T *)dy, dw);
   else

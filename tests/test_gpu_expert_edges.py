@@ -63,6 +63,34 @@ def test_expert_product_of_no_tokens_is_zero():
 
 
 # ---------------------------------------------------------------------------
+# the order of sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("C", [1, 64, 129, 1000, 2048])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (3, 2), (8, 0), (5, 7)])
+def test_gradients_do_not_depend_on_pitch_or_alignment(C, dt, pad, shift):
+    """Views whose rows lie apart or start anywhere give the bits of packed rows."""
+    T, k, E = 60, 3, 5
+    g = torch.Generator(device="cuda").manual_seed(C)
+    plan = nsg.expert_sort(torch.randint(-1, E, (T, k), generator=g, device="cuda"), E)
+    w = torch.randn((T, k), generator=g, device="cuda")
+
+    def moved(x):
+        big = torch.full((x.shape[0] * (C + pad) + shift,), float("nan"), dtype=dt, device="cuda")
+        view = big[shift:].view(x.shape[0], C + pad)[:, :C]
+        view.copy_(x)
+        return view
+
+    dout, y = (torch.randn((n, C), generator=g, device="cuda").to(dt) for n in (T, T * k))
+    dy, dw = nsg.expert_combine_backward(dout, y, plan, w)
+    for a, b in ((moved(dout), y), (dout, moved(y)), (moved(dout), moved(y))):
+        dy2, dw2 = nsg.expert_combine_backward(a, b, plan, w)
+        assert torch.equal(dw, dw2) and torch.equal(dy, dy2)
+    assert torch.equal(nsg.expert_combine(moved(y), plan, w), nsg.expert_combine(y, plan, w))
+    assert torch.equal(nsg.expert_dispatch(moved(dout), plan), nsg.expert_dispatch(dout, plan))
+
+
+# ---------------------------------------------------------------------------
 # whole-line stores: 16-bit outputs whose rows take 16-byte stores, in whole column
 # tiles, leave by lanes that swap halves.  Tiles of 256 x 256 are taken from 160 full
 # ones on (with experts only from 96 rows per expert on, 192 with row scales), tiles of
