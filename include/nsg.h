@@ -396,7 +396,8 @@ nsg_status_t ns_muon_step(void *W, int32_t w_dtype, void *M, int32_t m_dtype, co
  *     index outside its range counts as "none" and offsets are clamped to their
  *     range, so wrong ones give wrong results, never an access out of bounds.
  *   - Limits: E <= NSG_MAX_EXPERTS, at most NSG_MAX_ROWS tokens or sorted rows, other
- *     sides at most NSG_MAX_SIDE; beyond them NSG_ERR_SHAPE. */
+ *     sides at most NSG_MAX_SIDE, ld at most 2^31; beyond them, and beyond those that a
+ *     call names, NSG_ERR_SHAPE. */
 #define NSG_MAX_EXPERTS 1024
 #define NSG_MAX_ROWS (1 << 25)
 
@@ -449,7 +450,8 @@ nsg_status_t nsg_expert_combine_backward(const void *dout, int64_t lddo, const v
  *   q      [B][R][Cp], Cp = C rounded up to a multiple of 128, zeros behind C
  *   q_t, scale_t  (tiles only, both or neither) the transposed matrix with the
  *          same numbers: [B][C][Rp] and [B][Rp/128][ceil(C/128)]
- * B <= 65535. */
+ * B <= 65535; tiles: R <= 128 * 65535; rows: B ceil(R / 1048560) <= 65535 (a launch's
+ * grid). */
 #define NSG_BLOCK_ROW 0
 #define NSG_BLOCK_TILE 1
 nsg_status_t nsg_quantize_fp8(const void *x, int32_t x_dtype, int64_t B, int64_t R, int64_t C,

@@ -758,7 +758,8 @@ def quantize_fp8(x: torch.Tensor, block: str = "row", dtype=torch.float8_e4m3fn,
     with scale = max(amax / F, 2^-126).  With `transposed` (tiles) also the
     operand of the transposed matrix, (q, scale, qt, scale_t), with the same
     numbers.  Infinities and NaN do not change their block's scale and become NaN
-    (an infinity stays one in float8_e5m2)."""
+    (an infinity stays one in float8_e5m2).  At most 2^25 rows of a matrix,
+    128 * 65535 with "tile"."""
     device = _gpu(x, "quantize_fp8")
     xs = x.unsqueeze(0) if x.dim() == 2 else x
     if xs.dim() != 3 or x.dtype not in _DT:

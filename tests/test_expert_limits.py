@@ -29,3 +29,16 @@ def test_the_largest_batch_of_few_rows(M, N, out, block):
 @pytest.mark.parametrize("M,N", [(16, 65536), (1 << 25, 65536)])
 def test_more_tiles_than_a_launch_holds(M, N):
     assert gemm(65535, M, N) == SHAPE
+
+
+def quantize(block, B, R, C=128, ld=None):
+    return nsg.lib().nsg_quantize_fp8(P16, 1, B, R, C, C if ld is None else ld, block, 3, P16, P16, None, None, None)
+
+
+@pytest.mark.parametrize("block,B,R,ld,code", [
+    (1, 1, 128 * 65535, None, HIP), (1, 1, 128 * 65535 + 1, None, SHAPE), (0, 1, 1 << 25, None, HIP), (0, 1, (1 << 25) + 1, None, SHAPE),
+    (0, 65535, 1048560, None, HIP), (0, 65535, 1048561, None, SHAPE), (0, 32767, 1048561, None, HIP), (1, 65535, 1000, None, HIP),
+    (0, 1, 4, 1 << 31, HIP), (0, 1, 4, (1 << 31) + 1, SHAPE),
+])
+def test_the_documented_limits_of_the_quantisers(block, B, R, ld, code):
+    assert quantize(block, B, R, ld=ld) == code
