@@ -349,15 +349,18 @@ __device__ __forceinline__ int slice_swz(int r) { return (r ^ (r >> 3)) & 7; }
 __device__ __forceinline__ int lds_slice_off(int r, int c) { return r * 128 + ((c ^ slice_swz(r)) << 4); }
 
 // One direct global -> LDS load of 16 bytes per lane: lane l reads
-// base + voff (bytes) and writes LDS bytes [lds + 16 l, lds + 16 l + 16).
+// base + voff (bytes) and writes LDS bytes [lds + more + 16 l, lds + more + 16 l + 16).
 // Issued as inline assembly so that the compiler does not add waits for it
 // before unrelated LDS reads; the kernel waits (vmcnt) and synchronizes itself
 // before reading a stage.  The s_nop is the wait state that an LDS load needs
-// behind a write of m0; the compiler adds none inside assembly.
-__device__ __forceinline__ void lds_dma16(const void *base, unsigned voff, const void *lds) {
+// behind a write of m0; the compiler adds none inside assembly.  `more` is a
+// constant, so that one register serves a wave's loads of a slot (a register for
+// each load does not fit and is kept in vector lanes: 7B bucket 54.7 against 53.9
+// ms, square matrices 35.3 against 34.7).
+__device__ __forceinline__ void lds_dma16(const void *base, unsigned voff, const void *lds, int more) {
   const unsigned m0v = (unsigned)(size_t)(lds_ptr_t)lds;
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0v)
-               : "memory", "m0");
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0v), "i"(more)
+               : "memory", "m0", "scc");
 }
 
 // s_waitcnt vmcnt(n) with expcnt / lgkmcnt left unconstrained (gfx9 encoding).
@@ -880,8 +883,8 @@ __global__ void __launch_bounds__(NW * 64, 1) gemm256_kernel(const GemmArgs p) {
   auto dma_q = [&](int kt, int slot, int q) {  // q-th load: pair q / 2, operand q % 2
     unsigned char *st = lds + slot * STAGE;
     const int i = q >> 1;
-    if (q & 1) lds_dma16(gB + (size_t)kt * BK, offB[i], st + SLICE + (wave + NW * i) * 1024);
-    else lds_dma16(gA + (size_t)kt * BK, offA[i], st + (wave + NW * i) * 1024);
+    if (q & 1) lds_dma16(gB + (size_t)kt * BK, offB[i], st + wave * 1024, SLICE + NW * i * 1024);
+    else lds_dma16(gA + (size_t)kt * BK, offA[i], st + wave * 1024, NW * i * 1024);
   };
   frag_t fa[2][4], fb[2][TN];
   const std::integral_constant<bool, true> kRd;
@@ -1123,18 +1126,18 @@ __global__ void __launch_bounds__(256, 1) gemm256h_kernel(const GemmArgs p) {
   auto dma = [&](int kt, int slot, int q) {  // q-th of the 16 loads of a stage: pair q / 2, operand q % 2
     unsigned char *st = lds + slot * STAGE;
     const int i = q >> 1;
-    if (q & 1) lds_dma16(gB + (size_t)kt * stepB, offB[i], st + SLICE + (wave + NW * i) * 1024);
-    else lds_dma16(gA + (size_t)kt * stepA, offA[i], st + (wave + NW * i) * 1024);
+    if (q & 1) lds_dma16(gB + (size_t)kt * stepB, offB[i], st + wave * 1024, SLICE + NW * i * 1024);
+    else lds_dma16(gA + (size_t)kt * stepA, offA[i], st + wave * 1024, NW * i * 1024);
   };
   // converted operand X (CV) and the other one, Y: block i of stage kt
   auto x_load = [&](int kt, int i) {  // raw, into the raw area
-    if constexpr (CVA) lds_dma16(gA + (size_t)kt * stepA, offA[i], lds + RAW_OFF + (wave + NW * i) * 1024);
-    else lds_dma16(gB + (size_t)kt * stepB, offB[i], lds + RAW_OFF + (wave + NW * i) * 1024);
+    if constexpr (CVA) lds_dma16(gA + (size_t)kt * stepA, offA[i], lds + wave * 1024, RAW_OFF + NW * i * 1024);
+    else lds_dma16(gB + (size_t)kt * stepB, offB[i], lds + wave * 1024, RAW_OFF + NW * i * 1024);
   };
   auto y_load = [&](int kt, int slot, int i) {
     unsigned char *st = lds + slot * STAGE;
-    if constexpr (CVA) lds_dma16(gB + (size_t)kt * stepB, offB[i], st + SLICE + (wave + NW * i) * 1024);
-    else lds_dma16(gA + (size_t)kt * stepA, offA[i], st + (wave + NW * i) * 1024);
+    if constexpr (CVA) lds_dma16(gB + (size_t)kt * stepB, offB[i], st + wave * 1024, SLICE + NW * i * 1024);
+    else lds_dma16(gA + (size_t)kt * stepA, offA[i], st + wave * 1024, NW * i * 1024);
   };
   // this lane's 16 raw bytes of block i, and their conversion into X's
   // slice of a slot
