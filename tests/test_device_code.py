@@ -130,9 +130,8 @@ def test_the_check_itself(lines, what):
     assert [w for _, w in hazards(code)] == what
 
 
-@pytest.mark.parametrize("source", ["nsg_kernels.hip", "nsg_select.hip", "nsg_muon.hip", "nsg_expert.hip", "nsg_fp8.hip",
-                                    "nsg_fp8_gemm.hip"])
-def test_wait_states(source, tmp_path):
+def disassembly(source, tmp_path):
+    """The functions of a source's built device code."""
     obj = os.path.join(OBJS, source + ".o")
     tools = [os.path.join(LLVM, t) for t in ("llvm-objcopy", "clang-offload-bundler", "llvm-objdump")]
     if not (os.path.exists(obj) and all(map(os.path.exists, tools))):
@@ -143,5 +142,19 @@ def test_wait_states(source, tmp_path):
     text = subprocess.run([tools[2], "-d", device], check=True, stdout=subprocess.PIPE, text=True).stdout
     functions = parse(text)
     assert sum(len(f) for f in functions) > 100
+    return functions
+
+
+@pytest.mark.parametrize("source", ["nsg_kernels.hip", "nsg_select.hip", "nsg_muon.hip", "nsg_expert.hip", "nsg_fp8.hip",
+                                    "nsg_fp8_gemm.hip"])
+def test_wait_states(source, tmp_path):
+    functions = disassembly(source, tmp_path)
     found = [(f"{a:x}", w) for f in functions for a, w in hazards(f)]
     assert not found, (len(found), found[:10])
+
+
+@pytest.mark.parametrize("source", ["nsg_expert.hip", "nsg_fp8.hip", "nsg_fp8_gemm.hip"])
+def test_no_scratch_memory(source, tmp_path):
+    """The expert layer's kernels keep what they hold in registers and LDS."""
+    names = {name for f in disassembly(source, tmp_path) for name, _, _ in f}
+    assert not [n for n in names if n.startswith("scratch_")]
