@@ -17,10 +17,12 @@
 // 128 columns).  Rows of q are padded with zeros to a multiple of 128; scales
 // are stored block index first, so that a product's tile reads consecutive ones.
 //
-// All three are bound by HBM: x read once, q (1 byte) and s (1/32 byte) written.  Measured
-// (bytes of the definition): rows 16384 x 11008 in 110 us, 5.0 TB/s; tiles with the
-// transposed copy 512 x 2048 x 512 in 403 us, 5.3 TB/s; columns 131072 x 2048 of 512
-// experts in 212 us, 3.8 TB/s (their 128-byte rows of q_t lie cap apart).
+// All three read x once and write q (1 byte) and s (1/32 byte).  Measured (bytes of the
+// definition): rows 16384 x 11008 in 110 us, 5.0 TB/s; tiles with the transposed copy
+// 512 x 2048 x 512 in 420 us, 5.1 TB/s, both at the copy rate; columns 131072 x 2048 of
+// 512 experts in 212 us, 3.8 TB/s, 32771 x 2048 of 64 in 50 us, 4.1.  What keeps the
+// columns from the copy rate is not shown; counted for the latter: 134 MB read, as by the
+// definition, and 87 written for 69 (128-byte pieces of q_t's rows, which lie cap apart).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
