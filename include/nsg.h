@@ -511,6 +511,93 @@ nsg_status_t nsg_expert_wgrad_fp8(int32_t a_dtype, int32_t b_dtype, int32_t out_
                                   const void *qb_t, const float *sb, const int32_t *offsets, void *out,
                                   void *stream);
 
+/* ---- Between token ids and the expert layer --------------------------------
+ * What a training step runs before nsg_expert_sort, and its gradients: the
+ * embedding of token ids, layer norm, and the router that gives the ids and
+ * weights of the expert layer, with its balance loss.
+ *
+ * The rules of the expert layer's section hold here too (pointers, errors, limits,
+ * reproducible results, nothing allocated, outputs that overlap no inputs).  Workspaces are
+ * aligned to 16 bytes; two calls that may overlap need two.  Sums, statistics and
+ * probabilities are fp32; each output is rounded once. */
+#define NSG_MAX_VOCAB (1 << 20)
+#define NSG_MAX_CHOICES 64
+
+/* out[t] = scale W[ids[t]] for t in [0, T), zeros for an id outside 0 .. V - 1 (a
+ * padding token's).  ids int32 or int64 by id_bits; W [V][C] (ldw) and out [T][C] of
+ * dtype F16, BF16 or F32.  V <= NSG_MAX_VOCAB; scale finite. */
+nsg_status_t nsg_embedding(const void *ids, int32_t id_bits, int64_t T, const void *W, int32_t dtype, int64_t V, int64_t C,
+                           int64_t ldw, float scale, void *out, void *stream);
+
+/* The gradient of nsg_embedding: dW[v] = scale sum of dout[t] over the tokens with
+ * ids[t] = v, in [V][C] of dw_dtype (packed).  accumulate 0: every row is written, those
+ * without tokens with zeros; 1: the sums are added to what dW holds, and rows without
+ * tokens are left alone.  dout [T][C] (lddo) of dtype.
+ *   workspace  nsg_embedding_backward_workspace_size bytes */
+nsg_status_t nsg_embedding_backward_workspace_size(int64_t T, int64_t V, int64_t C, size_t *bytes);
+nsg_status_t nsg_embedding_backward(const void *dout, int32_t dtype, int64_t T, int64_t C, int64_t lddo, const void *ids,
+                                    int32_t id_bits, int64_t V, float scale, void *dW, int32_t dw_dtype, int32_t accumulate,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm of the rows of x [R][C] (ldx):
+ *   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
+ *   y = (x - mean) rstd weight + bias
+ * y [R][C] and x of dtype; weight and bias [C] of w_dtype, or NULL (1 and 0).
+ *   stats  [2][R] fp32: the means, then the rstd, which the gradient takes
+ * eps >= 0 and finite; C = 0 with rows is NSG_ERR_SHAPE.  The variance is that of the
+ * differences from the mean, also where the mean is large beside them; their squares
+ * must not overflow fp32. */
+nsg_status_t nsg_layer_norm(const void *x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, const void *weight,
+                            const void *bias, int32_t w_dtype, float eps, void *y, float *stats, void *stream);
+
+/* The gradient of nsg_layer_norm for dy [R][C] (lddy), with xh = (x - mean) rstd and
+ * g = dy weight:
+ *   dx = rstd (g - sum g / C - xh sum (g xh) / C)     [R][C] of dtype
+ *   dweight = sum over the rows of dy xh, dbias = sum over the rows of dy
+ *                                                     [C] of w_dtype; either may be NULL
+ *   workspace  nsg_layer_norm_backward_workspace_size bytes; none is needed where both
+ *              are NULL */
+nsg_status_t nsg_layer_norm_backward_workspace_size(int64_t R, int64_t C, size_t *bytes);
+nsg_status_t nsg_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t dtype, int64_t R,
+                                     int64_t C, const float *stats, const void *weight, int32_t w_dtype, void *dx,
+                                     void *dweight, void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The router: each of T tokens chooses k of E experts by its logits l [T][E] (ld).
+ *   s = softmax(l) (NSG_SCORE_SOFTMAX) or sigmoid(l) (NSG_SCORE_SIGMOID)
+ *   ids      [T][k]: the experts of the k largest l; with a bias [E] (fp32), of the k
+ *            largest s + bias, compared in fp64.  Largest first, equal ones by index.
+ *            An expert whose logit is -inf or NaN (or whose s + bias is) is not chosen;
+ *            -1 where none is left, as nsg_expert_sort drops it.
+ *   weights  [T][k] fp32: scale s; normalize 1: scale s / sum of the token's chosen s;
+ *            0 for a choice of -1
+ *   mask     [T] bytes or NULL: a token whose byte is 0 chooses nothing
+ * With counts, probs and loss (all or none) also the balance loss.  Over the N tokens
+ * with a choice:
+ *   counts   [E + 1]: the choices of each expert, and N
+ *   probs    [E] fp32: the mean of s / sum s
+ *   loss     [1] fp32: E / (k N) sum_e counts[e] probs[e], 0 where N = 0
+ * NaN among a token's logits (with softmax +inf too) makes its probabilities NaN, with
+ * softmax its weights.  k <= min(E, NSG_MAX_CHOICES), T k <= NSG_MAX_ROWS; scale finite.
+ *   workspace  nsg_expert_route_workspace_size bytes; none is needed without the loss */
+#define NSG_SCORE_SOFTMAX 0
+#define NSG_SCORE_SIGMOID 1
+nsg_status_t nsg_expert_route_workspace_size(int64_t T, int64_t E, size_t *bytes);
+nsg_status_t nsg_expert_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, int64_t k, int32_t score,
+                              const float *bias, const uint8_t *mask, int32_t normalize, float scale, int32_t *ids,
+                              float *weights, int32_t *counts, float *probs, float *loss, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* The gradient of nsg_expert_route with respect to the logits: dlogits [T][E] of dtype,
+ * for the weights' gradient dweights [T][k] (NULL: none) and balance times that of the
+ * balance loss (counts NULL: none; *dloss times as much where dloss is not NULL).  ids
+ * and counts as nsg_expert_route gives them (the experts of a token differ); counts
+ * are constants, so where they were summed over several processes the gradient is that
+ * of the loss over all their tokens.  A token without a choice gets zeros. */
+nsg_status_t nsg_expert_route_backward(const void *logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, int64_t k,
+                                       int32_t score, int32_t normalize, float scale, const int32_t *ids,
+                                       const float *dweights, const int32_t *counts, float balance, const float *dloss,
+                                       void *dlogits, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -86,7 +86,10 @@ EXPORTS = ("ns_default_params", "ns_workspace_size", "ns_orthogonalize", "ns_sta
            "ns_muon_workspace_size", "ns_muon_step", "ns_select_count", "ns_orthogonalize_noalloc",
            "nsg_expert_sort_workspace_size", "nsg_expert_sort", "nsg_expert_dispatch", "nsg_expert_combine",
            "nsg_expert_combine_backward", "nsg_quantize_fp8", "nsg_fp8_columns", "nsg_quantize_fp8_columns",
-           "nsg_gemm_fp8_nt", "nsg_expert_gemm_fp8", "nsg_expert_wgrad_fp8")
+           "nsg_gemm_fp8_nt", "nsg_expert_gemm_fp8", "nsg_expert_wgrad_fp8",
+           "nsg_embedding", "nsg_embedding_backward_workspace_size", "nsg_embedding_backward", "nsg_layer_norm",
+           "nsg_layer_norm_backward_workspace_size", "nsg_layer_norm_backward", "nsg_expert_route_workspace_size",
+           "nsg_expert_route", "nsg_expert_route_backward")
 SELECT_ROWS, SELECT_COLS, SELECT_SMALLER = 0, 1, -1
 
 _lib = None
@@ -171,6 +174,24 @@ def lib() -> ctypes.CDLL:
     L.nsg_expert_gemm_fp8.restype = i32
     L.nsg_expert_wgrad_fp8.argtypes = [i32, i32, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
     L.nsg_expert_wgrad_fp8.restype = i32
+    L.nsg_embedding.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, f32, vp, vp]
+    L.nsg_embedding.restype = i32
+    L.nsg_embedding_backward_workspace_size.argtypes = [i64, i64, i64, psz]
+    L.nsg_embedding_backward_workspace_size.restype = i32
+    L.nsg_embedding_backward.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, f32, vp, i32, i32, vp, sz, vp]
+    L.nsg_embedding_backward.restype = i32
+    L.nsg_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp]
+    L.nsg_layer_norm.restype = i32
+    L.nsg_layer_norm_backward_workspace_size.argtypes = [i64, i64, psz]
+    L.nsg_layer_norm_backward_workspace_size.restype = i32
+    L.nsg_layer_norm_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+    L.nsg_layer_norm_backward.restype = i32
+    L.nsg_expert_route_workspace_size.argtypes = [i64, i64, psz]
+    L.nsg_expert_route_workspace_size.restype = i32
+    L.nsg_expert_route.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.nsg_expert_route.restype = i32
+    L.nsg_expert_route_backward.argtypes = [vp, i32, i64, i64, i64, i64, i32, i32, f32, vp, vp, vp, f32, vp, vp, vp]
+    L.nsg_expert_route_backward.restype = i32
     _lib = L
     return L
 
@@ -919,3 +940,254 @@ def expert_wgrad_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: t
             max(P, min(P + FP8_BLOCK - 1, 1 << 25)), E, N, K, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), offsets.data_ptr(),
             out.data_ptr())
     return out
+
+
+# ---------------------------------------------------------------------------
+# Between token ids and the expert layer: the embedding, layer norm, the router
+# with its balance loss, and their gradients
+# ---------------------------------------------------------------------------
+
+def _ids(t: torch.Tensor, name: str, device=None):
+    if t.dtype not in (torch.int32, torch.int64) or not t.is_contiguous() or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a contiguous int32 or int64 tensor on the input's device")
+
+
+def _vectors(t: torch.Tensor, name: str, lead, device=None):
+    """t [*lead, C] (lead None: any) as rows of C elements: (rows, C, pitch).  Two dimensions may
+    have a pitch, more must be contiguous."""
+    if t.dim() < 2 or t.dtype not in _DT:
+        raise ValueError(f"{name} must be a float16, bfloat16 or float32 tensor of rows")
+    if lead is not None and t.shape[:-1] != lead:
+        raise ValueError(f"{name} must have shape [{', '.join(map(str, lead))}, C]")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on the input's device")
+    C = t.shape[-1]
+    if t.dim() == 2:
+        return t.shape[0], C, _pitch(t, name) if t.numel() else C
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or a matrix with unit column stride")
+    return t.numel() // C if C else 0, C, C
+
+
+def _space(workspace: Optional[torch.Tensor], need: int, device):
+    """A workspace of `need` bytes and its size: the caller's where it is large enough."""
+    if workspace is not None:
+        check_workspace(workspace, device)
+        if nbytes(workspace) >= need:
+            return workspace.data_ptr(), nbytes(workspace), workspace
+    if not need:
+        return None, 0, None
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), need, workspace
+
+
+def _size_of(fn, what: str, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(out)), what)
+    return out.value
+
+
+def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """out[t] = scale * weight[ids[t]]: ids of any shape (int32 or int64), weight [V, C],
+    out [*ids.shape, C] of weight's dtype (fp32 products, rounded once).  An id outside
+    0 .. V - 1, such as -1 for padding, gives zeros.  V <= 2^20."""
+    device = _gpu(weight, "embedding")
+    ld = _matrix(weight, "weight")
+    _ids(ids, "ids", device)
+    V, C = weight.shape
+    out = torch.empty((*ids.shape, C), dtype=weight.dtype, device=device)
+    _launch(device, "nsg_embedding", lib().nsg_embedding, ids.data_ptr(), 8 * ids.element_size(), ids.numel(),
+            weight.data_ptr(), _DT[weight.dtype], V, C, ld, float(scale), out.data_ptr())
+    return out
+
+
+def embedding_backward_workspace_size(T: int, V: int, C: int) -> int:
+    return _size_of(lib().nsg_embedding_backward_workspace_size, "nsg_embedding_backward_workspace_size", T, V, C)
+
+
+def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, num_embeddings: int, scale: float = 1.0,
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of embedding: dW [num_embeddings, C] of dout's dtype (or `out`, of any
+    dtype), dW[v] = scale * the sum of dout[t] over the tokens with ids[t] = v; fp32 sums,
+    rounded once.  dout [*ids.shape, C].
+
+    With `accumulate` the sums are added to what `out` holds, and rows without tokens are
+    left alone.  `workspace`: a uint8 tensor of embedding_backward_workspace_size(T, V, C)
+    bytes (allocated if not given)."""
+    device = _gpu(dout, "embedding_backward")
+    _ids(ids, "ids", device)
+    T, C, ld = _vectors(dout, "dout", ids.shape)
+    V = int(num_embeddings)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is None:
+        out = torch.empty((V, C), dtype=dout.dtype, device=device)
+    elif out.shape != (V, C) or out.dtype not in _DT or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous float tensor of shape {(V, C)} on the input's device")
+    ptr, size, _keep = _space(workspace, embedding_backward_workspace_size(ids.numel(), V, C), device)
+    _launch(device, "nsg_embedding_backward", lib().nsg_embedding_backward, dout.data_ptr(), _DT[dout.dtype], ids.numel(), C, ld,
+            ids.data_ptr(), 8 * ids.element_size(), V, float(scale), out.data_ptr(), _DT[out.dtype], 1 if accumulate else 0,
+            ptr, size)
+    return out
+
+
+def _norm_weights(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], C: int, device) -> int:
+    """The dtype code of layer norm's weight and bias."""
+    dtype = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.shape != (C,) or t.dtype not in _DT or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous float tensor of shape {(C,)} on the input's device")
+        if dtype not in (None, t.dtype):
+            raise ValueError("weight and bias must have one dtype")
+        dtype = t.dtype
+    return NSG_F32 if dtype is None else _DT[dtype]
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5):
+    """Layer norm over the last dimension of x [..., C]: (y, stats) with
+    y = (x - mean) * rstd * weight + bias of x's dtype and stats [2, R] float32 the R rows'
+    means and rstd = 1 / sqrt(var + eps), which layer_norm_backward takes.  weight and
+    bias [C]: of one dtype, float32 or another; None for 1 and 0."""
+    device = _gpu(x, "layer_norm")
+    R, C, ld = _vectors(x, "x", None)
+    code = _norm_weights(weight, bias, C, device)
+    y = torch.empty(x.shape, dtype=x.dtype, device=device)
+    stats = torch.empty((2, R), dtype=torch.float32, device=device)
+    _launch(device, "nsg_layer_norm", lib().nsg_layer_norm, x.data_ptr(), _DT[x.dtype], R, C, ld,
+            weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, code, float(eps),
+            y.data_ptr(), stats.data_ptr())
+    return y, stats
+
+
+def layer_norm_backward_workspace_size(R: int, C: int) -> int:
+    return _size_of(lib().nsg_layer_norm_backward_workspace_size, "nsg_layer_norm_backward_workspace_size", R, C)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                        weight_grad: bool = True, bias_grad: bool = True, workspace: Optional[torch.Tensor] = None):
+    """The gradient of layer_norm for dy: (dx, dweight, dbias), dx of x's dtype, dweight and
+    dbias [C] of weight's (float32 without a weight), None where weight_grad or bias_grad
+    is false.  fp32 sums, rounded once.  `workspace`: a uint8 tensor of
+    layer_norm_backward_workspace_size(R, C) bytes (allocated if not given)."""
+    device = _gpu(x, "layer_norm_backward")
+    R, C, ldx = _vectors(x, "x", None)
+    lddy = _vectors(dy, "dy", x.shape[:-1], device)[2]
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and dtype")
+    if stats.shape != (2, R) or stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != device:
+        raise ValueError(f"stats must be a contiguous float32 tensor of shape {(2, R)} on the input's device")
+    code = _norm_weights(weight, None, C, device)
+    wt = torch.float32 if weight is None else weight.dtype
+    dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+    dweight = torch.empty(C, dtype=wt, device=device) if weight_grad else None
+    dbias = torch.empty(C, dtype=wt, device=device) if bias_grad else None
+    need = layer_norm_backward_workspace_size(R, C) if weight_grad or bias_grad else 0
+    ptr, size, _keep = _space(workspace, need, device)
+    _launch(device, "nsg_layer_norm_backward", lib().nsg_layer_norm_backward, dy.data_ptr(), lddy, x.data_ptr(), ldx, _DT[x.dtype],
+            R, C, stats.data_ptr(), weight.data_ptr() if weight is not None else None, code, dx.data_ptr(),
+            dweight.data_ptr() if weight_grad else None, dbias.data_ptr() if bias_grad else None, ptr, size)
+    return dx, dweight, dbias
+
+
+class Routing(NamedTuple):
+    """What expert_route decides.
+
+    ids [T, k] int32, largest first, -1 for none (expert_sort drops it); weights [T, k]
+    float32.  With the balance loss: counts [E + 1] int32, the choices of each expert
+    and the number of tokens with a choice; probs [E] float32, the mean over these tokens
+    of their probabilities; loss, a float32 scalar."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    counts: Optional[torch.Tensor]
+    probs: Optional[torch.Tensor]
+    loss: Optional[torch.Tensor]
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score_code(score) -> int:
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return _SCORES[score]
+
+
+def expert_route_workspace_size(T: int, num_experts: int) -> int:
+    return _size_of(lib().nsg_expert_route_workspace_size, "nsg_expert_route_workspace_size", T, num_experts)
+
+
+def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 mask: Optional[torch.Tensor] = None, normalize: bool = True, scale: float = 1.0, balance: bool = False,
+                 workspace: Optional[torch.Tensor] = None) -> Routing:
+    """Each token's k experts and their weights, from logits [T, E].
+
+    s = softmax(logits) or sigmoid(logits).  The k largest logits are chosen, with `bias`
+    (float32 [E]) the k largest s + bias, compared in 64 bits; equal ones go to the lower
+    index.  weights = scale * s, with `normalize` divided by the sum of the token's chosen
+    s.  A logit of -inf or NaN is never chosen and a token whose `mask` (bool [T]) is
+    False chooses nothing: ids -1, weights 0.
+
+    With `balance` also counts, probs and loss = E / (k N) * sum(counts * probs) over the
+    N tokens with a choice (see Routing).  `workspace`, for the loss: a uint8 tensor of
+    expert_route_workspace_size(T, E) bytes (allocated if not given).  k <= 64, E <= 1024."""
+    device = _gpu(logits, "expert_route")
+    ld = _matrix(logits, "logits")
+    code = _score_code(score)
+    T, E = logits.shape
+    k = int(k)
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous() or bias.device != device):
+        raise ValueError("bias must be a contiguous float32 [E] tensor on the input's device")
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,) or not mask.is_contiguous()
+                             or mask.device != device):
+        raise ValueError("mask must be a contiguous bool [T] tensor on the input's device")
+    if not 1 <= k <= min(E, 64):
+        raise ValueError("k must lie in 1 .. min(E, 64)")
+    ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    counts = probs = loss = ptr = None
+    size = 0
+    if balance:
+        counts = torch.empty(E + 1, dtype=torch.int32, device=device)
+        probs = torch.empty(E, dtype=torch.float32, device=device)
+        loss = torch.empty((), dtype=torch.float32, device=device)
+        ptr, size, _keep = _space(workspace, expert_route_workspace_size(T, E), device)
+    _launch(device, "nsg_expert_route", lib().nsg_expert_route, logits.data_ptr(), _DT[logits.dtype], T, E, ld, k, code,
+            bias.data_ptr() if bias is not None else None, mask.data_ptr() if mask is not None else None,
+            1 if normalize else 0, float(scale), ids.data_ptr(), weights.data_ptr(), counts.data_ptr() if balance else None,
+            probs.data_ptr() if balance else None, loss.data_ptr() if balance else None, ptr, size)
+    return Routing(ids, weights, counts, probs, loss)
+
+
+def expert_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: Optional[torch.Tensor] = None,
+                          score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                          counts: Optional[torch.Tensor] = None, balance: float = 1.0,
+                          dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of expert_route with respect to the logits, of their dtype [T, E].
+
+    ids as expert_route gave them; dweights [T, k] float32 is the weights' gradient.  With
+    counts (of expert_route, or their sum over several processes) the balance loss's is
+    added: `balance` times it, times dloss where that (a float32 scalar) is given.
+    counts are constants.  A token without a choice gets zeros."""
+    device = _gpu(logits, "expert_route_backward")
+    ld = _matrix(logits, "logits")
+    code = _score_code(score)
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be [T, k]")
+    _ints(ids, None, "ids", device)
+    if dweights is not None and (dweights.dtype != torch.float32 or dweights.shape != ids.shape or not dweights.is_contiguous()
+                                 or dweights.device != device):
+        raise ValueError("dweights must be a contiguous float32 [T, k] tensor on the input's device")
+    if counts is not None:
+        _ints(counts, (E + 1,), "counts", device)
+    if dloss is not None and (counts is None or dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != device):
+        raise ValueError("dloss must be a float32 scalar on the input's device, with counts")
+    dlogits = torch.empty((T, E), dtype=logits.dtype, device=device)
+    _launch(device, "nsg_expert_route_backward", lib().nsg_expert_route_backward, logits.data_ptr(), _DT[logits.dtype], T, E, ld,
+            ids.shape[1], code, 1 if normalize else 0, float(scale), ids.data_ptr(),
+            dweights.data_ptr() if dweights is not None else None, counts.data_ptr() if counts is not None else None,
+            float(balance), dloss.data_ptr() if dloss is not None else None, dlogits.data_ptr())
+    return dlogits

@@ -1,0 +1,526 @@
+// Embedding of token ids and its gradient, on gfx950.
+//
+//   forward   out[t] = scale W[ids[t]], zeros for an id outside 0 .. V - 1
+//   gradient  dW[v] = scale sum of dout[t] over the tokens with ids[t] = v
+//
+// Both are streaming passes, bound by HBM.  The gradient sorts the tokens by id
+// (stably, in one or two digits) and sums the runs of equal ids.  The sorted list is
+// cut into chunks of a length that only the sizes fix; what a run has inside one
+// chunk is summed in token order, and a run over several chunks is joined from their
+// sums, in order.  No atomics on memory: every result is reproducible bit for bit.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "nsg_layer.h"
+#include "nsg_rows.h"
+#include "nsg_segments.h"
+
+namespace nsg {
+
+// ---------------------------------------------------------------------------
+// forward: one wave per 64 x 16 bytes of a token (a part); four waves of a workgroup
+// take 1 << lp parts of 4 >> lp tokens.
+// ---------------------------------------------------------------------------
+struct EmbedParts {
+  int64_t t, part;
+  __device__ __forceinline__ explicit EmbedParts(int lp) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    t = (int64_t)blockIdx.x * (4 >> lp) + (wave >> lp);
+    part = ((int64_t)blockIdx.y << lp) + (wave & ((1 << lp) - 1));
+  }
+};
+// (HIP counts a launch's threads in 32 bits)
+static int parts_log(int64_t rows, int64_t parts) { return rows > (1 << 23) || parts < 2 ? 0 : parts < 4 ? 1 : 2; }
+static dim3 parts_grid(int64_t rows, int64_t parts, int lp) {
+  return dim3((unsigned)((rows + (4 >> lp) - 1) / (4 >> lp)), (unsigned)((parts + (1 << lp) - 1) >> lp));
+}
+
+// id i, or -1 where it is none of 0 .. V - 1
+__device__ __forceinline__ int id_at(const void *ids, int wide, int64_t i, int64_t V) {
+  const int64_t v = wide ? reinterpret_cast<const int64_t *>(ids)[i] : reinterpret_cast<const int32_t *>(ids)[i];
+  return v >= 0 && v < V ? (int)v : -1;
+}
+
+template <typename T, int ALIGN>
+__global__ void __launch_bounds__(256) embedding_kernel(const void *__restrict__ ids, int wide, int64_t ntok,
+                                                        const T *__restrict__ W, int64_t V, int64_t C, int64_t ldw,
+                                                        float scale, int lp, T *__restrict__ out) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const EmbedParts at(lp);
+  const int64_t t = at.t, c = (at.part * 64 + (threadIdx.x & 63)) * N;
+  if (t >= ntok || c >= C) return;
+  const int v = id_at(ids, wide, t, V);
+  const T *from = W + (int64_t)v * ldw;
+  T *to = out + t * C;
+  if (c + N <= C) {
+    float f[N];
+    if (v >= 0) Row<T, N, ALIGN>::load(from + c, f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = v >= 0 ? f[i] * scale : 0.f;
+    Row<T, N, ALIGN>::store(to + c, f);
+  } else {
+    for (int64_t i = c; i < C; ++i) to[i] = (T)(v >= 0 ? (float)from[i] * scale : 0.f);
+  }
+}
+
+template <typename T> static hipError_t embedding_t(const EmbedArgs &a, hipStream_t s) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const int64_t parts = (a.C + 64 * N - 1) / (64 * N);
+  const int lp = parts_log(a.T, parts);
+  const dim3 grid = parts_grid(a.T, parts, lp);
+  if (aligned16(a.x) && aligned16(a.out) && a.C % N == 0 && a.ld % N == 0)
+    hipLaunchKernelGGL((embedding_kernel<T, 16>), grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V, a.C, a.ld,
+                       a.scale, lp, (T *)a.out);
+  else
+    hipLaunchKernelGGL((embedding_kernel<T, (int)sizeof(T)>), grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V,
+                       a.C, a.ld, a.scale, lp, (T *)a.out);
+  return hipGetLastError();
+}
+
+hipError_t launch_embedding(const EmbedArgs &a, hipStream_t s) {
+  switch (a.x_dtype) {
+    case NSG_F16: return embedding_t<_Float16>(a, s);
+    case NSG_BF16: return embedding_t<__bf16>(a, s);
+    default: return embedding_t<float>(a, s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the gradient's sort: a stable counting sort of the tokens by their id, by its low
+// digit and then by its high one (ids of up to 10 bits: one digit).  Tokens without an
+// id are left out: keys behind the last token that has one are -1.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortBins = 1024;
+constexpr int kSortKept = 4;                           // steps of 64 tokens that a wave keeps in registers
+constexpr int kSortChunk = kSortThreads * kSortKept;   // tokens of one workgroup, then
+constexpr int kSortMaxChunks = 128;                    // every workgroup reads the whole table
+constexpr int kSortAlone = 16;                         // steps of a sort by one workgroup
+static_assert(NSG_MAX_VOCAB <= kSortBins * kSortBins, "two digits");
+
+struct SortPlan {
+  int64_t chunk;
+  int chunks, digits, bits;  // bits of a digit
+};
+static SortPlan sort_plan(int64_t N, int64_t V) {
+  SortPlan p;
+  p.chunk = N;
+  if (N > kSortThreads * kSortAlone) {
+    p.chunk = (N + 63) / 64;
+    if (p.chunk > kSortChunk) p.chunk = kSortChunk;
+    const int64_t least = (N + kSortMaxChunks - 1) / kSortMaxChunks;
+    if (p.chunk < least) p.chunk = least;
+  }
+  p.chunk = (p.chunk + kSortThreads - 1) / kSortThreads * kSortThreads;
+  p.chunks = N == 0 ? 1 : (int)((N + p.chunk - 1) / p.chunk);
+  int bits = 1;
+  while ((1ll << bits) < V) ++bits;
+  p.digits = bits <= 10 ? 1 : 2;
+  p.bits = (bits + p.digits - 1) / p.digits;
+  return p;
+}
+
+// the tokens before a digit's pass: the ids as they are, or the pairs of the pass before
+struct SortInput {
+  const void *ids;
+  int wide;
+  int64_t V;
+  const int32_t *keys, *toks;  // NULL: ids
+  __device__ __forceinline__ int key(int64_t i) const { return keys ? keys[i] : id_at(ids, wide, i, V); }
+  __device__ __forceinline__ int tok(int64_t i) const { return keys ? toks[i] : (int)i; }
+};
+
+// tokens of each value of the digit in each chunk
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(SortInput in, int64_t N, int64_t chunk, int shift, int bits,
+                                                                   int32_t *__restrict__ table) {
+  __shared__ int count[kSortBins];
+  const int bins = 1 << bits;
+  for (int e = threadIdx.x; e < bins; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min(N, i0 + chunk);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
+    const int k = in.key(i);
+    if (k >= 0) atomicAdd(&count[(k >> shift) & (bins - 1)], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < bins; e += kSortThreads) table[(size_t)blockIdx.x * bins + e] = count[e];
+}
+
+// Place the tokens of chunk `block`.  at[w][d]: where the next token with digit d in
+// wave w's part of the chunk goes.  A wave takes its part 64 tokens at a time: the
+// lanes with the same digit find each other by ballots over its bits, so their order
+// is that of the tokens.  KEPT: steps of 64 tokens a wave keeps, 0: it reads them again.
+template <int KEPT>
+__device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int64_t chunk, int chunks, int block, int shift,
+                                            int bits, const int32_t *__restrict__ table, int *at, int *sh,
+                                            int32_t *__restrict__ keys, int32_t *__restrict__ toks) {
+  const int bins = 1 << bits;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i0 = (int64_t)block * chunk, i1 = min(N, i0 + chunk);
+  const int64_t part = chunk / kSortWaves;  // a multiple of 64, with KEPT at most KEPT 64
+  const int64_t w0 = i0 + wave * part, w1 = min(i1, w0 + part);
+  int kept[KEPT > 0 ? KEPT : 1], kept_tok[KEPT > 0 ? KEPT : 1];
+  if (KEPT > 0) {
+#pragma unroll
+    for (int u = 0; u < KEPT; ++u) {
+      const int64_t p = w0 + u * 64 + lane;  // (w1: also the end of the wave's part)
+      kept[u] = p < w1 ? in.key(p) : -1;
+      kept_tok[u] = p < w1 ? in.tok(p) : 0;
+    }
+  }
+  for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) at[i] = 0;
+  __syncthreads();
+  if (KEPT > 0) {
+#pragma unroll
+    for (int u = 0; u < KEPT; ++u)
+      if (kept[u] >= 0) atomicAdd(&at[wave * bins + ((kept[u] >> shift) & (bins - 1))], 1);
+  } else {
+    for (int64_t i = w0 + lane; i < w1; i += 64) {
+      const int k = in.key(i);
+      if (k >= 0) atomicAdd(&at[wave * bins + ((k >> shift) & (bins - 1))], 1);
+    }
+  }
+  __syncthreads();
+  // thread e: all tokens with digit e, and those before this chunk
+  const int e = threadIdx.x;
+  int total = 0, before = 0;
+  if (e < bins) {
+    if (chunks == 1) {
+      for (int w = 0; w < kSortWaves; ++w) total += at[w * bins + e];
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const int n = table[(size_t)c * bins + e];
+        total += n;
+        before += c < block ? n : 0;
+      }
+    }
+  }
+  int all;
+  const int first = block_before<kSortThreads>(total, sh, all);
+  if (e < bins) {
+    int next = first + before;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = at[w * bins + e];
+      at[w * bins + e] = next;
+      next += n;
+    }
+  }
+  __syncthreads();
+  volatile int *mine = at + wave * bins;
+  auto place = [&](int key, int tok) {
+    const int d = (key >> shift) & (bins - 1);
+    uint64_t same = __ballot(key >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot((d >> b) & 1);
+      same &= (d >> b) & 1 ? one : ~one;
+    }
+    if (key >= 0) {
+      const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
+      const int base = mine[d];
+      __builtin_amdgcn_wave_barrier();
+      if (rank == n - 1) mine[d] = base + n;
+      keys[base + rank] = key;
+      toks[base + rank] = tok;
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  if (KEPT > 0) {
+#pragma unroll
+    for (int u = 0; u < KEPT; ++u)
+      if (w0 + u * 64 < w1) place(kept[u], kept_tok[u]);
+  } else {
+    for (int64_t i = w0; i < w1; i += 64) {
+      const bool there = i + lane < w1;
+      place(there ? in.key(i + lane) : -1, there ? in.tok(i + lane) : 0);
+    }
+  }
+  for (int64_t p = i0 + threadIdx.x; p < i1; p += kSortThreads)
+    if (p >= all) keys[p] = -1;
+}
+
+template <int KEPT>
+__global__ void __launch_bounds__(kSortThreads) embed_place_kernel(SortInput in, int64_t N, int64_t chunk, int chunks, int shift,
+                                                                   int bits, const int32_t *__restrict__ table,
+                                                                   int32_t *__restrict__ keys, int32_t *__restrict__ toks) {
+  __shared__ int at[kSortWaves * kSortBins];
+  __shared__ int sh[kSortWaves + 1];
+  place_chunk<KEPT>(in, N, chunk, chunks, (int)blockIdx.x, shift, bits, table, at, sh, keys, toks);
+}
+
+// all digits by one workgroup
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortInput in, int64_t N, int64_t chunk, int digits, int bits,
+                                                                  int32_t *keys1, int32_t *toks1, int32_t *keys, int32_t *toks) {
+  __shared__ int at[kSortWaves * kSortBins];
+  __shared__ int sh[kSortWaves + 1];
+  if (digits == 2) {
+    place_chunk<kSortAlone>(in, N, chunk, 1, 0, 0, bits, nullptr, at, sh, keys1, toks1);
+    __syncthreads();
+    in.keys = keys1;
+    in.toks = toks1;
+  }
+  place_chunk<kSortAlone>(in, N, chunk, 1, 0, (digits - 1) * bits, bits, nullptr, at, sh, keys, toks);
+}
+
+// ---------------------------------------------------------------------------
+// the gradient's sums
+// ---------------------------------------------------------------------------
+constexpr int kRunUnroll = 8;
+
+// Sorted tokens of a chunk: enough waves (a chunk's 64 x 16 bytes each) to fill the
+// chip, at least one round of loads, and few sums of parts of runs.
+static int64_t run_chunk(int64_t N, int64_t C) {
+  const int64_t parts = (C + 511) / 512;
+  int64_t S = kRunUnroll;
+  while (S < 64 && N / (2 * S) * parts >= 8192) S *= 2;
+  return S;
+}
+static int64_t run_chunks(int64_t N, int64_t C) { return (N + run_chunk(N, C) - 1) / run_chunk(N, C); }
+
+// where the sums of parts of runs lie: two rows of fp32 for each chunk, what its first
+// run has here if it began before, and what its last one has if it began here and goes on
+static int64_t part_pitch(int64_t C) { return (C + 3) / 4 * 4; }
+
+// a chunk's runs; every value is the same in all lanes
+struct Chunk {
+  int64_t p0, p1;
+  bool before, after;  // the first run began in an earlier chunk; the last one goes on
+  __device__ __forceinline__ Chunk(const int32_t *keys, int64_t N, int64_t S, int64_t c) {
+    p0 = c * S;
+    p1 = min(N, p0 + S);
+    before = p0 > 0 && keys[p0] >= 0 && keys[p0 - 1] == keys[p0];
+    after = p1 < N && keys[p1] >= 0 && keys[p1] == keys[p1 - 1];
+  }
+};
+
+template <typename T, int N> __device__ __forceinline__ void add_row(T *p, int64_t c, int64_t C, const float (&f)[N], bool add) {
+  if (c + N <= C) {
+    float g[N];
+    if (add) {
+      Row<T, N, (int)sizeof(T)>::load(p + c, g);
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] += f[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = f[i];
+    }
+    Row<T, N, (int)sizeof(T)>::store(p + c, g);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < C) p[c + i] = (T)(add ? (float)p[c + i] + f[i] : f[i]);
+  }
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restrict__ keys, const int32_t *__restrict__ toks,
+                                                         int64_t ntok, int64_t S, int64_t chunks, const T *__restrict__ dout,
+                                                         int64_t ld, int64_t C, float scale, int add, int lp,
+                                                         O *__restrict__ out, float *__restrict__ parts, int64_t pitch) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const EmbedParts at(lp);
+  const int64_t c = (at.part * 64 + (threadIdx.x & 63)) * N;
+  if (at.t >= chunks || c >= C) return;
+  const Chunk ch(keys, ntok, S, at.t);
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  int run = keys[ch.p0];
+  bool began = ch.before;  // the present run began in an earlier chunk
+  if (run < 0) return;     // keys of -1 are the last ones
+  const bool full = c + N <= C;
+  auto close = [&](bool goes_on) {
+    if (began || goes_on) {
+      float *p = parts + (at.t * 2 + (began ? 0 : 1)) * pitch;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (c + i < C) p[c + i] = acc[i];
+    } else {
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = acc[i] * scale;
+      add_row<O, N>(out + (int64_t)run * C, c, C, f, add);
+    }
+  };
+  for (int64_t p = ch.p0; p < ch.p1; p += kRunUnroll) {
+    int key[kRunUnroll];
+    float f[kRunUnroll][N];
+#pragma unroll
+    for (int u = 0; u < kRunUnroll; ++u) {
+      key[u] = p + u < ch.p1 ? keys[p + u] : -1;
+      if (key[u] >= 0) {
+        const T *row = dout + (int64_t)toks[p + u] * ld;
+        if (full) {
+          Row<T, N, (int)sizeof(T)>::load(row + c, f[u]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[u][i] = c + i < C ? (float)row[c + i] : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRunUnroll; ++u) {
+      if (key[u] < 0) continue;
+      if (key[u] != run) {
+        close(false);
+        run = key[u];
+        began = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += f[u][i];
+    }
+  }
+  close(ch.after);
+}
+
+// The run that begins in chunk t and goes on: its parts in the order of the chunks.
+template <typename O>
+__global__ void __launch_bounds__(256) embed_join_kernel(const int32_t *__restrict__ keys, int64_t ntok, int64_t S,
+                                                         int64_t chunks, int64_t C, float scale, int add, int lp,
+                                                         O *__restrict__ out, const float *__restrict__ parts, int64_t pitch) {
+  const EmbedParts at(lp);
+  const int lane = threadIdx.x & 63;
+  const int64_t c = (at.part * 64 + lane) * 4;
+  if (at.t >= chunks) return;
+  const Chunk ch(keys, ntok, S, at.t);
+  const int run = keys[ch.p1 - 1];
+  if (!ch.after || (ch.before && keys[ch.p0] == run)) return;
+  // chunks that the run goes on in
+  int64_t more = 0;
+  for (;;) {
+    const int64_t q = (at.t + 1 + more + lane) * S;
+    const uint64_t on = __ballot(q < ntok && keys[q < ntok ? q : 0] == run);
+    if (on != ~0ull) {
+      more += __ffsll((long long)~on) - 1;
+      break;
+    }
+    more += 64;
+  }
+  if (c >= C) return;
+  float acc[4];
+  Row<float, 4>::load(parts + (at.t * 2 + 1) * pitch + c, acc);
+#pragma unroll 8
+  for (int64_t i = 1; i <= more; ++i) {
+    float f[4];
+    Row<float, 4>::load(parts + (at.t + i) * 2 * pitch + c, f);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += f[v];
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] *= scale;
+  add_row<O, 4>(out + (int64_t)run * C, c, C, acc, add);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// n units of 16 bytes from a 16-byte boundary, and the bytes before and behind them in twos
+__global__ void __launch_bounds__(256) embed_clear_kernel(uint16_t *__restrict__ head, int64_t nhead, u32x4 *__restrict__ mid,
+                                                          int64_t n, uint16_t *__restrict__ tail, int64_t ntail) {
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = i0; i < n; i += step) __builtin_nontemporal_store(u32x4(0), mid + i);
+  if (i0 < nhead) head[i0] = 0;
+  if (i0 < ntail) tail[i0] = 0;
+}
+
+static hipError_t clear(void *p, int64_t bytes, hipStream_t s) {
+  char *b = (char *)p;
+  int64_t head = (16 - reinterpret_cast<uintptr_t>(p) % 16) % 16;
+  if (head > bytes) head = bytes;
+  const int64_t n = (bytes - head) / 16;
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 4096) blocks = 4096;
+  if (blocks < 1) blocks = 1;
+  hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (uint16_t *)b, head / 2, (u32x4 *)(b + head), n,
+                     (uint16_t *)(b + head + n * 16), (bytes - head - n * 16) / 2);
+  return hipGetLastError();
+}
+
+// Two lists of pairs, the sort's table, the sums of parts of runs
+struct EmbedSpace {
+  size_t keys1, toks1, keys, toks, table, parts, bytes;
+  EmbedSpace(int64_t T, int64_t V, int64_t C) {
+    const SortPlan p = sort_plan(T, V);
+    const size_t list = ((size_t)T * 4 + 15) / 16 * 16;
+    keys1 = 0;
+    toks1 = keys1 + list;
+    keys = toks1 + list;
+    toks = keys + list;
+    table = toks + list;
+    parts = table + (p.chunks > 1 ? (size_t)p.chunks * (size_t)(4 << p.bits) : 0);
+    parts = (parts + 15) / 16 * 16;
+    bytes = parts + (size_t)run_chunks(T, C) * 2 * (size_t)part_pitch(C) * 4;
+  }
+};
+size_t embedding_backward_workspace(int64_t T, int64_t V, int64_t C) { return T == 0 || C == 0 ? 0 : EmbedSpace(T, V, C).bytes; }
+
+template <typename T, typename O> static hipError_t runs_to(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {
+  constexpr int N = 16 / (int)sizeof(T);
+  char *ws = (char *)a.workspace;
+  const int32_t *keys = (const int32_t *)(ws + sp.keys), *toks = (const int32_t *)(ws + sp.toks);
+  float *parts = (float *)(ws + sp.parts);
+  const int64_t S = run_chunk(a.T, a.C), chunks = run_chunks(a.T, a.C), pitch = part_pitch(a.C);
+  int64_t n = (a.C + 64 * N - 1) / (64 * N);
+  int lp = parts_log(chunks, n);
+  hipLaunchKernelGGL((embed_runs_kernel<T, O>), parts_grid(chunks, n, lp), dim3(256), 0, s, keys, toks, a.T, S, chunks,
+                     (const T *)a.x, a.ld, a.C, a.scale, a.accumulate, lp, (O *)a.out, parts, pitch);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || chunks < 2) return e;
+  n = (a.C + 255) / 256;
+  lp = parts_log(chunks, n);
+  hipLaunchKernelGGL((embed_join_kernel<O>), parts_grid(chunks, n, lp), dim3(256), 0, s, keys, a.T, S, chunks, a.C, a.scale,
+                     a.accumulate, lp, (O *)a.out, parts, pitch);
+  return hipGetLastError();
+}
+template <typename T> static hipError_t runs_t(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {
+  switch (a.out_dtype) {
+    case NSG_F16: return runs_to<T, _Float16>(a, sp, s);
+    case NSG_BF16: return runs_to<T, __bf16>(a, sp, s);
+    default: return runs_to<T, float>(a, sp, s);
+  }
+}
+
+hipError_t launch_embedding_backward(const EmbedArgs &a, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (!a.accumulate) e = clear(a.out, a.V * a.C * (a.out_dtype == NSG_F32 ? 4 : 2), s);
+  if (e != hipSuccess || a.T == 0) return e;
+  const EmbedSpace sp(a.T, a.V, a.C);
+  const SortPlan p = sort_plan(a.T, a.V);
+  char *ws = (char *)a.workspace;
+  int32_t *keys1 = (int32_t *)(ws + sp.keys1), *toks1 = (int32_t *)(ws + sp.toks1);
+  int32_t *keys = (int32_t *)(ws + sp.keys), *toks = (int32_t *)(ws + sp.toks), *table = (int32_t *)(ws + sp.table);
+  SortInput in{a.ids, a.wide, a.V, nullptr, nullptr};
+  if (p.chunks == 1) {
+    hipLaunchKernelGGL(embed_sort_kernel, dim3(1), dim3(kSortThreads), 0, s, in, a.T, p.chunk, p.digits, p.bits, keys1, toks1, keys, toks);
+    e = hipGetLastError();
+  } else {
+    for (int d = 0; d < p.digits && e == hipSuccess; ++d) {
+      const bool last = d == p.digits - 1;
+      int32_t *k = last ? keys : keys1, *t = last ? toks : toks1;
+      hipLaunchKernelGGL(embed_count_kernel, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk, d * p.bits,
+                         p.bits, table);
+      e = hipGetLastError();
+      if (e != hipSuccess) break;
+      if (p.chunk <= kSortChunk)
+        hipLaunchKernelGGL(embed_place_kernel<kSortKept>, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
+                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t);
+      else
+        hipLaunchKernelGGL(embed_place_kernel<0>, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
+                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t);
+      e = hipGetLastError();
+      in.keys = keys1;
+      in.toks = toks1;
+    }
+  }
+  if (e != hipSuccess) return e;
+  switch (a.x_dtype) {
+    case NSG_F16: return runs_t<_Float16>(a, sp, s);
+    case NSG_BF16: return runs_t<__bf16>(a, sp, s);
+    default: return runs_t<float>(a, sp, s);
+  }
+}
+
+}  // namespace nsg

@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "nsg_expert.h"
+#include "nsg_rows.h"
 #include "nsg_segments.h"
 
 namespace nsg {
@@ -247,8 +248,6 @@ __global__ void __launch_bounds__(256) expert_dispatch_kernel(const V *__restric
   }
 }
 
-static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 template <typename V>
 static hipError_t dispatch_t(const void *x, int64_t T, int64_t n, int64_t ldx, const int32_t *offsets, int E,
                              const int32_t *rows, int k, void *out, hipStream_t s) {
@@ -277,27 +276,6 @@ hipError_t launch_expert_dispatch(const void *x, int elem, int64_t T, int64_t C,
 // combine and its gradient.  A lane owns V consecutive elements of a row: 16
 // bytes of them, or one element where rows do not take 16-byte accesses.
 // ---------------------------------------------------------------------------
-// ALIGN: bytes that the elements are aligned to (the instructions take any).
-template <typename T, int V, int ALIGN = V * (int)sizeof(T)> struct Row {
-  typedef T vec __attribute__((ext_vector_type(V)));
-  typedef vec mem __attribute__((aligned(ALIGN)));
-  static __device__ __forceinline__ void load(const T *p, float (&f)[V]) {
-    const vec x = *reinterpret_cast<const mem *>(p);
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = (float)x[v];
-  }
-  static __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
-    vec x;
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = (T)f[v];
-    *reinterpret_cast<mem *>(p) = x;
-  }
-};
-template <typename T, int ALIGN> struct Row<T, 1, ALIGN> {
-  static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = (float)*p; }
-  static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = (T)f[0]; }
-};
-
 // One wave per 64 V elements of a token (a part).
 template <typename T, int V>
 __global__ void __launch_bounds__(256) expert_combine_kernel(const T *__restrict__ y, int64_t P, int64_t C, int64_t ldy,
