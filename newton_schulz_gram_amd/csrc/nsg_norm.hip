@@ -18,12 +18,31 @@ namespace nsg {
 
 // ---------------------------------------------------------------------------
 // A row belongs to WR waves; lane l of them has the NV pieces of 16 bytes
-// (j WR 64 + l) of it.
+// (j WR 64 + l) of it: at most 16 elements, rows of up to 16384.
 // ---------------------------------------------------------------------------
 template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
+constexpr int kNormLane = 16;    // elements of a lane
+constexpr int kNormWaves = 16;   // waves of a row at most
+constexpr int kNormRegisters = kNormLane * kNormWaves * 64;  // elements of a row in registers
 
-// N consecutive elements of a row from c on, zeros behind its end
-template <typename T, int N> __device__ __forceinline__ void load_piece(const T *row, int64_t c, int64_t C, float (&f)[N]) {
+// 16 bytes of a row from element c on, zeros behind its end
+template <typename T> struct Piece {
+  static constexpr int N = kPiece<T>;
+  typedef T vec __attribute__((ext_vector_type(N)));
+  typedef vec mem __attribute__((aligned(sizeof(T))));
+  vec v;
+  __device__ __forceinline__ void load(const T *row, int c, int C) {
+    if (c + N <= C) {
+      v = *reinterpret_cast<const mem *>(row + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = c + i < C ? row[c + i] : (T)0.f;
+    }
+  }
+};
+
+// N consecutive elements of a row from c on as fp32, zeros behind its end
+template <typename T, int N> __device__ __forceinline__ void load_piece(const T *row, int c, int C, float (&f)[N]) {
   if (c + N <= C) {
     Row<T, N, (int)sizeof(T)>::load(row + c, f);
   } else {
@@ -31,7 +50,7 @@ template <typename T, int N> __device__ __forceinline__ void load_piece(const T 
     for (int i = 0; i < N; ++i) f[i] = c + i < C ? (float)row[c + i] : 0.f;
   }
 }
-template <typename T, int N> __device__ __forceinline__ void store_piece(T *row, int64_t c, int64_t C, const float (&f)[N]) {
+template <typename T, int N> __device__ __forceinline__ void store_piece(T *row, int c, int C, const float (&f)[N]) {
   if (c + N <= C) {
     Row<T, N, (int)sizeof(T)>::store(row + c, f);
   } else {
@@ -40,30 +59,24 @@ template <typename T, int N> __device__ __forceinline__ void store_piece(T *row,
       if (c + i < C) row[c + i] = (T)f[i];
   }
 }
-// the same of weights of any type (`dtype` is the same in all lanes)
-template <int N> __device__ __forceinline__ void load_weights(const void *w, int dtype, int64_t c, int64_t C, float (&f)[N]) {
-  if (dtype == NSG_F32) load_piece<float, N>((const float *)w, c, C, f);
-  else if (dtype == NSG_BF16) load_piece<__bf16, N>((const __bf16 *)w, c, C, f);
-  else load_piece<_Float16, N>((const _Float16 *)w, c, C, f);
+// weights of any type (`dtype` is the same in all lanes), `none` where there are none
+template <int N>
+__device__ __forceinline__ void load_weights(const void *w, int dtype, int c, int C, float none, float (&f)[N]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = none;
+  } else if (dtype == NSG_F32) {
+    load_piece<float, N>((const float *)w, c, C, f);
+  } else if (dtype == NSG_BF16) {
+    load_piece<__bf16, N>((const __bf16 *)w, c, C, f);
+  } else {
+    load_piece<_Float16, N>((const _Float16 *)w, c, C, f);
+  }
 }
 __device__ __forceinline__ void store_weight(void *w, int dtype, int64_t c, float v) {
   if (dtype == NSG_F32) ((float *)w)[c] = v;
   else if (dtype == NSG_BF16) ((__bf16 *)w)[c] = (__bf16)v;
   else ((_Float16 *)w)[c] = (_Float16)v;
-}
-
-// f weight + bias, where there are any (w: room)
-template <int N> __device__ __forceinline__ void weigh(const NormArgs &p, int64_t c, float (&f)[N], float (&w)[N]) {
-  if (p.weight != nullptr) {
-    load_weights<N>(p.weight, p.w_dtype, c, p.C, w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] *= w[i];
-  }
-  if (p.bias != nullptr) {
-    load_weights<N>(p.bias, p.w_dtype, c, p.C, w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] += w[i];
-  }
 }
 
 // 1 / sqrt(var + eps) for the mean square m2 of differences whose mean is `rest` (a NaN stays one)
@@ -75,11 +88,8 @@ __device__ __forceinline__ float row_rstd(float m2, float rest, float eps) {
 // Sums of a and b over the WR waves of a row, the same in all their lanes.  `sh`:
 // a pair for each wave of the workgroup, not in use by an earlier sum.
 template <int WR> __device__ __forceinline__ void row_sum(float &a, float &b, float (*sh)[2]) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off, 64);
-    b += __shfl_xor(b, off, 64);
-  }
+  a = wave_sum(a);
+  b = wave_sum(b);
   if (WR == 1) return;
   const int wave = threadIdx.x >> 6, first = wave / WR * WR;
   if ((threadIdx.x & 63) == 0) {
@@ -95,105 +105,172 @@ template <int WR> __device__ __forceinline__ void row_sum(float &a, float &b, fl
   }
 }
 
+// A workgroup takes WAVES / WR rows at a time and keeps the weights; the next rows are
+// on their way while it works.
 template <typename T, int WAVES, int WR, int NV>
 __global__ void __launch_bounds__(WAVES * 64) layer_norm_kernel(NormArgs p) {
-  constexpr int N = kPiece<T>;
+  constexpr int N = kPiece<T>, kRows = WAVES / WR;
   __shared__ float sh[2][WAVES][2];
-  const int wave = threadIdx.x >> 6;
-  for (int64_t r0 = (int64_t)blockIdx.x * (WAVES / WR); r0 < p.R; r0 += (int64_t)gridDim.x * (WAVES / WR)) {
-  const int64_t r = r0 + wave / WR;
-  const bool there = r < p.R;
-  const T *x = (const T *)p.x + (there ? r : 0) * p.ldx;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = (wave % WR) * 64 + (threadIdx.x & 63);
-  float f[NV][N], a = 0.f, b = 0.f;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + wave / WR;
+  Piece<T> x[NV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) load_piece<T, N>(x, (int64_t)(j * WR * 64 + l) * N, p.C, f[j]);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < N; ++i) a += f[j][i];
-  row_sum<WR>(a, b, sh[0]);
-  const float n = (float)p.C;
-  float mean = a / n;
-  a = b = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = (j * WR * 64 + l) * N + i < p.C ? f[j][i] - mean : 0.f;
-      f[j][i] = d;
-      a += d;
-      b = fmaf(d, d, b);
-    }
-  row_sum<WR>(a, b, sh[1]);
-  // a / n: what rounding left of the mean
-  const float rest = a / n, rstd = row_rstd(b / n, rest, p.eps);
-  mean += rest;
-  if (!there) continue;
-  if (l == 0) {
-    p.stats[r] = mean;
-    p.stats[p.R + r] = rstd;
-  }
-  T *y = (T *)p.out + r * p.C;
+    for (int j = 0; j < NV; ++j) x[j].load((const T *)p.x + row * p.ldx, (j * WR * 64 + l) * N, row < p.R ? (int)p.C : 0);
+  };
+  constexpr bool kAhead = WR < 16;  // (16 waves have 128 registers each, too few for the next row)
+  if (kAhead) fetch(r);
+  float w[NV][N], b[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = (int64_t)(j * WR * 64 + l) * N;
-    if (c >= p.C) continue;
-    float w[N], v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = (f[j][i] - rest) * rstd;
-    weigh<N>(p, c, v, w);
-    store_piece<T, N>(y, c, p.C, v);
+    load_weights<N>(p.weight, p.w_dtype, (j * WR * 64 + l) * N, p.C, 1.f, w[j]);
+    load_weights<N>(p.bias, p.w_dtype, (j * WR * 64 + l) * N, p.C, 0.f, b[j]);
   }
+  const float n = (float)p.C;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.R; r0 += step, r += step) {
+    float f[NV][N], sum = 0.f, sq = 0.f;
+    if (!kAhead) fetch(r);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        f[j][i] = (float)x[j].v[i];
+        sum += f[j][i];
+      }
+    if (kAhead && r0 + step < p.R) fetch(r + step);
+    row_sum<WR>(sum, sq, sh[0]);
+    const float mean = sum / n;
+    sum = sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = (j * WR * 64 + l) * N + i < p.C ? f[j][i] - mean : 0.f;
+        f[j][i] = d;
+        sum += d;
+        sq = fmaf(d, d, sq);
+      }
+    row_sum<WR>(sum, sq, sh[1]);
+    const float rest = sum / n;  // what rounding left of the mean
+    const float rstd = row_rstd(sq / n, rest, p.eps);
+    if (r >= p.R) continue;
+    if (l == 0) {
+      p.stats[r] = mean + rest;
+      p.stats[p.R + r] = rstd;
+    }
+    T *y = (T *)p.out + r * p.C;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * WR * 64 + l) * N;
+      if (c >= p.C) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[j][i] = fmaf((f[j][i] - rest) * rstd, w[j][i], b[j][i]);
+      store_piece<T, N>(y, c, p.C, f[j]);
+    }
   }
 }
 
+// The gradient: dx, and with parts [groups][2][C] this workgroup's sums of dy xh and dy.
+// A lane has the same columns of every row, so these sums stay in its registers; the
+// rows that a workgroup takes at a time are added at the end, in LDS.
 template <typename T, int WAVES, int WR, int NV>
-__global__ void __launch_bounds__(WAVES * 64) layer_norm_dx_kernel(NormArgs p) {
-  constexpr int N = kPiece<T>;
+__global__ void __launch_bounds__(WAVES * 64) layer_norm_backward_kernel(NormArgs p, float *__restrict__ parts) {
+  constexpr int N = kPiece<T>, kRows = WAVES / WR;
   __shared__ float sh[2][WAVES][2];
-  const int wave = threadIdx.x >> 6;
-  int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * (WAVES / WR); r0 < p.R; r0 += (int64_t)gridDim.x * (WAVES / WR), turn ^= 1) {
-  const int64_t r = r0 + wave / WR;
-  const bool there = r < p.R;
-  const int64_t row = there ? r : 0;
-  const T *x = (const T *)p.x + row * p.ldx, *dy = (const T *)p.dy + row * p.lddy;
+  __shared__ float joined[kRows > 1 ? 2 * WR * 64 * NV * N : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = (wave % WR) * 64 + (threadIdx.x & 63);
-  const float mean = p.stats[row], rstd = p.stats[p.R + row];
-  float f[NV][N], g[NV][N], a = 0.f, b = 0.f;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + wave / WR;
+  Piece<T> x[NV], dy[NV];
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * WR * 64 + l) * N, C = row < p.R ? (int)p.C : 0;
+      x[j].load((const T *)p.x + row * p.ldx, c, C);
+      dy[j].load((const T *)p.dy + row * p.lddy, c, C);
+    }
+    mean = row < p.R ? p.stats[row] : 0.f;
+    rstd = row < p.R ? p.stats[p.R + row] : 0.f;
+  };
+  constexpr bool kAhead = WR < 16;
+  if (kAhead) fetch(r);
+  float w[NV][N], aw[NV][N], ab[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = (int64_t)(j * WR * 64 + l) * N;
-    load_piece<T, N>(x, c, p.C, f[j]);
-    load_piece<T, N>(dy, c, p.C, g[j]);
+    load_weights<N>(p.weight, p.w_dtype, (j * WR * 64 + l) * N, p.C, 1.f, w[j]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) aw[j][i] = ab[j][i] = 0.f;
   }
+  const float n = (float)p.C;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.R; r0 += step, r += step, turn ^= 1) {
+    float xh[NV][N], g[NV][N], a = 0.f, b = 0.f;
+    if (!kAhead) fetch(r);
+    const float rs = rstd;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t c = (int64_t)(j * WR * 64 + l) * N;
-    float w[N];
-    if (p.weight != nullptr) load_weights<N>(p.weight, p.w_dtype, c, p.C, w);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (p.weight != nullptr) g[j][i] *= w[i];
-      f[j][i] = c + i < p.C ? (f[j][i] - mean) * rstd : 0.f;
-      a += g[j][i];
-      b = fmaf(g[j][i], f[j][i], b);
+      for (int i = 0; i < N; ++i) {
+        const float d = (float)dy[j].v[i];
+        xh[j][i] = (j * WR * 64 + l) * N + i < p.C ? ((float)x[j].v[i] - mean) * rs : 0.f;
+        aw[j][i] = fmaf(d, xh[j][i], aw[j][i]);
+        ab[j][i] += d;
+        g[j][i] = d * w[j][i];
+        a += g[j][i];
+        b = fmaf(g[j][i], xh[j][i], b);
+      }
+    if (kAhead && r0 + step < p.R) fetch(r + step);
+    row_sum<WR>(a, b, sh[turn]);
+    a /= n;
+    b /= n;
+    if (r >= p.R) continue;
+    T *dx = (T *)p.out + r * p.C;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * WR * 64 + l) * N;
+      if (c >= p.C) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[j][i] = rs * (g[j][i] - a - xh[j][i] * b);
+      store_piece<T, N>(dx, c, p.C, g[j]);
     }
   }
-  row_sum<WR>(a, b, sh[turn]);
-  if (!there) continue;
-  a /= (float)p.C;
-  b /= (float)p.C;
-  T *dx = (T *)p.out + r * p.C;
+  if (parts == nullptr) return;
+  constexpr int kCols = WR * 64 * NV * N;
+  for (int k = 1; k < kRows; ++k) {
+    __syncthreads();
+    if (wave / WR == k) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Row<float, N>::store(joined + (j * WR * 64 + l) * N, aw[j]);
+        Row<float, N>::store(joined + kCols + (j * WR * 64 + l) * N, ab[j]);
+      }
+    }
+    __syncthreads();
+    if (wave < WR) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[N];
+        Row<float, N>::load(joined + (j * WR * 64 + l) * N, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) aw[j][i] += v[i];
+        Row<float, N>::load(joined + kCols + (j * WR * 64 + l) * N, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) ab[j][i] += v[i];
+      }
+    }
+  }
+  if (wave >= WR) return;
+  float *to = parts + (size_t)blockIdx.x * 2 * p.C;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = (int64_t)(j * WR * 64 + l) * N;
+    const int c = (j * WR * 64 + l) * N;
     if (c >= p.C) continue;
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[j][i] = rstd * (g[j][i] - a - f[j][i] * b);
-    store_piece<T, N>(dx, c, p.C, f[j]);
-  }
+    store_piece<float, N>(to, c, p.C, aw[j]);
+    store_piece<float, N>(to + p.C, c, p.C, ab[j]);
   }
 }
 
@@ -205,8 +282,8 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_ke
   for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x) {
     const T *x = (const T *)p.x + r * p.ldx;
     T *y = (T *)p.out + r * p.C;
-    float f[N], w[N], a = 0.f, b = 0.f;
-    for (int64_t c = (int64_t)threadIdx.x * N; c < p.C; c += 1024 * N) {
+    float f[N], w[N], b2[N], a = 0.f, b = 0.f;
+    for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
       load_piece<T, N>(x, c, p.C, f);
 #pragma unroll
       for (int i = 0; i < N; ++i) a += f[i];
@@ -214,7 +291,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_ke
     row_sum<16>(a, b, sh[0]);
     float mean = a / n;
     a = b = 0.f;
-    for (int64_t c = (int64_t)threadIdx.x * N; c < p.C; c += 1024 * N) {
+    for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
       load_piece<T, N>(x, c, p.C, f);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -229,11 +306,14 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_ke
       p.stats[r] = mean + rest;
       p.stats[p.R + r] = rstd;
     }
-    for (int64_t c = (int64_t)threadIdx.x * N; c < p.C; c += 1024 * N) {
+    for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
       load_piece<T, N>(x, c, p.C, f);
 #pragma unroll
       for (int i = 0; i < N; ++i) f[i] = (f[i] - mean - rest) * rstd;
-      weigh<N>(p, c, f, w);
+      load_weights<N>(p.weight, p.w_dtype, c, p.C, 1.f, w);
+      load_weights<N>(p.bias, p.w_dtype, c, p.C, 0.f, b2);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = fmaf(f[i], w[i], b2[i]);
       store_piece<T, N>(y, c, p.C, f);
     }
   }
@@ -246,18 +326,18 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_dx
     const T *x = (const T *)p.x + r * p.ldx, *dy = (const T *)p.dy + r * p.lddy;
     const float mean = p.stats[r], rstd = p.stats[p.R + r];
     float a = 0.f, b = 0.f;
-    auto at = [&](int64_t c, float (&f)[N], float (&g)[N]) {
+    auto at = [&](int c, float (&f)[N], float (&g)[N]) {
       float w[N];
       load_piece<T, N>(x, c, p.C, f);
       load_piece<T, N>(dy, c, p.C, g);
-      if (p.weight != nullptr) load_weights<N>(p.weight, p.w_dtype, c, p.C, w);
+      load_weights<N>(p.weight, p.w_dtype, c, p.C, 1.f, w);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (p.weight != nullptr) g[i] *= w[i];
+        g[i] *= w[i];
         f[i] = c + i < p.C ? (f[i] - mean) * rstd : 0.f;
       }
     };
-    for (int64_t c = (int64_t)threadIdx.x * N; c < p.C; c += 1024 * N) {
+    for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
       float f[N], g[N];
       at(c, f, g);
 #pragma unroll
@@ -269,7 +349,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_dx
     row_sum<16>(a, b, sh[turn]);
     a /= (float)p.C;
     b /= (float)p.C;
-    for (int64_t c = (int64_t)threadIdx.x * N; c < p.C; c += 1024 * N) {
+    for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
       float f[N], g[N];
       at(c, f, g);
 #pragma unroll
@@ -280,10 +360,9 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_dx
 }
 
 // ---------------------------------------------------------------------------
-// dweight and dbias: sums of groups of rows, then of the groups
+// dweight and dbias: sums of groups of rows, one of the groups after another
 // ---------------------------------------------------------------------------
-constexpr int kNormGroups = 256;
-static int64_t norm_groups(int64_t R) { return R < kNormGroups ? R : kNormGroups; }
+constexpr int kNormGroups = 512;
 
 // parts [groups][2][C]
 template <typename T> __global__ void __launch_bounds__(256) layer_norm_dw_kernel(NormArgs p, int64_t per, float *__restrict__ parts) {
@@ -332,39 +411,28 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(NormArgs p, int g
 }
 
 // ---------------------------------------------------------------------------
-// How many waves a row takes and how many pieces a lane of it has.
+// How many waves a row takes and how many pieces a lane of it has
 template <typename T, class K> static hipError_t by_width(const NormArgs &a, hipStream_t s) {
-  const int64_t need = (a.C + 64 * kPiece<T> - 1) / (64 * kPiece<T>);  // pieces of 64 lanes
-  if (need <= 1) return K::template rows<T, 4, 1, 1>(a, s);
-  if (need <= 2) return K::template rows<T, 4, 1, 2>(a, s);
-  if (need <= 4) return K::template rows<T, 4, 4, 1>(a, s);
-  if (need <= 8) return K::template rows<T, 4, 4, 2>(a, s);
-  if (need <= 16) return K::template rows<T, 4, 4, 4>(a, s);
-  if (need <= 64) return K::template rows<T, 16, 16, 4>(a, s);
+  constexpr int NV = kNormLane / kPiece<T>;
+  if (a.C <= 512) return K::template rows<T, 1, NV / 2>(a, s);
+  if (a.C <= 1024) return K::template rows<T, 1, NV>(a, s);
+  if (a.C <= 2048) return K::template rows<T, 2, NV>(a, s);
+  if (a.C <= 4096) return K::template rows<T, 4, NV>(a, s);
+  if (a.C <= 8192) return K::template rows<T, 8, NV>(a, s);
+  if (a.C <= kNormRegisters) return K::template rows<T, 16, NV>(a, s);
   return K::template wide<T>(a, s);
 }
-// workgroups for so many units of work (HIP counts a launch's threads in 32 bits; the kernels loop)
-static dim3 norm_grid(int64_t n) { return dim3((unsigned)(n < (1 << 21) ? n : 1 << 21)); }
+static int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
 
 struct NormForward {
-  template <typename T, int WAVES, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((layer_norm_kernel<T, WAVES, WR, NV>), norm_grid((a.R + WAVES / WR - 1) / (WAVES / WR)), dim3(WAVES * 64),
-                       0, s, a);
+  template <typename T, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
+    constexpr int waves = WR < 4 ? 4 : WR, most = 256 * 24 / waves;
+    hipLaunchKernelGGL((layer_norm_kernel<T, waves, WR, NV>), dim3((unsigned)fewer((a.R + waves / WR - 1) / (waves / WR), most)),
+                       dim3(waves * 64), 0, s, a);
     return hipGetLastError();
   }
   template <typename T> static hipError_t wide(const NormArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(layer_norm_wide_kernel<T>, norm_grid(a.R), dim3(1024), 0, s, a);
-    return hipGetLastError();
-  }
-};
-struct NormBackward {
-  template <typename T, int WAVES, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((layer_norm_dx_kernel<T, WAVES, WR, NV>), norm_grid((a.R + WAVES / WR - 1) / (WAVES / WR)),
-                       dim3(WAVES * 64), 0, s, a);
-    return hipGetLastError();
-  }
-  template <typename T> static hipError_t wide(const NormArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(layer_norm_wide_dx_kernel<T>, norm_grid(a.R), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(layer_norm_wide_kernel<T>, dim3((unsigned)fewer(a.R, 1 << 16)), dim3(1024), 0, s, a);
     return hipGetLastError();
   }
 };
@@ -377,33 +445,49 @@ hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s) {
   }
 }
 
-size_t layer_norm_backward_workspace(int64_t R, int64_t C) { return (size_t)norm_groups(R) * 2 * (size_t)C * 4; }
+size_t layer_norm_backward_workspace(int64_t R, int64_t C) { return (size_t)fewer(R, kNormGroups) * 2 * (size_t)C * 4; }
 
-template <typename T> static hipError_t backward_t(const NormArgs &a, hipStream_t s) {
-  if (a.out != nullptr && a.R > 0) {
-    const hipError_t e = by_width<T, NormBackward>(a, s);
-    if (e != hipSuccess) return e;
-  }
+static hipError_t norm_join(const NormArgs &a, int groups, hipStream_t s) {
   if (a.dweight == nullptr && a.dbias == nullptr) return hipSuccess;
-  float *parts = (float *)a.workspace;
-  const int64_t groups = norm_groups(a.R), per = groups ? (a.R + groups - 1) / groups : 0;
-  const int64_t used = groups ? (a.R + per - 1) / per : 0;
-  if (groups > 0) {
-    const dim3 grid((unsigned)((a.C + 256 * kPiece<T> - 1) / (256 * kPiece<T>)), (unsigned)used);
-    hipLaunchKernelGGL(layer_norm_dw_kernel<T>, grid, dim3(256), 0, s, a, per, parts);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(layer_norm_join_kernel, dim3((unsigned)((2 * a.C + 63) / 64)), dim3(1024), 0, s, a, (int)used,
-                     (const float *)parts);
+  hipLaunchKernelGGL(layer_norm_join_kernel, dim3((unsigned)((2 * a.C + 63) / 64)), dim3(1024), 0, s, a, groups,
+                     (const float *)a.workspace);
   return hipGetLastError();
 }
 
+struct NormBackward {
+  static float *parts(const NormArgs &a) { return a.dweight == nullptr && a.dbias == nullptr ? nullptr : (float *)a.workspace; }
+  template <typename T, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
+    constexpr int waves = WR < 8 ? 8 : WR, most = kNormGroups * 8 / waves;
+    const int groups = (int)fewer((a.R + waves / WR - 1) / (waves / WR), most);
+    if (groups > 0) {
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, waves, WR, NV>), dim3((unsigned)groups), dim3(waves * 64), 0, s, a, parts(a));
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return norm_join(a, groups, s);
+  }
+  template <typename T> static hipError_t wide(const NormArgs &a, hipStream_t s) {
+    const int64_t groups = fewer(a.R, kNormGroups), per = groups ? (a.R + groups - 1) / groups : 0, used = groups ? (a.R + per - 1) / per : 0;
+    if (a.R > 0) {
+      hipLaunchKernelGGL(layer_norm_wide_dx_kernel<T>, dim3((unsigned)fewer(a.R, 1 << 16)), dim3(1024), 0, s, a);
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      if (parts(a) != nullptr) {
+        const dim3 grid((unsigned)((a.C + 256 * kPiece<T> - 1) / (256 * kPiece<T>)), (unsigned)used);
+        hipLaunchKernelGGL(layer_norm_dw_kernel<T>, grid, dim3(256), 0, s, a, per, parts(a));
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+      }
+    }
+    return norm_join(a, (int)used, s);
+  }
+};
+
 hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s) {
   switch (a.dtype) {
-    case NSG_F16: return backward_t<_Float16>(a, s);
-    case NSG_BF16: return backward_t<__bf16>(a, s);
-    default: return backward_t<float>(a, s);
+    case NSG_F16: return by_width<_Float16, NormBackward>(a, s);
+    case NSG_BF16: return by_width<__bf16, NormBackward>(a, s);
+    default: return by_width<float, NormBackward>(a, s);
   }
 }
 

@@ -32,4 +32,21 @@ template <typename T, int ALIGN> struct Row<T, 1, ALIGN> {
   static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = (T)f[0]; }
 };
 
+// ---------------------------------------------------------------------------
+// Sums over the 64 lanes, the same in all of them: within rows of 16 lanes, then over
+// the rows, by data-parallel moves between lanes (no LDS).
+// ---------------------------------------------------------------------------
+template <int CTRL, int ROWS> __device__ __forceinline__ float lanes_moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, ROWS == 0xf));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += lanes_moved<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: zeros come in
+  v += lanes_moved<0x112, 0xf>(v);
+  v += lanes_moved<0x114, 0xf>(v);
+  v += lanes_moved<0x118, 0xf>(v);
+  v += lanes_moved<0x142, 0xa>(v);  // lane 15 of a row to the next one (rows 1 and 3; the others add 0)
+  v += lanes_moved<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
 }  // namespace nsg
