@@ -87,6 +87,57 @@ hipError_t launch_embedding(const EmbedArgs &a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
+// Clearing dW.  The sort waits for its own memory accesses most of the time and keeps few
+// CUs busy, so its launches have more workgroups, which clear a share of dW each.
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+struct Clear {
+  u32x4 *mid = nullptr;             // n units of 16 bytes
+  int64_t n = 0;
+  uint16_t *head = nullptr, *tail = nullptr;  // what lies before and behind them: less than 16 bytes each
+  int nhead = 0, ntail = 0;
+  int blocks = 0;                   // workgroups that share it, behind those of the sort
+  bool stream = false;              // past the caches
+  __device__ __forceinline__ void run(int block) const {
+    const int64_t per = (n + blocks - 1) / blocks, i1 = min(n, (block + 1) * per);
+    if (stream) {
+      for (int64_t i = block * per + threadIdx.x; i < i1; i += blockDim.x) __builtin_nontemporal_store(u32x4(0), mid + i);
+    } else {
+      for (int64_t i = block * per + threadIdx.x; i < i1; i += blockDim.x) mid[i] = u32x4(0);
+    }
+    if (block == 0 && (int)threadIdx.x < nhead) head[threadIdx.x] = 0;
+    if (block == 0 && (int)threadIdx.x < ntail) tail[threadIdx.x] = 0;
+  }
+};
+// A dW that the last-level cache (256 MB) holds is cleared in it, a larger one past it: the
+// gradient of 4099 tokens (98 MB) takes 34 us, streamed 39; of 65536 (1.05 GB) 380, streamed 358.
+constexpr int64_t kClearKept = 224 << 20;
+
+// share i of `shares` of `bytes` bytes at p
+static Clear clear_share(void *p, int64_t bytes, int i, int shares) {
+  Clear c;
+  if (bytes == 0) return c;
+  char *b = (char *)p;
+  int64_t head = (16 - reinterpret_cast<uintptr_t>(p) % 16) % 16;
+  if (head > bytes) head = bytes;
+  const int64_t n = (bytes - head) / 16, i0 = n * i / shares;
+  c.mid = (u32x4 *)(b + head) + i0;
+  c.n = n * (i + 1) / shares - i0;
+  if (i == 0) {
+    c.head = (uint16_t *)b;
+    c.nhead = (int)(head / 2);
+    c.tail = (uint16_t *)(b + head + n * 16);
+    c.ntail = (int)((bytes - head - n * 16) / 2);
+  }
+  const int64_t blocks = (c.n + 4095) / 4096;  // 64 KB or more to a workgroup
+  c.blocks = blocks > 1024 ? 1024 : blocks < 1 ? 1 : (int)blocks;
+  c.stream = bytes > kClearKept;
+  return c;
+}
+__global__ void __launch_bounds__(1024) embed_clear_kernel(Clear c) { c.run((int)blockIdx.x); }
+
+// ---------------------------------------------------------------------------
 // the gradient's sort: a stable counting sort of the tokens by their id, by its low
 // digit and then by its high one (ids of up to 10 bits: one digit).  Tokens without an
 // id are left out: keys behind the last token that has one are -1.
@@ -134,7 +185,8 @@ struct SortInput {
 
 // tokens of each value of the digit in each chunk
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(SortInput in, int64_t N, int64_t chunk, int shift, int bits,
-                                                                   int32_t *__restrict__ table) {
+                                                                   int32_t *__restrict__ table, int chunks, Clear c) {
+  if ((int)blockIdx.x >= chunks) return c.run((int)blockIdx.x - chunks);
   __shared__ int count[kSortBins];
   const int bins = 1 << bits;
   for (int e = threadIdx.x; e < bins; e += kSortThreads) count[e] = 0;
@@ -185,10 +237,13 @@ __device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int6
   __syncthreads();
   // thread e: all tokens with digit e, and those before this chunk
   const int e = threadIdx.x;
-  int total = 0, before = 0;
+  int total = 0, before = 0, own[kSortWaves];
   if (e < bins) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) own[w] = at[w * bins + e];
     if (chunks == 1) {
-      for (int w = 0; w < kSortWaves; ++w) total += at[w * bins + e];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) total += own[w];
     } else {
 #pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
@@ -202,10 +257,10 @@ __device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int6
   const int first = block_before<kSortThreads>(total, sh, all);
   if (e < bins) {
     int next = first + before;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int n = at[w * bins + e];
       at[w * bins + e] = next;
-      next += n;
+      next += own[w];
     }
   }
   __syncthreads();
@@ -244,7 +299,8 @@ __device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int6
 template <int KEPT>
 __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(SortInput in, int64_t N, int64_t chunk, int chunks, int shift,
                                                                    int bits, const int32_t *__restrict__ table,
-                                                                   int32_t *__restrict__ keys, int32_t *__restrict__ toks) {
+                                                                   int32_t *__restrict__ keys, int32_t *__restrict__ toks, Clear c) {
+  if ((int)blockIdx.x >= chunks) return c.run((int)blockIdx.x - chunks);
   __shared__ int at[kSortWaves * kSortBins];
   __shared__ int sh[kSortWaves + 1];
   place_chunk<KEPT>(in, N, chunk, chunks, (int)blockIdx.x, shift, bits, table, at, sh, keys, toks);
@@ -252,7 +308,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(SortInput in,
 
 // all digits by one workgroup
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortInput in, int64_t N, int64_t chunk, int digits, int bits,
-                                                                  int32_t *keys1, int32_t *toks1, int32_t *keys, int32_t *toks) {
+                                                                  int32_t *keys1, int32_t *toks1, int32_t *keys, int32_t *toks,
+                                                                  Clear c) {
+  if (blockIdx.x > 0) return c.run((int)blockIdx.x - 1);
   __shared__ int at[kSortWaves * kSortBins];
   __shared__ int sh[kSortWaves + 1];
   if (digits == 2) {
@@ -295,29 +353,36 @@ struct Chunk {
   }
 };
 
-template <typename T, int N> __device__ __forceinline__ void add_row(T *p, int64_t c, int64_t C, const float (&f)[N], bool add) {
-  if (c + N <= C) {
-    float g[N];
-    if (add) {
-      Row<T, N, (int)sizeof(T)>::load(p + c, g);
-#pragma unroll
-      for (int i = 0; i < N; ++i) g[i] += f[i];
+// N elements of a row from c on, zeros behind its end
+template <typename T, int N> struct Cells {
+  typedef T vec __attribute__((ext_vector_type(N)));
+  typedef vec mem __attribute__((aligned(sizeof(T))));
+  vec v;
+  __device__ __forceinline__ void load(const T *row, int64_t c, int64_t C) {
+    if (c + N <= C) {
+      v = *reinterpret_cast<const mem *>(row + c);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) g[i] = f[i];
+      for (int i = 0; i < N; ++i) v[i] = c + i < C ? row[c + i] : (T)0.f;
     }
-    Row<T, N, (int)sizeof(T)>::store(p + c, g);
+  }
+};
+template <typename T, int N> __device__ __forceinline__ void store_cells(T *row, int64_t c, int64_t C, const float (&f)[N]) {
+  if (c + N <= C) {
+    Row<T, N, (int)sizeof(T)>::store(row + c, f);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (c + i < C) p[c + i] = (T)(add ? (float)p[c + i] + f[i] : f[i]);
+      if (c + i < C) row[c + i] = (T)f[i];
   }
 }
 
-template <typename T, typename O>
+// One wave per chunk and 64 x 16 bytes of its rows.  With ADD a run's row of dW is read
+// together with its first row of dout.
+template <typename T, typename O, bool ADD>
 __global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restrict__ keys, const int32_t *__restrict__ toks,
                                                          int64_t ntok, int64_t S, int64_t chunks, const T *__restrict__ dout,
-                                                         int64_t ld, int64_t C, float scale, int add, int lp,
+                                                         int64_t ld, int64_t C, float scale, int lp,
                                                          O *__restrict__ out, float *__restrict__ parts, int64_t pitch) {
   constexpr int N = 16 / (int)sizeof(T);
   const EmbedParts at(lp);
@@ -325,62 +390,62 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restri
   if (at.t >= chunks || c >= C) return;
   const Chunk ch(keys, ntok, S, at.t);
   float acc[N];
+  Cells<O, N> old;
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
-  int run = keys[ch.p0];
+  for (int i = 0; i < N; ++i) {
+    acc[i] = 0.f;
+    if (ADD) old.v[i] = (O)0.f;
+  }
+  int run = -1;
   bool began = ch.before;  // the present run began in an earlier chunk
-  if (run < 0) return;     // keys of -1 are the last ones
-  const bool full = c + N <= C;
   auto close = [&](bool goes_on) {
     if (began || goes_on) {
-      float *p = parts + (at.t * 2 + (began ? 0 : 1)) * pitch;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (c + i < C) p[c + i] = acc[i];
+      store_cells<float, N>(parts + (at.t * 2 + (began ? 0 : 1)) * pitch, c, C, acc);
     } else {
       float f[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = acc[i] * scale;
-      add_row<O, N>(out + (int64_t)run * C, c, C, f, add);
+      for (int i = 0; i < N; ++i) f[i] = ADD ? fmaf(acc[i], scale, (float)old.v[i]) : acc[i] * scale;
+      store_cells<O, N>(out + (int64_t)run * C, c, C, f);
     }
   };
+  int last = -1;
   for (int64_t p = ch.p0; p < ch.p1; p += kRunUnroll) {
     int key[kRunUnroll];
-    float f[kRunUnroll][N];
+    Cells<T, N> row[kRunUnroll];
+    Cells<O, N> was[ADD ? kRunUnroll : 1];
 #pragma unroll
     for (int u = 0; u < kRunUnroll; ++u) {
-      key[u] = p + u < ch.p1 ? keys[p + u] : -1;
+      key[u] = p + u < ch.p1 ? keys[p + u] : -1;  // keys of -1 are the last ones
       if (key[u] >= 0) {
-        const T *row = dout + (int64_t)toks[p + u] * ld;
-        if (full) {
-          Row<T, N, (int)sizeof(T)>::load(row + c, f[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) f[u][i] = c + i < C ? (float)row[c + i] : 0.f;
-        }
+        row[u].load(dout + (int64_t)toks[p + u] * ld, c, C);
+        if (ADD && key[u] != last) was[ADD ? u : 0].load(out + (int64_t)key[u] * C, c, C);
       }
+      last = key[u];
     }
 #pragma unroll
     for (int u = 0; u < kRunUnroll; ++u) {
       if (key[u] < 0) continue;
       if (key[u] != run) {
-        close(false);
+        if (run >= 0) {
+          close(false);
+          began = false;
+        }
         run = key[u];
-        began = false;
+        if (ADD) old = was[ADD ? u : 0];
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] += f[u][i];
+      for (int i = 0; i < N; ++i) acc[i] += (float)row[u].v[i];
     }
   }
-  close(ch.after);
+  if (run >= 0) close(ch.after);
 }
 
 // The run that begins in chunk t and goes on: its parts in the order of the chunks.
 template <typename O>
 __global__ void __launch_bounds__(256) embed_join_kernel(const int32_t *__restrict__ keys, int64_t ntok, int64_t S,
-                                                         int64_t chunks, int64_t C, float scale, int add, int lp,
+                                                         int64_t chunks, int64_t C, float scale, bool add, int lp,
                                                          O *__restrict__ out, const float *__restrict__ parts, int64_t pitch) {
   const EmbedParts at(lp);
   const int lane = threadIdx.x & 63;
@@ -410,33 +475,12 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const int32_t *__restri
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] += f[v];
   }
+  O *row = out + (int64_t)run * C;
+  Cells<O, 4> old;
+  if (add) old.load(row, c, C);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) acc[v] *= scale;
-  add_row<O, 4>(out + (int64_t)run * C, c, C, acc, add);
-}
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// n units of 16 bytes from a 16-byte boundary, and the bytes before and behind them in twos
-__global__ void __launch_bounds__(256) embed_clear_kernel(uint16_t *__restrict__ head, int64_t nhead, u32x4 *__restrict__ mid,
-                                                          int64_t n, uint16_t *__restrict__ tail, int64_t ntail) {
-  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = i0; i < n; i += step) __builtin_nontemporal_store(u32x4(0), mid + i);
-  if (i0 < nhead) head[i0] = 0;
-  if (i0 < ntail) tail[i0] = 0;
-}
-
-static hipError_t clear(void *p, int64_t bytes, hipStream_t s) {
-  char *b = (char *)p;
-  int64_t head = (16 - reinterpret_cast<uintptr_t>(p) % 16) % 16;
-  if (head > bytes) head = bytes;
-  const int64_t n = (bytes - head) / 16;
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 4096) blocks = 4096;
-  if (blocks < 1) blocks = 1;
-  hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (uint16_t *)b, head / 2, (u32x4 *)(b + head), n,
-                     (uint16_t *)(b + head + n * 16), (bytes - head - n * 16) / 2);
-  return hipGetLastError();
+  for (int v = 0; v < 4; ++v) acc[v] = add ? fmaf(acc[v], scale, (float)old.v[v]) : acc[v] * scale;
+  store_cells<O, 4>(row, c, C, acc);
 }
 
 // Two lists of pairs, the sort's table, the sums of parts of runs
@@ -465,14 +509,19 @@ template <typename T, typename O> static hipError_t runs_to(const EmbedArgs &a, 
   const int64_t S = run_chunk(a.T, a.C), chunks = run_chunks(a.T, a.C), pitch = part_pitch(a.C);
   int64_t n = (a.C + 64 * N - 1) / (64 * N);
   int lp = parts_log(chunks, n);
-  hipLaunchKernelGGL((embed_runs_kernel<T, O>), parts_grid(chunks, n, lp), dim3(256), 0, s, keys, toks, a.T, S, chunks,
-                     (const T *)a.x, a.ld, a.C, a.scale, a.accumulate, lp, (O *)a.out, parts, pitch);
+  const dim3 grid = parts_grid(chunks, n, lp);
+  if (a.accumulate)
+    hipLaunchKernelGGL((embed_runs_kernel<T, O, true>), grid, dim3(256), 0, s, keys, toks, a.T, S, chunks, (const T *)a.x, a.ld,
+                       a.C, a.scale, lp, (O *)a.out, parts, pitch);
+  else
+    hipLaunchKernelGGL((embed_runs_kernel<T, O, false>), grid, dim3(256), 0, s, keys, toks, a.T, S, chunks, (const T *)a.x, a.ld,
+                       a.C, a.scale, lp, (O *)a.out, parts, pitch);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks < 2) return e;
   n = (a.C + 255) / 256;
   lp = parts_log(chunks, n);
   hipLaunchKernelGGL((embed_join_kernel<O>), parts_grid(chunks, n, lp), dim3(256), 0, s, keys, a.T, S, chunks, a.C, a.scale,
-                     a.accumulate, lp, (O *)a.out, parts, pitch);
+                     a.accumulate != 0, lp, (O *)a.out, parts, pitch);
   return hipGetLastError();
 }
 template <typename T> static hipError_t runs_t(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {
@@ -484,32 +533,40 @@ template <typename T> static hipError_t runs_t(const EmbedArgs &a, const EmbedSp
 }
 
 hipError_t launch_embedding_backward(const EmbedArgs &a, hipStream_t s) {
-  hipError_t e = hipSuccess;
-  if (!a.accumulate) e = clear(a.out, a.V * a.C * (a.out_dtype == NSG_F32 ? 4 : 2), s);
-  if (e != hipSuccess || a.T == 0) return e;
+  const int64_t bytes = a.accumulate ? 0 : a.V * a.C * (a.out_dtype == NSG_F32 ? 4 : 2);
+  if (a.T == 0) {
+    const Clear c = clear_share(a.out, bytes, 0, 1);
+    if (c.blocks > 0) hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)c.blocks), dim3(1024), 0, s, c);
+    return hipGetLastError();
+  }
   const EmbedSpace sp(a.T, a.V, a.C);
   const SortPlan p = sort_plan(a.T, a.V);
   char *ws = (char *)a.workspace;
   int32_t *keys1 = (int32_t *)(ws + sp.keys1), *toks1 = (int32_t *)(ws + sp.toks1);
   int32_t *keys = (int32_t *)(ws + sp.keys), *toks = (int32_t *)(ws + sp.toks), *table = (int32_t *)(ws + sp.table);
   SortInput in{a.ids, a.wide, a.V, nullptr, nullptr};
+  hipError_t e = hipSuccess;
   if (p.chunks == 1) {
-    hipLaunchKernelGGL(embed_sort_kernel, dim3(1), dim3(kSortThreads), 0, s, in, a.T, p.chunk, p.digits, p.bits, keys1, toks1, keys, toks);
+    const Clear c = clear_share(a.out, bytes, 0, 1);
+    hipLaunchKernelGGL(embed_sort_kernel, dim3(1 + (unsigned)c.blocks), dim3(kSortThreads), 0, s, in, a.T, p.chunk, p.digits,
+                       p.bits, keys1, toks1, keys, toks, c);
     e = hipGetLastError();
   } else {
     for (int d = 0; d < p.digits && e == hipSuccess; ++d) {
       const bool last = d == p.digits - 1;
       int32_t *k = last ? keys : keys1, *t = last ? toks : toks1;
-      hipLaunchKernelGGL(embed_count_kernel, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk, d * p.bits,
-                         p.bits, table);
+      Clear c = clear_share(a.out, bytes, 2 * d, 2 * p.digits);
+      hipLaunchKernelGGL(embed_count_kernel, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
+                         d * p.bits, p.bits, table, p.chunks, c);
       e = hipGetLastError();
       if (e != hipSuccess) break;
+      c = clear_share(a.out, bytes, 2 * d + 1, 2 * p.digits);
       if (p.chunk <= kSortChunk)
-        hipLaunchKernelGGL(embed_place_kernel<kSortKept>, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
-                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t);
+        hipLaunchKernelGGL(embed_place_kernel<kSortKept>, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T,
+                           p.chunk, p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t, c);
       else
-        hipLaunchKernelGGL(embed_place_kernel<0>, dim3((unsigned)p.chunks), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
-                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t);
+        hipLaunchKernelGGL(embed_place_kernel<0>, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
+                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t, c);
       e = hipGetLastError();
       in.keys = keys1;
       in.toks = toks1;
