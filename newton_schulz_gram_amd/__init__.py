@@ -12,6 +12,8 @@ CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -952,38 +954,41 @@ def _ids(t: torch.Tensor, name: str, device=None):
         raise ValueError(f"{name} must be a contiguous int32 or int64 tensor on the input's device")
 
 
-def _vectors(t: torch.Tensor, name: str, lead, device=None):
-    """t [*lead, C] (lead None: any) as rows of C elements: (rows, C, pitch).  Two dimensions may
-    have a pitch, more must be contiguous."""
-    if t.dim() < 2 or t.dtype not in _DT:
+def _vectors(t: torch.Tensor, name: str, device=None):
+    """t [..., C] as rows of C elements: (rows, C, pitch).  Two dimensions may have a pitch,
+    more must be contiguous."""
+    shape = t.shape
+    if len(shape) < 2 or t.dtype not in _DT:
         raise ValueError(f"{name} must be a float16, bfloat16 or float32 tensor of rows")
-    if lead is not None and t.shape[:-1] != lead:
-        raise ValueError(f"{name} must have shape [{', '.join(map(str, lead))}, C]")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on the input's device")
-    C = t.shape[-1]
-    if t.dim() == 2:
-        return t.shape[0], C, _pitch(t, name) if t.numel() else C
-    if not t.is_contiguous():
+    C = shape[-1]
+    if t.is_contiguous():
+        return t.numel() // C if C else math.prod(shape[:-1]), C, C
+    if len(shape) > 2:
         raise ValueError(f"{name} must be contiguous, or a matrix with unit column stride")
-    return t.numel() // C if C else 0, C, C
+    return shape[0], C, _pitch(t, name)
 
 
-def _space(workspace: Optional[torch.Tensor], need: int, device):
-    """A workspace of `need` bytes and its size: the caller's where it is large enough."""
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A packed tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _space(workspace: Optional[torch.Tensor], need: int, t: torch.Tensor) -> torch.Tensor:
+    """A workspace of `need` bytes on t's device: the caller's where it is large enough."""
     if workspace is not None:
-        check_workspace(workspace, device)
+        check_workspace(workspace, t.device)
         if nbytes(workspace) >= need:
-            return workspace.data_ptr(), nbytes(workspace), workspace
-    if not need:
-        return None, 0, None
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace.data_ptr(), need, workspace
+            return workspace
+    return t.new_empty(need, dtype=torch.uint8)
 
 
-def _size_of(fn, what: str, *args) -> int:
+@functools.lru_cache(maxsize=1024)
+def _size_of(what: str, *args) -> int:
+    """A workspace's size, which these numbers alone decide (the call is a tenth of a short launch's time)."""
     out = ctypes.c_size_t(0)
-    _check(fn(*args, ctypes.byref(out)), what)
+    _check(getattr(lib(), what)(*args, ctypes.byref(out)), what)
     return out.value
 
 
@@ -992,17 +997,18 @@ def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0) -> to
     out [*ids.shape, C] of weight's dtype (fp32 products, rounded once).  An id outside
     0 .. V - 1, such as -1 for padding, gives zeros.  V <= 2^20."""
     device = _gpu(weight, "embedding")
-    ld = _matrix(weight, "weight")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [V, C]")
+    V, C, ld = _vectors(weight, "weight")
     _ids(ids, "ids", device)
-    V, C = weight.shape
-    out = torch.empty((*ids.shape, C), dtype=weight.dtype, device=device)
+    out = weight.new_empty((*ids.shape, C))
     _launch(device, "nsg_embedding", lib().nsg_embedding, ids.data_ptr(), 8 * ids.element_size(), ids.numel(),
             weight.data_ptr(), _DT[weight.dtype], V, C, ld, float(scale), out.data_ptr())
     return out
 
 
 def embedding_backward_workspace_size(T: int, V: int, C: int) -> int:
-    return _size_of(lib().nsg_embedding_backward_workspace_size, "nsg_embedding_backward_workspace_size", T, V, C)
+    return _size_of("nsg_embedding_backward_workspace_size", T, V, C)
 
 
 def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, num_embeddings: int, scale: float = 1.0,
@@ -1017,33 +1023,29 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, num_embeddings: in
     bytes (allocated if not given)."""
     device = _gpu(dout, "embedding_backward")
     _ids(ids, "ids", device)
-    T, C, ld = _vectors(dout, "dout", ids.shape)
+    if dout.shape[:-1] != ids.shape:
+        raise ValueError(f"dout must have shape [*{tuple(ids.shape)}, C]")
+    T = ids.numel()
+    C, ld = _vectors(dout if dout.dim() > 1 else dout.unsqueeze(0), "dout")[1:]
     V = int(num_embeddings)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is None:
-        out = torch.empty((V, C), dtype=dout.dtype, device=device)
+        out = dout.new_empty((V, C))
     elif out.shape != (V, C) or out.dtype not in _DT or not out.is_contiguous() or out.device != device:
         raise ValueError(f"out must be a contiguous float tensor of shape {(V, C)} on the input's device")
-    ptr, size, _keep = _space(workspace, embedding_backward_workspace_size(ids.numel(), V, C), device)
-    _launch(device, "nsg_embedding_backward", lib().nsg_embedding_backward, dout.data_ptr(), _DT[dout.dtype], ids.numel(), C, ld,
+    ws = _space(workspace, embedding_backward_workspace_size(T, V, C), dout)
+    _launch(device, "nsg_embedding_backward", lib().nsg_embedding_backward, dout.data_ptr(), _DT[dout.dtype], T, C, ld,
             ids.data_ptr(), 8 * ids.element_size(), V, float(scale), out.data_ptr(), _DT[out.dtype], 1 if accumulate else 0,
-            ptr, size)
+            ws.data_ptr(), nbytes(ws))
     return out
 
 
-def _norm_weights(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], C: int, device) -> int:
-    """The dtype code of layer norm's weight and bias."""
-    dtype = None
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        if t.shape != (C,) or t.dtype not in _DT or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be a contiguous float tensor of shape {(C,)} on the input's device")
-        if dtype not in (None, t.dtype):
-            raise ValueError("weight and bias must have one dtype")
-        dtype = t.dtype
-    return NSG_F32 if dtype is None else _DT[dtype]
+def _norm_weight(t: torch.Tensor, name: str, C: int, device) -> int:
+    """The dtype code of layer norm's weight or bias."""
+    if t.shape != (C,) or t.dtype not in _DT or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous float tensor of shape {(C,)} on the input's device")
+    return _DT[t.dtype]
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5):
@@ -1052,10 +1054,16 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     means and rstd = 1 / sqrt(var + eps), which layer_norm_backward takes.  weight and
     bias [C]: of one dtype, float32 or another; None for 1 and 0."""
     device = _gpu(x, "layer_norm")
-    R, C, ld = _vectors(x, "x", None)
-    code = _norm_weights(weight, bias, C, device)
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
-    stats = torch.empty((2, R), dtype=torch.float32, device=device)
+    R, C, ld = _vectors(x, "x")
+    code = NSG_F32
+    if weight is not None:
+        code = _norm_weight(weight, "weight", C, device)
+    if bias is not None:
+        if weight is not None and bias.dtype != weight.dtype:
+            raise ValueError("weight and bias must have one dtype")
+        code = _norm_weight(bias, "bias", C, device)
+    y = _like(x)
+    stats = x.new_empty((2, R), dtype=torch.float32)
     _launch(device, "nsg_layer_norm", lib().nsg_layer_norm, x.data_ptr(), _DT[x.dtype], R, C, ld,
             weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, code, float(eps),
             y.data_ptr(), stats.data_ptr())
@@ -1063,7 +1071,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 
 
 def layer_norm_backward_workspace_size(R: int, C: int) -> int:
-    return _size_of(lib().nsg_layer_norm_backward_workspace_size, "nsg_layer_norm_backward_workspace_size", R, C)
+    return _size_of("nsg_layer_norm_backward_workspace_size", R, C)
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -1073,22 +1081,24 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, 
     is false.  fp32 sums, rounded once.  `workspace`: a uint8 tensor of
     layer_norm_backward_workspace_size(R, C) bytes (allocated if not given)."""
     device = _gpu(x, "layer_norm_backward")
-    R, C, ldx = _vectors(x, "x", None)
-    lddy = _vectors(dy, "dy", x.shape[:-1], device)[2]
+    R, C, ldx = _vectors(x, "x")
+    lddy = _vectors(dy, "dy", device)[2]
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must have x's shape and dtype")
     if stats.shape != (2, R) or stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != device:
         raise ValueError(f"stats must be a contiguous float32 tensor of shape {(2, R)} on the input's device")
-    code = _norm_weights(weight, None, C, device)
-    wt = torch.float32 if weight is None else weight.dtype
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device)
-    dweight = torch.empty(C, dtype=wt, device=device) if weight_grad else None
-    dbias = torch.empty(C, dtype=wt, device=device) if bias_grad else None
-    need = layer_norm_backward_workspace_size(R, C) if weight_grad or bias_grad else 0
-    ptr, size, _keep = _space(workspace, need, device)
+    code = NSG_F32 if weight is None else _norm_weight(weight, "weight", C, device)
+    row = (lambda: torch.empty_like(weight)) if weight is not None else (lambda: x.new_empty(C, dtype=torch.float32))
+    dx = _like(x)
+    dweight = row() if weight_grad else None
+    dbias = row() if bias_grad else None
+    ws = None
+    if weight_grad or bias_grad:
+        ws = _space(workspace, layer_norm_backward_workspace_size(R, C), x)
     _launch(device, "nsg_layer_norm_backward", lib().nsg_layer_norm_backward, dy.data_ptr(), lddy, x.data_ptr(), ldx, _DT[x.dtype],
             R, C, stats.data_ptr(), weight.data_ptr() if weight is not None else None, code, dx.data_ptr(),
-            dweight.data_ptr() if weight_grad else None, dbias.data_ptr() if bias_grad else None, ptr, size)
+            dweight.data_ptr() if weight_grad else None, dbias.data_ptr() if bias_grad else None,
+            ws.data_ptr() if ws is not None else None, nbytes(ws) if ws is not None else 0)
     return dx, dweight, dbias
 
 
@@ -1116,7 +1126,7 @@ def _score_code(score) -> int:
 
 
 def expert_route_workspace_size(T: int, num_experts: int) -> int:
-    return _size_of(lib().nsg_expert_route_workspace_size, "nsg_expert_route_workspace_size", T, num_experts)
+    return _size_of("nsg_expert_route_workspace_size", T, num_experts)
 
 
 def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -1134,9 +1144,10 @@ def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
     N tokens with a choice (see Routing).  `workspace`, for the loss: a uint8 tensor of
     expert_route_workspace_size(T, E) bytes (allocated if not given).  k <= 64, E <= 1024."""
     device = _gpu(logits, "expert_route")
-    ld = _matrix(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E, ld = _vectors(logits, "logits")
     code = _score_code(score)
-    T, E = logits.shape
     k = int(k)
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous() or bias.device != device):
         raise ValueError("bias must be a contiguous float32 [E] tensor on the input's device")
@@ -1145,19 +1156,19 @@ def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
         raise ValueError("mask must be a contiguous bool [T] tensor on the input's device")
     if not 1 <= k <= min(E, 64):
         raise ValueError("k must lie in 1 .. min(E, 64)")
-    ids = torch.empty((T, k), dtype=torch.int32, device=device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    counts = probs = loss = ptr = None
-    size = 0
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    counts = probs = loss = ws = None
     if balance:
-        counts = torch.empty(E + 1, dtype=torch.int32, device=device)
-        probs = torch.empty(E, dtype=torch.float32, device=device)
-        loss = torch.empty((), dtype=torch.float32, device=device)
-        ptr, size, _keep = _space(workspace, expert_route_workspace_size(T, E), device)
+        counts = logits.new_empty(E + 1, dtype=torch.int32)
+        probs = logits.new_empty(E, dtype=torch.float32)
+        loss = logits.new_empty((), dtype=torch.float32)
+        ws = _space(workspace, expert_route_workspace_size(T, E), logits)
     _launch(device, "nsg_expert_route", lib().nsg_expert_route, logits.data_ptr(), _DT[logits.dtype], T, E, ld, k, code,
             bias.data_ptr() if bias is not None else None, mask.data_ptr() if mask is not None else None,
             1 if normalize else 0, float(scale), ids.data_ptr(), weights.data_ptr(), counts.data_ptr() if balance else None,
-            probs.data_ptr() if balance else None, loss.data_ptr() if balance else None, ptr, size)
+            probs.data_ptr() if balance else None, loss.data_ptr() if balance else None, ws.data_ptr() if balance else None,
+            nbytes(ws) if balance else 0)
     return Routing(ids, weights, counts, probs, loss)
 
 
@@ -1172,9 +1183,10 @@ def expert_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: Opt
     added: `balance` times it, times dloss where that (a float32 scalar) is given.
     counts are constants.  A token without a choice gets zeros."""
     device = _gpu(logits, "expert_route_backward")
-    ld = _matrix(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E, ld = _vectors(logits, "logits")
     code = _score_code(score)
-    T, E = logits.shape
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError("ids must be [T, k]")
     _ints(ids, None, "ids", device)
@@ -1185,7 +1197,7 @@ def expert_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: Opt
         _ints(counts, (E + 1,), "counts", device)
     if dloss is not None and (counts is None or dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != device):
         raise ValueError("dloss must be a float32 scalar on the input's device, with counts")
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=device)
+    dlogits = _like(logits)
     _launch(device, "nsg_expert_route_backward", lib().nsg_expert_route_backward, logits.data_ptr(), _DT[logits.dtype], T, E, ld,
             ids.shape[1], code, 1 if normalize else 0, float(scale), ids.data_ptr(),
             dweights.data_ptr() if dweights is not None else None, counts.data_ptr() if counts is not None else None,

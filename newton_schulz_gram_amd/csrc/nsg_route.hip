@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "nsg_layer.h"
 #include "nsg_rows.h"
@@ -23,10 +24,10 @@
 namespace nsg {
 
 constexpr int kRouteThreads = 256;
+constexpr int kRouteBlocks = 2048;   // workgroups of a launch
 constexpr int kBalanceBlocks = 256;  // with the balance loss: workgroups, whose sums are joined
 
-// N consecutive logits of a row from e on, -inf behind the last expert.  (The type of
-// the logits is the same in all lanes: one branch a row instead of three kernels.)
+// N consecutive numbers of a row from e on, -inf behind the last expert
 template <typename T, int N> __device__ __forceinline__ void load_as(const T *row, int e, int E, float (&f)[N]) {
   if (e + N <= E) {
     Row<T, N, (int)sizeof(T)>::load(row + e, f);
@@ -35,12 +36,57 @@ template <typename T, int N> __device__ __forceinline__ void load_as(const T *ro
     for (int i = 0; i < N; ++i) f[i] = e + i < E ? (float)row[e + i] : -INFINITY;
   }
 }
-template <int N> __device__ __forceinline__ void load_logits(const RouteArgs &p, int64_t t, int e, float (&f)[N]) {
-  const int64_t at = t * p.ld;
-  if (p.dtype == NSG_F32) load_as((const float *)p.logits + at, e, p.E, f);
-  else if (p.dtype == NSG_BF16) load_as((const __bf16 *)p.logits + at, e, p.E, f);
-  else load_as((const _Float16 *)p.logits + at, e, p.E, f);
-}
+// N consecutive logits, loaded as they are and converted when they are used: a conversion
+// would wait for the load.  (The type of the logits is the same in all lanes: a branch or two
+// for each token instead of three kernels.)
+template <int N> struct Logits {
+  uint32_t w[N];  // one to a word, or two
+  __device__ __forceinline__ void load(const RouteArgs &p, int64_t t, int e) {
+    const int64_t at = t * p.ld + e;
+    if (p.dtype == NSG_F32) words<uint32_t, N>((const uint32_t *)p.logits + at, e, p.E, 0xff800000u);
+    else words<uint16_t, (N + 1) / 2>((const uint16_t *)p.logits + at, e, p.E, p.dtype == NSG_BF16 ? 0xff80ff80u : 0xfc00fc00u);
+  }
+  __device__ __forceinline__ void get(const RouteArgs &p, float (&f)[N]) const {
+    if (p.dtype == NSG_F32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+    } else if (p.dtype == NSG_BF16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i / 2] >> (16 * (i & 1))));
+    }
+  }
+
+ private:
+  template <typename T, int W> __device__ __forceinline__ void words(const T *row, int e, int E, uint32_t none) {
+    constexpr int kIn = sizeof(T) == 2 ? 2 : 1;  // elements of a word
+    if (N % kIn == 0 && e + N <= E) {
+      typedef uint32_t vec __attribute__((ext_vector_type(W)));
+      typedef vec mem __attribute__((aligned(sizeof(T))));
+      const vec v = *reinterpret_cast<const mem *>(row);
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = none;
+      if (e < E) {
+        if (N == 1) {
+          w[0] = row[0];  // (kIn 2: the other half is not used)
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (e + i < E) {
+              const uint32_t x = row[i];
+              if (kIn == 1) w[i] = x;
+              else w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | x << 16 : (w[i / 2] & 0xffff0000u) | x;
+            }
+        }
+      }
+    }
+  }
+};
 __device__ __forceinline__ float logit(const RouteArgs &p, int64_t t, int e) {
   const int64_t at = t * p.ld + e;
   if (p.dtype == NSG_F32) return ((const float *)p.logits)[at];
@@ -90,16 +136,40 @@ template <int L, class Op> __device__ __forceinline__ float group_join(float v, 
   }
   return v;
 }
-template <int L> __device__ __forceinline__ float group_max(float v) {
-  return group_join<L>(v, [](float a, float b) { return fmaxf(a, b); });
+// Floats as whole numbers in the same order (a NaN counts as -inf), and back
+__device__ __forceinline__ int ordered(float f) {
+  const int i = __builtin_bit_cast(int, f == f ? f : -INFINITY);
+  return i ^ ((i >> 31) & 0x7fffffff);
 }
+__device__ __forceinline__ float unordered(int i) { return __builtin_bit_cast(float, i ^ ((i >> 31) & 0x7fffffff)); }
+// Largest of the group in whole numbers, which a move between lanes and the comparison
+// take one instruction for (floats: three)
+template <int L> __device__ __forceinline__ int group_max(int v) {
+  auto moved = [](int x, auto ctrl) { return __builtin_amdgcn_update_dpp(x, x, decltype(ctrl)::value, 0xf, 0xf, true); };
+  v = max(v, moved(v, std::integral_constant<int, 0xB1>()));
+  v = max(v, moved(v, std::integral_constant<int, 0x4E>()));
+  if (L >= 16) {
+    v = max(v, moved(v, std::integral_constant<int, 0x141>()));
+    v = max(v, moved(v, std::integral_constant<int, 0x140>()));
+  }
+  if (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+    v = max((int)r[0], (int)r[1]);
+  }
+  if (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+    v = max((int)r[0], (int)r[1]);
+  }
+  return v;
+}
+template <int L> __device__ __forceinline__ float group_max(float v) { return unordered(group_max<L>(ordered(v))); }
 template <int L> __device__ __forceinline__ float group_sum(float v) {
   return group_join<L>(v, [](float a, float b) { return a + b; });
 }
 // lanes of this lane's group among those of the wave
 template <int L> __device__ __forceinline__ uint64_t group_lanes() {
   const int lane = threadIdx.x & 63;
-  return (L == 64 ? ~0ull : (1ull << L) - 1) << (lane / L * L);
+  return (~0ull >> (64 - L)) << (lane / L * L);
 }
 // LDS written by some lanes of a wave is read by others
 __device__ __forceinline__ void wave_sync() {
@@ -110,14 +180,10 @@ __device__ __forceinline__ void wave_sync() {
 // ---------------------------------------------------------------------------
 // scores
 // ---------------------------------------------------------------------------
-// e^x for x <= 0 within 2 units of its last place, 0 from -104 on: 2^h (1 + r ln 2)
-// for x log2 e = h + r, h in fp32 (a fifth of the instructions of expf; NaN stays NaN)
+// e^x for x <= 0 by the hardware's 2^x (within 1 unit): the argument's rounding makes it |x|
+// roundings, which for the scores e^(l - top) of a token is less than one of the largest
 __device__ __forceinline__ float exp_down(float x) {
-  x = x < -104.f ? -104.f : x;
-  const float h = x * 1.44269502f;  // log2 e = 1.44269502 + 1.9259630e-8
-  const float r = fmaf(x, 1.9259630e-8f, fmaf(x, 1.44269502f, -h));
-  const float v = __builtin_amdgcn_exp2f(h);
-  return fmaf(v, r * 0.693147181f, v);
+  return __builtin_amdgcn_exp2f(fmaf(x, 1.44269502f, x * 1.9259630e-8f));  // the two parts of log2 e
 }
 __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }  // within 1 unit
 
@@ -158,98 +224,143 @@ template <bool SIGMOID, int N, int L> __device__ __forceinline__ float scores(co
 // ---------------------------------------------------------------------------
 // choice
 // ---------------------------------------------------------------------------
-// The k largest of a token's keys, one after the other, equal ones by index: index and
-// key to id[j], val[j], -1 and -inf where none is left.  Returns how many there were.
-//
-// With gap > 0 the keys are off by rounding: two of them are `close` if they are less than
-// gap (sizes + 1/8 of the largest size of a key) apart, else their order is right.  Then the
-// keys that come next are taken too, at most kNext, until one is not close to the k-th:
-// the first k in the right order are among these `taken` ones, unless `more`.
-constexpr int kNext = 16;
-struct Closeness {
-  float gap, sizes;
-  bool close, more;
-  int taken;
-};
-template <int N, int L, bool GAPS>
-__device__ __forceinline__ int choose(float (&key)[N], int k, int sub, int32_t *id, float *val, Closeness &c) {
+// fp32 keys of scores with a bias are off by rounding: the scores, at most `size`, by less
+// than 44 roundings of it (5 of the exponential; its sum's 4 + ln 1024 of the terms and 22
+// of adding; the quotient's), the keys by one of their own.  Two that are further apart
+// than this are in the order of the exact ones.
+__device__ __forceinline__ float key_margin(float size, float a, float b) {
+  return 0x1p-24f * (96.f * size + 8.f * fmaxf(fabsf(a), fabsf(b)));
+}
+// The key in 64 bits; `all`: the sum of e^(l - top)
+template <bool SIGMOID> __device__ __forceinline__ double exact_key(float l, float top, double all, float bias) {
+  const double x = (double)l;
+  const double s = SIGMOID ? (x >= 0 ? 1.0 : exp(x)) / (1.0 + exp(-fabs(x))) : exp(x - (double)top) / all;
+  return s + (double)bias;
+}
+template <int N, int L> __device__ __forceinline__ double exact_sum(const float (&l)[N], float top) {
+  double all = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) all += l[i] > -INFINITY ? exp((double)l[i] - (double)top) : 0.0;
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) all += __shfl_xor(all, off, 64);
+  return all;
+}
+template <int N, bool SIGMOID> __device__ __forceinline__ void exact_keys(const float (&l)[N], const float (&bias)[N], float top,
+                                                                          double all, double (&key)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    key[i] = l[i] > -INFINITY ? exact_key<SIGMOID>(l[i], top, all, bias[i]) : -(double)INFINITY;
+    if (!(key[i] > -(double)INFINITY)) key[i] = -(double)INFINITY;
+  }
+}
+// fp32 keys: logits, or scores s `whole` with the bias; -inf (kNever) for what is never chosen
+template <int N, bool BIAS> __device__ __forceinline__ void make_keys(const float (&l)[N], const float (&s)[N], float whole,
+                                                                      const float (&bias)[N], float (&key)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float v = BIAS ? fmaf(s[i], whole, bias[i]) : l[i];
+    key[i] = l[i] > -INFINITY && v == v ? v : -INFINITY;
+  }
+}
+
+// fp32 keys as whole numbers in the same order (both zeros alike), which take fewer
+// instructions; never chosen: kNever
+constexpr int kNever = INT32_MIN;
+__device__ __forceinline__ int key_of(float f) { return f > -INFINITY ? ordered(f + 0.f) : kNever; }
+
+__device__ __forceinline__ bool never(int key) { return key == kNever; }
+__device__ __forceinline__ bool never(double key) { return !(key > -(double)INFINITY); }
+__device__ __forceinline__ void take(int &key) { key = kNever; }
+__device__ __forceinline__ void take(double &key) { key = -(double)INFINITY; }
+template <int L> __device__ __forceinline__ double group_max(double v) {
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) {
+    const double o = __shfl_xor(v, off, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// Whether this lane is the first of its group among those of the wave's mask
+template <int L> __device__ __forceinline__ bool first_of_group(uint64_t mask) {
+  const unsigned lo = (unsigned)mask, hi = (unsigned)(mask >> 32);
+  if (L == 64) return __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0)) == 0;
   const int lane = threadIdx.x & 63;
-  const uint64_t group = group_lanes<L>();
-  const int rounds = GAPS ? k + kNext : k;
-  int found = 0, taken = 0;
-  float first = 0.f, last = INFINITY, kth = 0.f, least = INFINITY;
-  bool on = true;
-  for (int j = 0; j < rounds; ++j) {
-    float best = key[0];
+  const unsigned up_to = (lane < 32 ? lo : hi) << (31 - (lane & 31));  // this lane's bit is the highest
+  return (up_to & 0x7fffffffu) >> (31 - lane % L) == 0;
+}
+
+// The largest of a token's keys, of equal ones the first, as choice j: its index and (fp32
+// keys) itself to id[j] and val[j], if `write`.  It is taken out of the keys.  Returns
+// whether there was one.
+template <int N, int L, typename K>
+__device__ __forceinline__ bool choose_one(K (&key)[N], int j, int sub, int32_t *id, float *val, bool write) {
+  K best = key[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) best = fmaxf(best, key[i]);
-    const float top = group_max<L>(best);
-    const bool some = top > -INFINITY;
-    if (GAPS) {
-      if (j == 0) first = top;
-      const float margin = c.gap * (c.sizes + 0.125f * fmaxf(fabsf(first), fabsf(top)));
-      if (j >= k) {
-        on = on && some && !(kth - top > margin);
-        if (__ballot(on) == 0) break;
-      }
-      if (some && on && !(last - top > margin)) least = 0.f;
-      last = top;
-      if (j == k - 1) kth = top;
+  for (int i = 1; i < N; ++i) best = key[i] > best ? key[i] : best;
+  const K top = group_max<L>(best);
+  const bool some = !never(top), mine = some && best == top;
+  const uint64_t who = __ballot(mine);
+  if (mine && first_of_group<L>(who)) {
+    int at = N - 1;
+#pragma unroll
+    for (int i = N - 2; i >= 0; --i) at = key[i] == top ? i : at;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      K gone;
+      take(gone);
+      key[i] = at == i ? gone : key[i];
     }
-    const uint64_t who = __ballot(some && best == top) & group;
-    if (on && some && __ffsll((unsigned long long)who) - 1 == lane) {
-      int at = 0;
-      bool hit = false;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool now = key[i] == top && !hit;
-        key[i] = now ? -INFINITY : key[i];
-        at = now ? i : at;
-        hit = hit || now;
-      }
+    if (write) {
       id[j] = sub * N + at;
-      val[j] = top;
-    } else if (!some && j < k && sub == 0) {
-      id[j] = -1;
-      val[j] = -INFINITY;
+      if (sizeof(K) == 4) val[j] = unordered((int)top);
     }
-    if (j < k) found += some;
-    taken += some && on;
   }
-  if (GAPS) {
-    c.close = least == 0.f;
-    c.taken = taken;
-    c.more = c.close && on && taken == k + kNext;
-  }
+  return some;
+}
+// The k largest, one after the other; how many there were
+template <int N, int L, typename K>
+__device__ __forceinline__ int choose(K (&key)[N], int k, int sub, int32_t *id, float *val, bool write) {
+  int found = 0;
+  for (int j = 0; j < k; ++j) found += choose_one<N, L, K>(key, j, sub, id, val, write);
   return found;
 }
 
-// The same with keys in 64 bits.
-template <int N, int L> __device__ __forceinline__ void choose64(double (&key)[N], int k, int sub, int32_t *id, bool write) {
-  const int lane = threadIdx.x & 63;
+// The same with fp32 keys of scores with a bias.  Where two that follow each other are too
+// near to tell (`close`), the first k in the right order are among them and those that come
+// next, until one is far enough from the k-th: these are taken too (`taken` in all), at most
+// kNext of them; `more`: there are more.
+constexpr int kNext = 16;
+struct Closeness {
+  bool close, more;
+  int taken;
+};
+template <int N, int L>
+__device__ __forceinline__ int choose_near(int (&key)[N], int k, int sub, int32_t *id, float *val, float size, Closeness &c) {
   const uint64_t group = group_lanes<L>();
-  for (int j = 0; j < k; ++j) {
-    double best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    double top = best;
-#pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) top = fmax(top, __shfl_xor(top, off, 64));
-    const bool some = top > -(double)INFINITY;
-    const uint64_t who = __ballot(some && best == top) & group;
-    const bool won = some && __ffsll((unsigned long long)who) - 1 == lane;
-    if (won) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i == at) key[i] = -(double)INFINITY;
+  c.taken = choose<N, L, int>(key, k, sub, id, val, true);
+  const int found = c.taken;
+  // one that comes next tells how close the k-th is to it
+  bool on = choose_one<N, L, int>(key, k, sub, id, val, true);
+  c.taken += on;
+  wave_sync();
+  const float margin = c.taken > 0 ? key_margin(size, val[0], val[c.taken - 1]) : 0.f;
+  bool near = false;
+  for (int j = sub; j + 1 < c.taken; j += L) near = near || !(val[j] - val[j + 1] > margin);
+  c.close = (__ballot(near) & group) != 0;
+  on = on && !(val[k - 1] - val[k] > margin);
+  c.more = false;
+  for (int j = k + 1; __ballot(on) != 0; ++j) {
+    if (j == k + kNext) {
+      c.more = on;
+      break;
     }
-    if (write && (won || (!some && sub == 0))) id[j] = some ? sub * N + at : -1;
+    on = choose_one<N, L, int>(key, j, sub, id, val, on) && on;
+    wave_sync();
+    c.taken += on;
+    on = on && !(val[k - 1] - val[j] > margin);
   }
+  return found;
 }
 
 struct BalanceRow {  // a workgroup's sum and count of an expert; behind the last one, its tokens
@@ -258,136 +369,146 @@ struct BalanceRow {  // a workgroup's sum and count of an expert; behind the las
 };
 static int64_t balance_pitch(int E) { return (E + 2) / 2 * 2; }
 
-// LDS of a token: the chosen experts and what chose them; with a bias also those that
-// come next, their exact keys and the order of these
-static __host__ __device__ int route_kept(int k, int E, bool bias) { return bias ? (k + kNext < E ? k + kNext : E) : k; }
-static __host__ __device__ int route_room(int k, int E, bool bias) { return route_kept(k, E, bias) * (bias ? 20 : 8); }
+// What a workgroup adds up for the balance loss
+__device__ __forceinline__ void balance_clear(const RouteArgs &p, int32_t *count) {
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) count[e] = 0;
+  __syncthreads();
+}
+// The groups' sums: one group after the other in a wave, then the waves', whose sums of
+// expert e lie at (e % N) L + e / N of their rows of `sums`, so that lanes write next to each other.
+template <int N, int L>
+__device__ __forceinline__ void balance_store(const RouteArgs &p, float (&acc)[N], const int32_t *count, float *sums, BalanceRow *to) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int off = L; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off, 64);
+  }
+  __syncthreads();
+  const int wave = threadIdx.x / 64, waves = blockDim.x / 64, lane = threadIdx.x & 63;
+  if (lane < L) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[(wave * N + i) * L + lane] = acc[i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    float v = 0.f;
+    if (e < p.E)
+      for (int w = 0; w < waves; ++w) v += sums[(w * N + e % N) * L + e / N];
+    to[e] = BalanceRow{v, count[e]};
+  }
+}
 
-template <int N> constexpr int kBalanceThreads = N > 8 ? 512 : 1024;
+// The weight of a chosen expert with logit x.  `high`: score_shift of the largest chosen
+// logit, `whole`: scale / sum of the chosen's shifted scores; not normalised, softmax:
+// the largest logit and scale / sum of all.
+template <bool SIGMOID> __device__ __forceinline__ float chosen_weight(const RouteArgs &p, float x, float high, float whole) {
+  return SIGMOID && !p.normalize ? p.scale * sigmoid(x) : whole * shifted_score<SIGMOID>(x, high);
+}
+
+// ---- several tokens to a wave: up to 256 experts ---------------------------------
+// LDS of a token: the chosen experts and their logits; with a bias also those that come
+// next, their exact keys and the order of these
+static __host__ __device__ int group_kept(int k, int E, bool bias) { return bias ? (k + kNext <= E ? k + kNext : E + 1) : k; }
+static __host__ __device__ int group_room(int k, int E, bool bias) { return group_kept(k, E, bias) * (bias ? 20 : 8); }
 
 template <int N, int L, bool SIGMOID, bool BIAS>
-__global__ void __launch_bounds__(kBalanceThreads<N>) expert_route_kernel(RouteArgs p, BalanceRow *__restrict__ rows, int64_t pitch) {
+__global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, BalanceRow *__restrict__ rows, int64_t pitch) {
   extern __shared__ __attribute__((aligned(16))) char room[];
-  __shared__ int32_t count[NSG_MAX_EXPERTS + 1];
-  __shared__ float total[NSG_MAX_EXPERTS];
+  __shared__ int32_t count[N * L + 1];
   const int tokens = blockDim.x / L;
   const int sub = threadIdx.x % L, token = threadIdx.x / L, e0 = sub * N;
-  const int kept = route_kept(p.k, p.E, BIAS);
+  const int kept = group_kept(p.k, p.E, BIAS);
   double *const exact = reinterpret_cast<double *>(room) + (BIAS ? token * kept : 0);
   int32_t *const id = reinterpret_cast<int32_t *>(room + (BIAS ? tokens * kept * 8 : 0)) + token * kept;
   float *const val = reinterpret_cast<float *>(id + tokens * kept);
   int32_t *const sorted = id + 2 * tokens * kept;  // (BIAS)
-  constexpr bool softmax = !SIGMOID;
   const bool balance = rows != nullptr;
-  if (balance) {
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) count[e] = 0;
-    __syncthreads();
-  }
+  if (balance) balance_clear(p, count);
   float acc[N], bias[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    acc[i] = 0.f;
-    bias[i] = BIAS && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
-  }
-  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < p.T; t0 += (int64_t)gridDim.x * tokens) {
+  for (int i = 0; i < N; ++i) acc[i] = bias[i] = 0.f;
+  if (BIAS) load_as(p.bias, e0, p.E, bias);
+  // the next tokens' logits are on their way while these are worked on
+  const int64_t step = (int64_t)gridDim.x * tokens;
+  Logits<N> next;
+  int counts = 0;
+  auto fetch = [&](int64_t t) {
+    counts = t < p.T && (p.mask == nullptr || p.mask[t]);
+    next.load(p, t < p.T ? t : 0, e0);
+  };
+  fetch((int64_t)blockIdx.x * tokens + token);
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < p.T; t0 += step) {
     const int64_t t = t0 + token;
-    const bool there = t < p.T && (p.mask == nullptr || p.mask[t]);
-    float l[N];
-    if (there) {
-      load_logits<N>(p, t, e0, l);
-    } else {
+    float l[N], s[N], key[N];
+    next.get(p, l);
 #pragma unroll
-      for (int i = 0; i < N; ++i) l[i] = -INFINITY;
-    }
+    for (int i = 0; i < N; ++i) l[i] = counts ? l[i] : -INFINITY;
+    if (t0 + step < p.T) fetch(t + step);
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, l[i]);
     top = group_max<L>(top);
     if (!(top > -INFINITY)) top = 0.f;
     const float shift = score_shift<SIGMOID>(top);
-    float s[N], sum = 0.f;
-    if (balance || BIAS || softmax) sum = scores<SIGMOID, N, L>(l, shift, s);
-    int found;
-    if (BIAS) {
-      float key[N];
-      const float whole = softmax ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
+    float sum = 0.f, unit = 1.f;
+    if (balance || BIAS || !SIGMOID) sum = scores<SIGMOID, N, L>(l, shift, s);
+    if (BIAS) unit = !SIGMOID ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
+    make_keys<N, BIAS>(l, s, unit, bias, key);
+    int found, whole_key[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float v = fmaf(s[i], whole, bias[i]);
-        key[i] = l[i] > -INFINITY && v == v ? v : -INFINITY;
-      }
-      // Scores, at most `whole` times the largest shifted one, are off by less than 32
-      // roundings of that, with the bias by one of the key.
-      Closeness c{64.f * 0x1p-24f, softmax ? whole : 1.f, false, false, 0};
-      found = choose<N, L, true>(key, p.k, sub, id, val, c);
+    for (int i = 0; i < N; ++i) whole_key[i] = key_of(key[i]);
+    if (BIAS) {
+      Closeness c;
+      found = choose_near<N, L>(whole_key, p.k, sub, id, val, SIGMOID ? 1.f : unit, c);
       if (__ballot(c.close) != 0) {
         // keys in 64 bits: of the taken experts, or all where the next ones did not end
-        double all = 1.0;
-        if (softmax) {
-          all = 0;
-#pragma unroll
-          for (int i = 0; i < N; ++i) all += l[i] > -INFINITY ? exp((double)l[i] - (double)top) : 0.0;
-#pragma unroll
-          for (int off = L / 2; off >= 1; off >>= 1) all += __shfl_xor(all, off, 64);
-        }
-        auto key64 = [&](float x, float b) {
-          const double v = (double)x;
-          return (softmax ? exp(v - (double)top) / all : (v >= 0 ? 1.0 : exp(v)) / (1.0 + exp(-fabs(v)))) + (double)b;
-        };
+        const double all = SIGMOID ? 1.0 : exact_sum<N, L>(l, top);
+        const bool few = c.close && !c.more;
+        for (int j = sub; few && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(logit(p, t, id[j]), top, all, p.bias[id[j]]);
         wave_sync();
-        if (c.close && !c.more) {
-          for (int j = sub; j < c.taken; j += L) exact[j] = key64(logit(p, t, id[j]), p.bias[id[j]]);
+        for (int j = sub; few && j < c.taken; j += L) {
+          int rank = 0;
+          for (int i = 0; i < c.taken; ++i) rank += exact[i] > exact[j] || (exact[i] == exact[j] && id[i] < id[j]);
+          sorted[rank] = id[j];
         }
         wave_sync();
-        if (c.close && !c.more) {
-          for (int j = sub; j < c.taken; j += L) {
-            int rank = 0;
-            for (int i = 0; i < c.taken; ++i) rank += exact[i] > exact[j] || (exact[i] == exact[j] && id[i] < id[j]);
-            sorted[rank] = id[j];
-          }
-        }
-        wave_sync();
-        if (c.close && !c.more) {
-          for (int j = sub; j < found; j += L) id[j] = sorted[j];
-        }
+        for (int j = sub; few && j < found; j += L) id[j] = sorted[j];
         if (__ballot(c.more) != 0) {
-          double whole64[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) whole64[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? key64(l[i], bias[i]) : -(double)INFINITY;
+          double key64[N];
+          exact_keys<N, SIGMOID>(l, bias, top, all, key64);
           wave_sync();
-          choose64<N, L>(whole64, p.k, sub, id, c.more);
+          choose<N, L, double>(key64, p.k, sub, id, val, c.more);
         }
+        wave_sync();
       }
-      wave_sync();
       for (int j = sub; j < found; j += L) val[j] = logit(p, t, id[j]);
     } else {
-      float key[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) key[i] = l[i] == l[i] ? l[i] : -INFINITY;
-      Closeness c{};
-      found = choose<N, L, false>(key, p.k, sub, id, val, c);
+      found = choose<N, L, int>(whole_key, p.k, sub, id, val, true);
     }
     wave_sync();
-    // the weights, a choice to a lane; with softmax a NaN among the logits is in all of them
-    float high = -INFINITY, whole = 0.f;
+    // a choice to a lane
+    float high = top, whole = 0.f;
     if (p.normalize) {
-      for (int j = sub; j < found; j += L) high = fmaxf(high, val[j]);
-      high = score_shift<SIGMOID>(group_max<L>(high));
+      if (BIAS) {
+        high = -INFINITY;
+        for (int j = sub; j < found; j += L) high = fmaxf(high, val[j]);
+        high = group_max<L>(high);
+      }
+      high = score_shift<SIGMOID>(high);
       for (int j = sub; j < found; j += L) whole += shifted_score<SIGMOID>(val[j], high);
-      whole = p.scale / group_sum<L>(whole);
-    } else {
-      whole = softmax ? p.scale / sum : p.scale;
+      whole = p.scale * inverse_sum(group_sum<L>(whole));
+    } else if (!SIGMOID) {
+      whole = p.scale * inverse_sum(sum);
     }
     if (t < p.T) {
       for (int j = sub; j < p.k; j += L) {
         float w = 0.f;
         if (j < found) {
-          const float x = val[j];
-          w = whole * (p.normalize ? shifted_score<SIGMOID>(x, high) : softmax ? exp_down(x - top) : sigmoid(x));
-          if (softmax && sum != sum) w = sum;
+          w = chosen_weight<SIGMOID>(p, val[j], high, whole);
+          if (!SIGMOID && sum != sum) w = sum;  // with softmax a NaN among the logits is in all weights
           if (balance) atomicAdd(&count[id[j]], 1);
         }
-        p.ids[t * p.k + j] = id[j];
+        p.ids[t * p.k + j] = j < found ? id[j] : -1;
         p.weights[t * p.k + j] = w;
       }
     }
@@ -399,86 +520,338 @@ __global__ void __launch_bounds__(kBalanceThreads<N>) expert_route_kernel(RouteA
     }
     wave_sync();
   }
-  if (!balance) return;
-  // the groups' sums, one group after the other in a wave, one wave after the other
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float v = acc[i];
-#pragma unroll
-    for (int off = L; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
-    acc[i] = v;
-  }
-  for (int w = 0; w < (int)blockDim.x / 64; ++w) {
-    if ((int)threadIdx.x / 64 == w && (threadIdx.x & 63) < L) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (e0 + i < p.E) total[e0 + i] = w == 0 ? acc[i] : total[e0 + i] + acc[i];
-    }
-    __syncthreads();
-  }
-  BalanceRow *to = rows + (int64_t)blockIdx.x * pitch;
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) to[e] = BalanceRow{e < p.E ? total[e] : 0.f, count[e]};
+  if (balance) balance_store<N, L>(p, acc, count, reinterpret_cast<float *>(room), rows + (int64_t)blockIdx.x * pitch);
 }
 
-// One workgroup: groups of `pitch / 2` threads share the rows, a thread two experts of them.
-__global__ void __launch_bounds__(1024) expert_balance_kernel(RouteArgs p, int blocks, const BalanceRow *__restrict__ rows,
-                                                              int64_t pitch) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  __shared__ float fs[2][1024];
-  __shared__ int is[2][1024];
-  __shared__ float part[16];
-  __shared__ int tokens;
-  const int units = (int)pitch / 2, share = 1024 / units, u = (int)threadIdx.x % units, g = (int)threadIdx.x / units;
-  float a0 = 0.f, a1 = 0.f;
-  int n0 = 0, n1 = 0;
+// ---- a token to a wave -----------------------------------------------------------
+__device__ __forceinline__ int wave_max(int v) { return __builtin_amdgcn_readfirstlane(group_max<64>(v)); }
+__device__ __forceinline__ float wave_max(float v) { return unordered(wave_max(ordered(v))); }
+
+// What a wave chooses from: the keys of at least `from`, their experts and logits
+struct Candidate {
+  float key;
+  int32_t id;
+  float logit;
+};
+constexpr int kCandidates = 64;  // one to a lane
+// How many of the n candidates, one to a lane, come before this lane's
+__device__ __forceinline__ int candidate_rank(const Candidate &mine, int n) {
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const float key = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine.key), j));
+    const int id = __builtin_amdgcn_readlane(mine.id, j);
+    rank += key > mine.key || (key == mine.key && id < mine.id);
+  }
+  return rank;
+}
+
+// A bound that at least `need` and hardly more of the lanes' largest keys are not below: so
+// many keys, and a few more, are not below it.  -inf where no more than `need` lanes have a key.
+__device__ __forceinline__ float candidate_bound(float best, float top, int need) {
+  int lo = ~wave_max(best > -INFINITY ? ~ordered(best) : INT32_MIN);  // the smallest
+  if (__popcll(__ballot(best > -INFINITY)) <= need) return -INFINITY;
+  int hi = ordered(top) + 1;  // (of +inf too)
+  while ((unsigned)hi - (unsigned)lo > 1u) {  // at least `need` are not below lo, fewer not below hi
+    const int mid = (int)((unsigned)lo + ((unsigned)hi - (unsigned)lo) / 2);
+    const int n = __popcll(__ballot(best >= unordered(mid)));
+    if (n < need) {
+      hi = mid;
+    } else {
+      lo = mid;
+      if (n <= need + 4) break;
+    }
+  }
+  return unordered(lo);
+}
+template <int N>
+__device__ __forceinline__ int gather_candidates(const float (&key)[N], const float (&l)[N], int e0, float from, Candidate *c) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool in = key[i] > -INFINITY && !(key[i] < from);
+    const uint64_t who = __ballot(in);
+    if (who != 0) {
+      const int at = n + (int)__builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
+      if (in && at < kCandidates) c[at] = Candidate{key[i], e0 + i, l[i]};
+      n += __popcll(who);
+    }
+  }
+  return n;
+}
+
+// threads of a workgroup, by the registers that a thread needs
+template <int N, bool BIAS> constexpr int kWaveThreads() { return N > (BIAS ? 4 : 8) ? 512 : 1024; }
+
+template <int N, bool SIGMOID, bool BIAS>
+__global__ void __launch_bounds__((kWaveThreads<N, BIAS>())) expert_route_kernel(RouteArgs p, BalanceRow *__restrict__ rows, int64_t pitch) {
+  extern __shared__ float sums[];  // the waves' sums
+  __shared__ Candidate cands[kWaveThreads<N, BIAS>() / 64][kCandidates];
+  __shared__ int32_t ids[kWaveThreads<N, BIAS>() / 64][kCandidates];
+  __shared__ float vals[kWaveThreads<N, BIAS>() / 64][kCandidates];  // the chosen's logits
+  __shared__ float sorted[BIAS ? kWaveThreads<N, BIAS>() / 64 : 1][kCandidates];  // and keys
+  __shared__ double exact[BIAS ? kWaveThreads<N, BIAS>() / 64 : 1][kCandidates];
+  __shared__ int32_t count[NSG_MAX_EXPERTS + 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e0 = lane * N;
+  Candidate *const cand = cands[wave];
+  int32_t *const id = ids[wave];
+  float *const val = vals[wave];
+  float *const skey = sorted[BIAS ? wave : 0];
+  double *const key64 = exact[BIAS ? wave : 0];
+  const bool balance = rows != nullptr;
+  if (balance) balance_clear(p, count);
+  float acc[N], bias[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = bias[i] = 0.f;
+  if (BIAS) load_as(p.bias, e0, p.E, bias);
+  // the next token's logits are on their way while one is worked on
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / 64);
+  Logits<N> next;
+  int counts = 1;
+  auto fetch = [&](int64_t t) {
+    if (p.mask != nullptr) counts = p.mask[t];
+    next.load(p, t, e0);
+  };
+  // A token's results are stored in the next one's turn: what waits for the logits would wait
+  // for these stores too.
+  int64_t done = -1;
+  int32_t out_id = 0;
+  float out_weight = 0.f;
+  auto store = [&]() {
+    if (done >= 0 && lane < p.k) {
+      p.ids[done * p.k + lane] = out_id;
+      p.weights[done * p.k + lane] = out_weight;
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * (blockDim.x / 64) + wave;
+  if (t < p.T) fetch(t);
+  for (; t < p.T; t += step) {
+    float l[N], s[N], key[N];
+    next.get(p, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = counts ? l[i] : -INFINITY;
+    store();
+    if (t + step < p.T) fetch(t + step);
+    float best = l[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = fmaxf(best, l[i]);
+    float top = wave_max(best);
+    if (!(top > -INFINITY)) top = 0.f;
+    const float shift = score_shift<SIGMOID>(top);
+    float sum = 0.f, unit = 1.f;
+    if (balance || BIAS || !SIGMOID) sum = scores<SIGMOID, N, 64>(l, shift, s);
+    if (BIAS) unit = !SIGMOID ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
+    make_keys<N, BIAS>(l, s, unit, bias, key);
+    best = key[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = fmaxf(best, key[i]);
+    const float first = BIAS ? wave_max(best) : top;
+    const int need = BIAS ? p.k + 1 : p.k;  // one more, to see how close it is
+    int n = gather_candidates<N>(key, l, e0, candidate_bound(best, first, need), cand);
+    int found = n < p.k ? n : p.k;
+    wave_sync();
+    if (n <= kCandidates) {
+      // the candidates in order, one to a lane
+      Candidate mine = cand[lane < n ? lane : 0];
+      int rank = candidate_rank(mine, n);
+      if (lane < n) {
+        id[rank] = mine.id;
+        val[rank] = mine.logit;
+        if (BIAS) skey[rank] = mine.key;
+      }
+      if (BIAS) {
+        wave_sync();
+        const int last = n < need ? n - 1 : p.k;
+        const float margin = n > 1 ? key_margin(SIGMOID ? 1.f : unit, skey[0], skey[last]) : 0.f;
+        const int at = lane < last ? lane : 0;
+        const uint64_t close = __ballot(lane < last && !(skey[at] - skey[at + 1 < 64 ? at + 1 : 63] > margin));
+        if (close != 0) {
+          // exact keys: of all that may be among the first k, if they are no more than the lanes
+          if (last == p.k && (close >> (p.k - 1) & 1)) {
+            const float from = skey[p.k - 1] - 2.f * margin;
+            wave_sync();
+            n = gather_candidates<N>(key, l, e0, from, cand);
+            wave_sync();
+          }
+          const double all = SIGMOID ? 1.0 : exact_sum<N, 64>(l, top);
+          if (n <= kCandidates) {
+            mine = cand[lane < n ? lane : 0];
+            const double x = exact_key<SIGMOID>(mine.logit, top, all, p.bias[mine.id]);
+            if (lane < n) key64[lane] = x;
+            wave_sync();
+            rank = 0;
+            for (int j = 0; j < n; ++j) rank += key64[j] > x || (key64[j] == x && cand[j].id < mine.id);
+            if (lane < n && rank < p.k) {
+              id[rank] = mine.id;
+              val[rank] = mine.logit;
+            }
+          } else {
+            double keys64[N];
+            exact_keys<N, SIGMOID>(l, bias, top, all, keys64);
+            choose<N, 64, double>(keys64, p.k, lane, id, val, true);
+            wave_sync();
+            if (lane < found) val[lane] = logit(p, t, id[lane]);
+          }
+        }
+      }
+    } else if (BIAS) {  // many equal or nearly equal keys, or k near 64
+      double keys64[N];
+      exact_keys<N, SIGMOID>(l, bias, top, SIGMOID ? 1.0 : exact_sum<N, 64>(l, top), keys64);
+      found = choose<N, 64, double>(keys64, p.k, lane, id, val, true);
+      wave_sync();
+      if (lane < found) val[lane] = logit(p, t, id[lane]);
+    } else {
+      int whole_key[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) whole_key[i] = key_of(key[i]);
+      found = choose<N, 64, int>(whole_key, p.k, lane, id, val, true);
+    }
+    wave_sync();
+    // a choice to a lane
+    const bool in = lane < found;
+    const float x = in ? val[lane] : -INFINITY;
+    float high = top, whole = 0.f;
+    if (p.normalize) {
+      high = score_shift<SIGMOID>(BIAS ? wave_max(x) : top);
+      whole = p.scale / wave_sum(in ? shifted_score<SIGMOID>(x, high) : 0.f);
+    } else if (!SIGMOID) {
+      whole = p.scale / sum;
+    }
+    done = t;
+    out_id = in ? id[lane] : -1;
+    out_weight = in ? chosen_weight<SIGMOID>(p, x, high, whole) : 0.f;
+    if (!SIGMOID && in && sum != sum) out_weight = sum;  // with softmax a NaN among the logits is in all weights
+    if (balance) {
+      if (in) atomicAdd(&count[out_id], 1);
+      if (found > 0) {
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+        if (lane == 0) atomicAdd(&count[p.E], 1);
+      }
+    }
+    wave_sync();
+  }
+  store();
+  if (balance) balance_store<N, 64>(p, acc, count, sums, rows + (int64_t)blockIdx.x * pitch);
+}
+
+// Sums of the rows of experts 2 u and 2 u + 1 (behind the last one, the tokens): `units`
+// threads side by side, 1024 / units of them for a unit, which share the rows and join
+// their sums in halves.  In the first ones' results.
+struct BalancePair {
+  float a0, a1;
+  int n0, n1;
+};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ BalancePair balance_sum(const BalanceRow *__restrict__ rows, int blocks, int64_t pitch, int unit,
+                                                   int units, BalancePair *sh) {
+  const int share = 1024 / units, g = (int)threadIdx.x / units;
+  BalancePair r{0.f, 0.f, 0, 0};
   if (g < share) {
     for (int b0 = g; b0 < blocks; b0 += 16 * share) {
       u32x4 v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int b = b0 + i * share;
-        v[i] = b < blocks ? *reinterpret_cast<const u32x4 *>(rows + (int64_t)b * pitch + 2 * u) : u32x4(0);
+        v[i] = b < blocks ? *reinterpret_cast<const u32x4 *>(rows + (int64_t)b * pitch + 2 * unit) : u32x4(0);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        a0 += __uint_as_float(v[i][0]);
-        n0 += (int)v[i][1];
-        a1 += __uint_as_float(v[i][2]);
-        n1 += (int)v[i][3];
+        r.a0 += __uint_as_float(v[i][0]);
+        r.n0 += (int)v[i][1];
+        r.a1 += __uint_as_float(v[i][2]);
+        r.n1 += (int)v[i][3];
       }
     }
   }
-  fs[0][threadIdx.x] = a0;
-  fs[1][threadIdx.x] = a1;
-  is[0][threadIdx.x] = n0;
-  is[1][threadIdx.x] = n1;
-  __syncthreads();
-  const bool mine = g == 0 && u < units;
-  if (mine) {
-    for (int i = 1; i < share; ++i) {
-      a0 += fs[0][i * units + u];
-      a1 += fs[1][i * units + u];
-      n0 += is[0][i * units + u];
-      n1 += is[1][i * units + u];
+  for (int n = share; n > 1;) {
+    const int half = (n + 1) / 2;
+    if (g < n) sh[threadIdx.x] = r;
+    __syncthreads();
+    if (g + half < n) {
+      const BalancePair o = sh[threadIdx.x + half * units];
+      r.a0 += o.a0;
+      r.a1 += o.a1;
+      r.n0 += o.n0;
+      r.n1 += o.n1;
     }
-    if (2 * u == p.E) tokens = n0;
-    if (2 * u + 1 == p.E) tokens = n1;
+    __syncthreads();
+    n = half;
   }
+  return r;
+}
+
+// 16 experts to a workgroup, which has 128 threads for each two of them: one row of the
+// rows' sums
+__global__ void __launch_bounds__(1024) expert_balance_rows_kernel(int blocks, const BalanceRow *__restrict__ rows, int64_t pitch,
+                                                                   BalanceRow *__restrict__ out) {
+  __shared__ BalancePair sh[16][8];
+  const int wave = threadIdx.x / 64, unit = (int)blockIdx.x * 8 + (int)threadIdx.x % 8, units = (int)pitch / 2;
+  BalancePair r{0.f, 0.f, 0, 0};
+  if (unit < units) {
+    u32x4 v[kBalanceBlocks / 128];
+#pragma unroll
+    for (int i = 0; i < kBalanceBlocks / 128; ++i) {
+      const int b = (int)threadIdx.x / 8 + i * 128;
+      v[i] = b < blocks ? *reinterpret_cast<const u32x4 *>(rows + (int64_t)b * pitch + 2 * unit) : u32x4(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBalanceBlocks / 128; ++i) {
+      r.a0 += __uint_as_float(v[i][0]);
+      r.n0 += (int)v[i][1];
+      r.a1 += __uint_as_float(v[i][2]);
+      r.n1 += (int)v[i][3];
+    }
+  }
+#pragma unroll
+  for (int off = 8; off < 64; off <<= 1) {
+    r.a0 += __shfl_xor(r.a0, off, 64);
+    r.n0 += __shfl_xor(r.n0, off, 64);
+    r.a1 += __shfl_xor(r.a1, off, 64);
+    r.n1 += __shfl_xor(r.n1, off, 64);
+  }
+  if ((threadIdx.x & 63) < 8) sh[wave][threadIdx.x & 63] = r;
+  __syncthreads();
+  if (threadIdx.x < 8 && unit < units) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) {
+      const BalancePair o = sh[w][threadIdx.x];
+      r.a0 += o.a0;
+      r.n0 += o.n0;
+      r.a1 += o.a1;
+      r.n1 += o.n1;
+    }
+    out[2 * unit] = BalanceRow{r.a0, r.n0};
+    out[2 * unit + 1] = BalanceRow{r.a1, r.n1};
+  }
+}
+
+// One workgroup: counts, probs and loss
+__global__ void __launch_bounds__(1024) expert_balance_kernel(RouteArgs p, int blocks, const BalanceRow *__restrict__ rows,
+                                                              int64_t pitch) {
+  __shared__ BalancePair sh[1024];
+  __shared__ float part[16];
+  __shared__ int tokens;
+  const int units = (int)pitch / 2, u = (int)threadIdx.x % units;
+  BalancePair r = balance_sum(rows, blocks, pitch, u, units, sh);
+  const bool mine = (int)threadIdx.x < units;
+  if (mine && 2 * u == p.E) tokens = r.n0;
+  if (mine && 2 * u + 1 == p.E) tokens = r.n1;
   __syncthreads();
   const int N = tokens;
   float v = 0.f;
   if (mine) {
-    a0 = N > 0 ? a0 / (float)N : 0.f;
-    a1 = N > 0 ? a1 / (float)N : 0.f;
+    r.a0 = N > 0 ? r.a0 / (float)N : 0.f;
+    r.a1 = N > 0 ? r.a1 / (float)N : 0.f;
     if (2 * u < p.E) {
-      p.counts[2 * u] = n0;
-      p.probs[2 * u] = a0;
-      v = (float)n0 * a0;
+      p.counts[2 * u] = r.n0;
+      p.probs[2 * u] = r.a0;
+      v = (float)r.n0 * r.a0;
     }
     if (2 * u + 1 < p.E) {
-      p.counts[2 * u + 1] = n1;
-      p.probs[2 * u + 1] = a1;
-      v = fmaf((float)n1, a1, v);
+      p.counts[2 * u + 1] = r.n1;
+      p.probs[2 * u + 1] = r.a1;
+      v = fmaf((float)r.n1, r.a1, v);
     }
   }
   v = wave_sum(v);
@@ -521,32 +894,54 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
   if (p.counts != nullptr) {
     const float n = (float)p.counts[p.E];
     const float f = n > 0.f ? p.balance * (p.dloss != nullptr ? *p.dloss : 1.f) * ((float)p.E / (float)p.k) / n / n : 0.f;
+    load_as(p.counts, e0, p.E, c);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (e0 + i < p.E) c[i] = f * (float)p.counts[e0 + i];
+    for (int i = 0; i < N; ++i) c[i] = e0 + i < p.E ? f * c[i] : 0.f;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kTokens) {
-    const int64_t t = t0 + token;
-    const bool there = t < p.T;
-    // this lane's choices (j = sub, sub + L, ...), and the logits
-    int e[kMine];
-    float g[kMine], x[kMine];
+  // a token's logits and this lane's choices (j = sub, sub + L, ...); the next ones are on
+  // their way while these are worked on
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  Logits<N> next_l;
+  float next_g[kMine];
+  int next_e[kMine];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
       const int j = sub + m * L;
-      const bool in = there && j < p.k;
-      e[m] = in ? p.ids[t * p.k + j] : -1;
-      if (e[m] >= p.E) e[m] = -1;
-      g[m] = in && weights ? p.dweights[t * p.k + j] * p.scale : 0.f;
+      const bool in = t < p.T && j < p.k;
+      next_e[m] = in ? p.ids[t * p.k + j] : -1;
+      next_g[m] = in && weights ? p.dweights[t * p.k + j] : 0.f;
     }
-    float l[N];
-    load_logits<N>(p, there ? t : 0, e0, l);
+    next_l.load(p, t < p.T ? t : 0, e0);
+  };
+  // a token's gradient is stored in the next one's turn: what waits for the logits would
+  // wait for these stores too
+  int64_t done = -1;
+  float out[N];
+  auto store = [&]() {
+    if (done < 0 || e0 >= p.E) return;
+    const int64_t to = done * p.E;
+    if (p.dtype == NSG_F32) store_as((float *)p.dlogits + to, e0, p.E, out);
+    else if (p.dtype == NSG_BF16) store_as((__bf16 *)p.dlogits + to, e0, p.E, out);
+    else store_as((_Float16 *)p.dlogits + to, e0, p.E, out);
+  };
+  fetch((int64_t)blockIdx.x * kTokens + token);
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + token;
+    const bool there = t < p.T;
+    int e[kMine];
+    float l[N], g[kMine], x[kMine];
     bool any = false;
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
+      e[m] = next_e[m] < p.E ? next_e[m] : -1;
+      g[m] = next_g[m] * p.scale;
       any = any || e[m] >= 0;
       x[m] = e[m] >= 0 ? logit(p, t, e[m]) : -INFINITY;
     }
+    next_l.get(p, l);
+    store();
+    if (t0 + step < p.T) fetch(t + step);
     const bool found = (__ballot(any) & group) != 0;
     float top = l[0];
 #pragma unroll
@@ -596,84 +991,113 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
         if (e[m] >= 0) add[token][e[m] % N * L + e[m] / N] = 0.f;
       wave_sync();
     }
-    if (there && e0 < p.E) {
-      const bool full = softmax && !p.normalize && weights;
+    const bool full = softmax && !p.normalize && weights;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float pe = s[i] * sum;
-        if (full) d[i] = pe * (d[i] - dot);
-        if (p.counts != nullptr) d[i] = fmaf(softmax ? pe : pe * sigmoid(-l[i]), c[i] - pc, d[i]);
-        if (!found) d[i] = 0.f;
-      }
-      const int64_t to = t * p.E;
-      if (p.dtype == NSG_F32) store_as((float *)p.dlogits + to, e0, p.E, d);
-      else if (p.dtype == NSG_BF16) store_as((__bf16 *)p.dlogits + to, e0, p.E, d);
-      else store_as((_Float16 *)p.dlogits + to, e0, p.E, d);
+    for (int i = 0; i < N; ++i) {
+      const float pe = s[i] * sum;
+      if (full) d[i] = pe * (d[i] - dot);
+      if (p.counts != nullptr) d[i] = fmaf(softmax ? pe : pe * sigmoid(-l[i]), c[i] - pc, d[i]);
+      out[i] = found ? d[i] : 0.f;
     }
+    done = there ? t : -1;
     wave_sync();
   }
+  store();
 }
 
 // ---------------------------------------------------------------------------
-// workgroups of `threads` for T tokens of so many lanes, at most `most`
-static int64_t route_blocks(int64_t T, int threads, int lanes, int64_t most) {
-  const int64_t tokens = threads / lanes, n = (T + tokens - 1) / tokens;
-  return n < most ? n : most;
-}
-
-// N and L for E experts
-template <class K> static hipError_t by_experts(const RouteArgs &a, hipStream_t s) {
-  const bool few = a.T <= 1024;
-  if (a.E <= 16) return K::template launch<4, 4>(a, s);
-  if (a.E <= 64) return few ? K::template launch<1, 64>(a, s) : K::template launch<4, 16>(a, s);
-  if (a.E <= 128) return few ? K::template launch<2, 64>(a, s) : K::template launch<8, 16>(a, s);
-  if (a.E <= 256) return few ? K::template launch<4, 64>(a, s) : K::template launch<8, 32>(a, s);
-  if (a.E <= 512) return K::template launch<8, 64>(a, s);
-  return K::template launch<16, 64>(a, s);
-}
-
 size_t expert_route_workspace(int64_t T, int E) {
-  return T == 0 ? 0 : (size_t)kBalanceBlocks * (size_t)balance_pitch(E) * sizeof(BalanceRow);
+  return T == 0 ? 0 : (size_t)(kBalanceBlocks + 1) * (size_t)balance_pitch(E) * sizeof(BalanceRow);
 }
 
 struct RouteForward {
-  template <int N, int L> static hipError_t launch(const RouteArgs &a, hipStream_t s) {
+  // Many rows are summed by as many workgroups as there are 16 experts first: one that reads
+  // them all takes 8 us for 256 rows of 256 experts, 14 of 512 and 25 of 1024.
+  static hipError_t join(const RouteArgs &a, int blocks, BalanceRow *rows, int64_t pitch, hipStream_t s) {
+    if (blocks * pitch > 8192) {
+      BalanceRow *sums = rows + kBalanceBlocks * pitch;
+      hipLaunchKernelGGL(expert_balance_rows_kernel, dim3((unsigned)((pitch / 2 + 7) / 8)), dim3(1024), 0, s, blocks,
+                         (const BalanceRow *)rows, pitch, sums);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      rows = sums;
+      blocks = 1;
+    }
+    hipLaunchKernelGGL(expert_balance_kernel, dim3(1), dim3(1024), 0, s, a, blocks, (const BalanceRow *)rows, pitch);
+    return hipGetLastError();
+  }
+  template <class F> static hipError_t with_kernel(const RouteArgs &a, F kernel) {
+    const bool g = a.score == NSG_SCORE_SIGMOID, b = a.bias != nullptr;
+    return g ? b ? kernel(std::true_type(), std::true_type()) : kernel(std::true_type(), std::false_type())
+             : b ? kernel(std::false_type(), std::true_type()) : kernel(std::false_type(), std::false_type());
+  }
+  // threads of a workgroup and the tokens that it takes at a time
+  template <class F> static hipError_t launch(const RouteArgs &a, int threads, int tokens, hipStream_t s, F kernel) {
     const bool balance = a.counts != nullptr;
-    // with the balance loss as many threads as the choices' LDS allows: few rows to join
-    int threads = balance ? kBalanceThreads<N> : kRouteThreads;
-    const int room = route_room(a.k, a.E, a.bias != nullptr);
-    while (threads > 64 && threads / L * room > 48 << 10) threads /= 2;
-    const int64_t pitch = balance_pitch(a.E), blocks = route_blocks(a.T, threads, L, balance ? kBalanceBlocks : 1 << 16);
+    const int64_t pitch = balance_pitch(a.E), need = (a.T + tokens - 1) / tokens, most = balance ? kBalanceBlocks : kRouteBlocks;
+    const int blocks = (int)(need < most ? need : most);
     BalanceRow *rows = balance ? (BalanceRow *)a.workspace : nullptr;
     if (blocks > 0) {
-      const dim3 grid((unsigned)blocks), block(threads);
-      const unsigned lds = (unsigned)(threads / L * room);
-      if (a.score == NSG_SCORE_SIGMOID && a.bias != nullptr)
-        hipLaunchKernelGGL((expert_route_kernel<N, L, true, true>), grid, block, lds, s, a, rows, pitch);
-      else if (a.score == NSG_SCORE_SIGMOID)
-        hipLaunchKernelGGL((expert_route_kernel<N, L, true, false>), grid, block, lds, s, a, rows, pitch);
-      else if (a.bias != nullptr)
-        hipLaunchKernelGGL((expert_route_kernel<N, L, false, true>), grid, block, lds, s, a, rows, pitch);
-      else
-        hipLaunchKernelGGL((expert_route_kernel<N, L, false, false>), grid, block, lds, s, a, rows, pitch);
+      kernel(dim3((unsigned)blocks), dim3((unsigned)threads), rows, pitch);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (!balance) return hipSuccess;
-    hipLaunchKernelGGL(expert_balance_kernel, dim3(1), dim3(1024), 0, s, a, (int)blocks, (const BalanceRow *)rows, pitch);
-    return hipGetLastError();
+    return balance ? join(a, blocks, rows, pitch, s) : hipSuccess;
   }
-};
-struct RouteBackward {
-  template <int N, int L> static hipError_t launch(const RouteArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)route_blocks(a.T, kRouteThreads, L, 1 << 16)), block(kRouteThreads);
-    if (a.score == NSG_SCORE_SIGMOID) hipLaunchKernelGGL((expert_route_backward_kernel<N, L, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((expert_route_backward_kernel<N, L, false>), grid, block, 0, s, a);
-    return hipGetLastError();
+  template <int N, int L> static hipError_t group(const RouteArgs &a, hipStream_t s) {
+    return with_kernel(a, [&](auto sigmoid, auto bias) {
+      constexpr bool S = decltype(sigmoid)::value, B = decltype(bias)::value;
+      const bool balance = a.counts != nullptr;
+      // with the balance loss as many threads as their LDS allows: few rows to join
+      int threads = balance ? 1024 : kRouteThreads;
+      const int room = group_room(a.k, a.E, B);
+      while (threads > 64 && threads / L * room > 48 << 10) threads /= 2;
+      unsigned lds = threads / L * room;
+      if (balance && lds < threads / 64 * N * L * 4u) lds = threads / 64 * N * L * 4u;  // the waves' sums
+      return launch(a, threads, threads / L, s, [&](dim3 grid, dim3 block, BalanceRow *rows, int64_t pitch) {
+        hipLaunchKernelGGL((expert_route_group_kernel<N, L, S, B>), grid, block, lds, s, a, rows, pitch);
+      });
+    });
+  }
+  template <int N> static hipError_t wave(const RouteArgs &a, hipStream_t s) {
+    return with_kernel(a, [&](auto sigmoid, auto bias) {
+      constexpr bool S = decltype(sigmoid)::value, B = decltype(bias)::value;
+      const bool balance = a.counts != nullptr;
+      const int threads = balance ? kWaveThreads<N, B>() : kRouteThreads;
+      const unsigned lds = balance ? threads * N * 4 : 0;
+      return launch(a, threads, threads / 64, s, [&](dim3 grid, dim3 block, BalanceRow *rows, int64_t pitch) {
+        hipLaunchKernelGGL((expert_route_kernel<N, S, B>), grid, block, lds, s, a, rows, pitch);
+      });
+    });
   }
 };
 
-hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s) { return by_experts<RouteForward>(a, s); }
-hipError_t launch_expert_route_backward(const RouteArgs &a, hipStream_t s) { return by_experts<RouteBackward>(a, s); }
+hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s) {
+  if (a.E <= 16) return RouteForward::group<4, 4>(a, s);
+  if (a.E <= 64) return RouteForward::group<4, 16>(a, s);
+  if (a.E <= 128) return RouteForward::group<8, 16>(a, s);
+  if (a.E <= 256) return RouteForward::group<8, 32>(a, s);
+  if (a.E <= 512) return RouteForward::wave<8>(a, s);
+  return RouteForward::wave<16>(a, s);
+}
+
+template <int N, int L> static hipError_t route_backward(const RouteArgs &a, hipStream_t s) {
+  constexpr int tokens = kRouteThreads / L;
+  const int64_t need = (a.T + tokens - 1) / tokens;
+  const dim3 grid((unsigned)(need < kRouteBlocks ? need : kRouteBlocks)), block(kRouteThreads);
+  if (a.score == NSG_SCORE_SIGMOID) hipLaunchKernelGGL((expert_route_backward_kernel<N, L, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((expert_route_backward_kernel<N, L, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_route_backward(const RouteArgs &a, hipStream_t s) {
+  const bool few = a.T <= 1024;
+  if (a.E <= 16) return route_backward<4, 4>(a, s);
+  if (a.E <= 64) return few ? route_backward<1, 64>(a, s) : route_backward<4, 16>(a, s);
+  if (a.E <= 128) return few ? route_backward<2, 64>(a, s) : route_backward<8, 16>(a, s);
+  if (a.E <= 256) return few ? route_backward<4, 64>(a, s) : route_backward<16, 16>(a, s);
+  if (a.E <= 512) return few ? route_backward<8, 64>(a, s) : route_backward<16, 32>(a, s);
+  return route_backward<16, 64>(a, s);
+}
 
 }  // namespace nsg
