@@ -144,11 +144,13 @@ __global__ void __launch_bounds__(1024) embed_clear_kernel(Clear c) { c.run((int
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortBins = 1024;
+constexpr int kSortBits = 10;
+constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortKept = 4;                           // steps of 64 tokens that a wave keeps in registers
 constexpr int kSortChunk = kSortThreads * kSortKept;   // tokens of one workgroup, then
 constexpr int kSortMaxChunks = 128;                    // every workgroup reads the whole table
-constexpr int kSortAlone = 16;                         // steps of a sort by one workgroup
+// Steps of a sort by one workgroup, in LDS: 8192 tokens take 18 us, in four launches 20 (1024: 7)
+constexpr int kSortAlone = 8;
 static_assert(NSG_MAX_VOCAB <= kSortBins * kSortBins, "two digits");
 
 struct SortPlan {
@@ -168,19 +170,21 @@ static SortPlan sort_plan(int64_t N, int64_t V) {
   p.chunks = N == 0 ? 1 : (int)((N + p.chunk - 1) / p.chunk);
   int bits = 1;
   while ((1ll << bits) < V) ++bits;
-  p.digits = bits <= 10 ? 1 : 2;
+  p.digits = bits <= kSortBits ? 1 : 2;
   p.bits = (bits + p.digits - 1) / p.digits;
   return p;
 }
 
+struct Pair {  // a token and its id, -1 behind the last token that has one
+  int key, tok;
+};
 // the tokens before a digit's pass: the ids as they are, or the pairs of the pass before
 struct SortInput {
   const void *ids;
   int wide;
   int64_t V;
-  const int32_t *keys, *toks;  // NULL: ids
-  __device__ __forceinline__ int key(int64_t i) const { return keys ? keys[i] : id_at(ids, wide, i, V); }
-  __device__ __forceinline__ int tok(int64_t i) const { return keys ? toks[i] : (int)i; }
+  const Pair *pairs;  // NULL: ids
+  __device__ __forceinline__ Pair operator()(int64_t i) const { return pairs ? pairs[i] : Pair{id_at(ids, wide, i, V), (int)i}; }
 };
 
 // tokens of each value of the digit in each chunk
@@ -193,33 +197,34 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(SortInput in,
   __syncthreads();
   const int64_t i0 = (int64_t)blockIdx.x * chunk, i1 = min(N, i0 + chunk);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
-    const int k = in.key(i);
+    const int k = in(i).key;
     if (k >= 0) atomicAdd(&count[(k >> shift) & (bins - 1)], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < bins; e += kSortThreads) table[(size_t)blockIdx.x * bins + e] = count[e];
 }
 
-// Place the tokens of chunk `block`.  at[w][d]: where the next token with digit d in
-// wave w's part of the chunk goes.  A wave takes its part 64 tokens at a time: the
-// lanes with the same digit find each other by ballots over its bits, so their order
-// is that of the tokens.  KEPT: steps of 64 tokens a wave keeps, 0: it reads them again.
-template <int KEPT>
-__device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int64_t chunk, int chunks, int block, int shift,
-                                            int bits, const int32_t *__restrict__ table, int *at, int *sh,
-                                            int32_t *__restrict__ keys, int32_t *__restrict__ toks) {
+// Place the tokens of chunk `block`: get(i) reads pair i, put(i, pair) writes it.
+// at[w][d]: where the next token with digit d in wave w's part of the chunk goes.  A wave
+// takes its part 64 tokens at a time: the lanes with the same digit find each other by
+// ballots over its bits, so their order is that of the tokens.  KEPT: steps of 64 tokens a
+// wave keeps, 0: it reads them again.
+template <int KEPT, class Get, class Put>
+__device__ __forceinline__ void place_chunk(Get get, Put put, int64_t N, int64_t chunk, int chunks, int block, int shift, int bits,
+                                            const int32_t *__restrict__ table, int *at, int *sh) {
   const int bins = 1 << bits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t i0 = (int64_t)block * chunk, i1 = min(N, i0 + chunk);
   const int64_t part = chunk / kSortWaves;  // a multiple of 64, with KEPT at most KEPT 64
   const int64_t w0 = i0 + wave * part, w1 = min(i1, w0 + part);
-  int kept[KEPT > 0 ? KEPT : 1], kept_tok[KEPT > 0 ? KEPT : 1];
+  const Pair none{-1, 0};
+  Pair kept[KEPT > 0 ? KEPT : 1];
   if (KEPT > 0) {
 #pragma unroll
     for (int u = 0; u < KEPT; ++u) {
       const int64_t p = w0 + u * 64 + lane;  // (w1: also the end of the wave's part)
-      kept[u] = p < w1 ? in.key(p) : -1;
-      kept_tok[u] = p < w1 ? in.tok(p) : 0;
+      kept[u] = none;
+      if (p < w1) kept[u] = get(p);
     }
   }
   for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) at[i] = 0;
@@ -227,10 +232,10 @@ __device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int6
   if (KEPT > 0) {
 #pragma unroll
     for (int u = 0; u < KEPT; ++u)
-      if (kept[u] >= 0) atomicAdd(&at[wave * bins + ((kept[u] >> shift) & (bins - 1))], 1);
+      if (kept[u].key >= 0) atomicAdd(&at[wave * bins + ((kept[u].key >> shift) & (bins - 1))], 1);
   } else {
     for (int64_t i = w0 + lane; i < w1; i += 64) {
-      const int k = in.key(i);
+      const int k = get(i).key;
       if (k >= 0) atomicAdd(&at[wave * bins + ((k >> shift) & (bins - 1))], 1);
     }
   }
@@ -265,61 +270,68 @@ __device__ __forceinline__ void place_chunk(const SortInput &in, int64_t N, int6
   }
   __syncthreads();
   volatile int *mine = at + wave * bins;
-  auto place = [&](int key, int tok) {
-    const int d = (key >> shift) & (bins - 1);
-    uint64_t same = __ballot(key >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t one = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? one : ~one;
+  auto place = [&](Pair v) {
+    const int d = (v.key >> shift) & (bins - 1);
+    const uint64_t there = __ballot(v.key >= 0);
+    unsigned lo = (unsigned)there, hi = (unsigned)(there >> 32);
+#pragma unroll
+    for (int b = 0; b < kSortBits; ++b) {  // (bits that no digit has change nothing)
+      const int set = (int)((unsigned)d << (31 - b)) >> 31;  // all bits of it
+      const uint64_t one = __ballot(set);
+      lo &= ~((unsigned)one ^ (unsigned)set);
+      hi &= ~((unsigned)(one >> 32) ^ (unsigned)set);
     }
-    if (key >= 0) {
-      const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
+    if (v.key >= 0) {
+      const int rank = (int)__builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0)), n = __popc(lo) + __popc(hi);
       const int base = mine[d];
       __builtin_amdgcn_wave_barrier();
       if (rank == n - 1) mine[d] = base + n;
-      keys[base + rank] = key;
-      toks[base + rank] = tok;
+      put(base + rank, v);
     }
     __builtin_amdgcn_wave_barrier();
   };
   if (KEPT > 0) {
 #pragma unroll
     for (int u = 0; u < KEPT; ++u)
-      if (w0 + u * 64 < w1) place(kept[u], kept_tok[u]);
+      if (w0 + u * 64 < w1) place(kept[u]);
   } else {
     for (int64_t i = w0; i < w1; i += 64) {
-      const bool there = i + lane < w1;
-      place(there ? in.key(i + lane) : -1, there ? in.tok(i + lane) : 0);
+      Pair v = none;
+      if (i + lane < w1) v = get(i + lane);
+      place(v);
     }
   }
   for (int64_t p = i0 + threadIdx.x; p < i1; p += kSortThreads)
-    if (p >= all) keys[p] = -1;
+    if (p >= all) put(p, none);
 }
 
 template <int KEPT>
 __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(SortInput in, int64_t N, int64_t chunk, int chunks, int shift,
                                                                    int bits, const int32_t *__restrict__ table,
-                                                                   int32_t *__restrict__ keys, int32_t *__restrict__ toks, Clear c) {
+                                                                   Pair *__restrict__ pairs, Clear c) {
   if ((int)blockIdx.x >= chunks) return c.run((int)blockIdx.x - chunks);
   __shared__ int at[kSortWaves * kSortBins];
   __shared__ int sh[kSortWaves + 1];
-  place_chunk<KEPT>(in, N, chunk, chunks, (int)blockIdx.x, shift, bits, table, at, sh, keys, toks);
+  place_chunk<KEPT>(in, [&](int64_t i, Pair v) { pairs[i] = v; }, N, chunk, chunks, (int)blockIdx.x, shift, bits, table, at, sh);
 }
 
-// all digits by one workgroup
+// All digits by one workgroup.  The pairs stay in LDS between the passes, where stores to
+// scattered places cost less than in memory (a cache line each).
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortInput in, int64_t N, int64_t chunk, int digits, int bits,
-                                                                  int32_t *keys1, int32_t *toks1, int32_t *keys, int32_t *toks,
-                                                                  Clear c) {
+                                                                  Pair *__restrict__ pairs, Clear c) {
   if (blockIdx.x > 0) return c.run((int)blockIdx.x - 1);
   __shared__ int at[kSortWaves * kSortBins];
   __shared__ int sh[kSortWaves + 1];
+  __shared__ Pair list[kSortThreads * kSortAlone];
+  auto put = [&](int64_t i, Pair v) { list[i] = v; };
+  place_chunk<kSortAlone>(in, put, N, chunk, 1, 0, 0, bits, nullptr, at, sh);
+  __syncthreads();
   if (digits == 2) {
-    place_chunk<kSortAlone>(in, N, chunk, 1, 0, 0, bits, nullptr, at, sh, keys1, toks1);
+    // (every thread has read its pairs before the first barrier in there, so they may be overwritten)
+    place_chunk<kSortAlone>([&](int64_t i) { return list[i]; }, put, N, chunk, 1, 0, bits, bits, nullptr, at, sh);
     __syncthreads();
-    in.keys = keys1;
-    in.toks = toks1;
   }
-  place_chunk<kSortAlone>(in, N, chunk, 1, 0, (digits - 1) * bits, bits, nullptr, at, sh, keys, toks);
+  for (int64_t i = threadIdx.x; i < N; i += kSortThreads) pairs[i] = list[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -345,11 +357,11 @@ static int64_t part_pitch(int64_t C) { return (C + 3) / 4 * 4; }
 struct Chunk {
   int64_t p0, p1;
   bool before, after;  // the first run began in an earlier chunk; the last one goes on
-  __device__ __forceinline__ Chunk(const int32_t *keys, int64_t N, int64_t S, int64_t c) {
+  __device__ __forceinline__ Chunk(const Pair *pairs, int64_t N, int64_t S, int64_t c) {
     p0 = c * S;
     p1 = min(N, p0 + S);
-    before = p0 > 0 && keys[p0] >= 0 && keys[p0 - 1] == keys[p0];
-    after = p1 < N && keys[p1] >= 0 && keys[p1] == keys[p1 - 1];
+    before = p0 > 0 && pairs[p0].key >= 0 && pairs[p0 - 1].key == pairs[p0].key;
+    after = p1 < N && pairs[p1].key >= 0 && pairs[p1].key == pairs[p1 - 1].key;
   }
 };
 
@@ -380,15 +392,14 @@ template <typename T, int N> __device__ __forceinline__ void store_cells(T *row,
 // One wave per chunk and 64 x 16 bytes of its rows.  With ADD a run's row of dW is read
 // together with its first row of dout.
 template <typename T, typename O, bool ADD>
-__global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restrict__ keys, const int32_t *__restrict__ toks,
-                                                         int64_t ntok, int64_t S, int64_t chunks, const T *__restrict__ dout,
+__global__ void __launch_bounds__(256) embed_runs_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S, int64_t chunks, const T *__restrict__ dout,
                                                          int64_t ld, int64_t C, float scale, int lp,
                                                          O *__restrict__ out, float *__restrict__ parts, int64_t pitch) {
   constexpr int N = 16 / (int)sizeof(T);
   const EmbedParts at(lp);
   const int64_t c = (at.part * 64 + (threadIdx.x & 63)) * N;
   if (at.t >= chunks || c >= C) return;
-  const Chunk ch(keys, ntok, S, at.t);
+  const Chunk ch(pairs, ntok, S, at.t);
   float acc[N];
   Cells<O, N> old;
 #pragma unroll
@@ -415,9 +426,10 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restri
     Cells<O, N> was[ADD ? kRunUnroll : 1];
 #pragma unroll
     for (int u = 0; u < kRunUnroll; ++u) {
-      key[u] = p + u < ch.p1 ? keys[p + u] : -1;  // keys of -1 are the last ones
+      const Pair v = p + u < ch.p1 ? pairs[p + u] : Pair{-1, 0};  // keys of -1 are the last ones
+      key[u] = v.key;
       if (key[u] >= 0) {
-        row[u].load(dout + (int64_t)toks[p + u] * ld, c, C);
+        row[u].load(dout + (int64_t)v.tok * ld, c, C);
         if (ADD && key[u] != last) was[ADD ? u : 0].load(out + (int64_t)key[u] * C, c, C);
       }
       last = key[u];
@@ -444,21 +456,21 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const int32_t *__restri
 
 // The run that begins in chunk t and goes on: its parts in the order of the chunks.
 template <typename O>
-__global__ void __launch_bounds__(256) embed_join_kernel(const int32_t *__restrict__ keys, int64_t ntok, int64_t S,
+__global__ void __launch_bounds__(256) embed_join_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S,
                                                          int64_t chunks, int64_t C, float scale, bool add, int lp,
                                                          O *__restrict__ out, const float *__restrict__ parts, int64_t pitch) {
   const EmbedParts at(lp);
   const int lane = threadIdx.x & 63;
   const int64_t c = (at.part * 64 + lane) * 4;
   if (at.t >= chunks) return;
-  const Chunk ch(keys, ntok, S, at.t);
-  const int run = keys[ch.p1 - 1];
-  if (!ch.after || (ch.before && keys[ch.p0] == run)) return;
+  const Chunk ch(pairs, ntok, S, at.t);
+  const int run = pairs[ch.p1 - 1].key;
+  if (!ch.after || (ch.before && pairs[ch.p0].key == run)) return;
   // chunks that the run goes on in
   int64_t more = 0;
   for (;;) {
     const int64_t q = (at.t + 1 + more + lane) * S;
-    const uint64_t on = __ballot(q < ntok && keys[q < ntok ? q : 0] == run);
+    const uint64_t on = __ballot(q < ntok && pairs[q < ntok ? q : 0].key == run);
     if (on != ~0ull) {
       more += __ffsll((long long)~on) - 1;
       break;
@@ -483,17 +495,15 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const int32_t *__restri
   store_cells<O, 4>(row, c, C, acc);
 }
 
-// Two lists of pairs, the sort's table, the sums of parts of runs
+// Two lists of pairs (one where one workgroup sorts), the sort's table, the sums of parts of runs
 struct EmbedSpace {
-  size_t keys1, toks1, keys, toks, table, parts, bytes;
+  size_t pairs1, pairs, table, parts, bytes;
   EmbedSpace(int64_t T, int64_t V, int64_t C) {
     const SortPlan p = sort_plan(T, V);
-    const size_t list = ((size_t)T * 4 + 15) / 16 * 16;
-    keys1 = 0;
-    toks1 = keys1 + list;
-    keys = toks1 + list;
-    toks = keys + list;
-    table = toks + list;
+    const size_t list = ((size_t)T * sizeof(Pair) + 15) / 16 * 16;
+    pairs = 0;
+    pairs1 = list;
+    table = pairs1 + (p.chunks > 1 ? list : 0);
     parts = table + (p.chunks > 1 ? (size_t)p.chunks * (size_t)(4 << p.bits) : 0);
     parts = (parts + 15) / 16 * 16;
     bytes = parts + (size_t)run_chunks(T, C) * 2 * (size_t)part_pitch(C) * 4;
@@ -504,23 +514,23 @@ size_t embedding_backward_workspace(int64_t T, int64_t V, int64_t C) { return T 
 template <typename T, typename O> static hipError_t runs_to(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {
   constexpr int N = 16 / (int)sizeof(T);
   char *ws = (char *)a.workspace;
-  const int32_t *keys = (const int32_t *)(ws + sp.keys), *toks = (const int32_t *)(ws + sp.toks);
+  const Pair *pairs = (const Pair *)(ws + sp.pairs);
   float *parts = (float *)(ws + sp.parts);
   const int64_t S = run_chunk(a.T, a.C), chunks = run_chunks(a.T, a.C), pitch = part_pitch(a.C);
   int64_t n = (a.C + 64 * N - 1) / (64 * N);
   int lp = parts_log(chunks, n);
   const dim3 grid = parts_grid(chunks, n, lp);
   if (a.accumulate)
-    hipLaunchKernelGGL((embed_runs_kernel<T, O, true>), grid, dim3(256), 0, s, keys, toks, a.T, S, chunks, (const T *)a.x, a.ld,
+    hipLaunchKernelGGL((embed_runs_kernel<T, O, true>), grid, dim3(256), 0, s, pairs, a.T, S, chunks, (const T *)a.x, a.ld,
                        a.C, a.scale, lp, (O *)a.out, parts, pitch);
   else
-    hipLaunchKernelGGL((embed_runs_kernel<T, O, false>), grid, dim3(256), 0, s, keys, toks, a.T, S, chunks, (const T *)a.x, a.ld,
+    hipLaunchKernelGGL((embed_runs_kernel<T, O, false>), grid, dim3(256), 0, s, pairs, a.T, S, chunks, (const T *)a.x, a.ld,
                        a.C, a.scale, lp, (O *)a.out, parts, pitch);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks < 2) return e;
   n = (a.C + 255) / 256;
   lp = parts_log(chunks, n);
-  hipLaunchKernelGGL((embed_join_kernel<O>), parts_grid(chunks, n, lp), dim3(256), 0, s, keys, a.T, S, chunks, a.C, a.scale,
+  hipLaunchKernelGGL((embed_join_kernel<O>), parts_grid(chunks, n, lp), dim3(256), 0, s, pairs, a.T, S, chunks, a.C, a.scale,
                      a.accumulate != 0, lp, (O *)a.out, parts, pitch);
   return hipGetLastError();
 }
@@ -542,19 +552,19 @@ hipError_t launch_embedding_backward(const EmbedArgs &a, hipStream_t s) {
   const EmbedSpace sp(a.T, a.V, a.C);
   const SortPlan p = sort_plan(a.T, a.V);
   char *ws = (char *)a.workspace;
-  int32_t *keys1 = (int32_t *)(ws + sp.keys1), *toks1 = (int32_t *)(ws + sp.toks1);
-  int32_t *keys = (int32_t *)(ws + sp.keys), *toks = (int32_t *)(ws + sp.toks), *table = (int32_t *)(ws + sp.table);
-  SortInput in{a.ids, a.wide, a.V, nullptr, nullptr};
+  Pair *pairs1 = (Pair *)(ws + sp.pairs1), *pairs = (Pair *)(ws + sp.pairs);
+  int32_t *table = (int32_t *)(ws + sp.table);
+  SortInput in{a.ids, a.wide, a.V, nullptr};
   hipError_t e = hipSuccess;
   if (p.chunks == 1) {
     const Clear c = clear_share(a.out, bytes, 0, 1);
     hipLaunchKernelGGL(embed_sort_kernel, dim3(1 + (unsigned)c.blocks), dim3(kSortThreads), 0, s, in, a.T, p.chunk, p.digits,
-                       p.bits, keys1, toks1, keys, toks, c);
+                       p.bits, pairs, c);
     e = hipGetLastError();
   } else {
     for (int d = 0; d < p.digits && e == hipSuccess; ++d) {
       const bool last = d == p.digits - 1;
-      int32_t *k = last ? keys : keys1, *t = last ? toks : toks1;
+      Pair *to = last ? pairs : pairs1;
       Clear c = clear_share(a.out, bytes, 2 * d, 2 * p.digits);
       hipLaunchKernelGGL(embed_count_kernel, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
                          d * p.bits, p.bits, table, p.chunks, c);
@@ -563,13 +573,12 @@ hipError_t launch_embedding_backward(const EmbedArgs &a, hipStream_t s) {
       c = clear_share(a.out, bytes, 2 * d + 1, 2 * p.digits);
       if (p.chunk <= kSortChunk)
         hipLaunchKernelGGL(embed_place_kernel<kSortKept>, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T,
-                           p.chunk, p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t, c);
+                           p.chunk, p.chunks, d * p.bits, p.bits, (const int32_t *)table, to, c);
       else
         hipLaunchKernelGGL(embed_place_kernel<0>, dim3((unsigned)(p.chunks + c.blocks)), dim3(kSortThreads), 0, s, in, a.T, p.chunk,
-                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, k, t, c);
+                           p.chunks, d * p.bits, p.bits, (const int32_t *)table, to, c);
       e = hipGetLastError();
-      in.keys = keys1;
-      in.toks = toks1;
+      in.pairs = pairs1;
     }
   }
   if (e != hipSuccess) return e;
