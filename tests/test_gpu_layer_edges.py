@@ -1,0 +1,411 @@
+"""GPU tests of the operators between token ids and the expert layer as a training step
+uses them: together with the expert layer, on other streams, captured into graphs, with
+workspaces of the caller's, with offsets past 32 bits, at the ends of their limits."""
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_gram_amd as nsg
+from oracle import layer_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def rand(shape, seed, dtype=torch.float32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g, device="cuda")).to(dtype)
+
+
+def integers(hi, shape, seed, lo=0, dtype=torch.int64):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=dtype)
+
+
+def same(a, b):
+    for x, y in zip(a, b):
+        assert (x is None and y is None) or torch.equal(x, y)
+
+
+def every_call(seed, dtype=torch.bfloat16, T=300, V=500, C=264, E=60, k=4):
+    """Inputs, and a function that makes each call once and returns all outputs."""
+    ids, W = integers(V, (T,), seed, lo=-3), rand((V, C), seed + 1, dtype)
+    gamma, beta = rand((C,), seed + 2), rand((C,), seed + 3)
+    dy, logits = rand((T, C), seed + 4, dtype), rand((T, E), seed + 5, dtype)
+    bias, dw = rand((E,), seed + 6, scale=0.1), rand((T, k), seed + 7)
+    mask = rand((T,), seed + 8) > -1
+    dloss = torch.full((), 3.0, device="cuda")
+
+    def run(ws=(None,) * 3):
+        x = nsg.embedding(ids, W, 1.5)
+        y, stats = nsg.layer_norm(x, gamma, beta)
+        dx, dg, db = nsg.layer_norm_backward(dy, x, stats, gamma, workspace=ws[0])
+        dW = nsg.embedding_backward(dx, ids, V, 1.5, workspace=ws[1])
+        r = nsg.expert_route(logits, k, score="sigmoid", bias=bias, mask=mask, balance=True, workspace=ws[2])
+        dl = nsg.expert_route_backward(logits, r.ids, dw, score="sigmoid", counts=r.counts, balance=0.5, dloss=dloss)
+        return (x, y, stats, dx, dg, db, dW, *r, dl)
+
+    inputs = (ids, W, gamma, beta, dy, logits, bias, dw, mask)
+    need = (nsg.layer_norm_backward_workspace_size(T, C), nsg.embedding_backward_workspace_size(T, V, C),
+            nsg.expert_route_workspace_size(T, E))
+    return inputs, run, need
+
+
+def test_workspaces_of_the_caller():
+    """Exactly as large as needed, larger, and full of anything; nothing behind their end is written."""
+    _, run, need = every_call(1)
+    want = run()
+    for fill in (0, 255):
+        rooms = [torch.full((n + 64,), fill, dtype=torch.uint8, device="cuda") for n in need]
+        same(run([r[:n] for r, n in zip(rooms, need)]), want)
+        for r in rooms:
+            assert r[-64:].eq(fill).all()
+    big = [torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda") for n in need]
+    same(run(big), want)
+    # one that is too small is not used
+    small = [torch.full((max(n - 1, 0),), 5, dtype=torch.uint8, device="cuda") for n in need]
+    same(run(small), want)
+    assert all(s.eq(5).all() for s in small)
+
+
+def test_workspaces_refused():
+    _, run, need = every_call(2)
+    with pytest.raises(ValueError):
+        run([torch.empty(need[0], dtype=torch.uint8), None, None])
+    with pytest.raises(nsg.NSGError):  # off its 16-byte boundary
+        run([torch.empty(need[0] + 16, dtype=torch.uint8, device="cuda")[8:], None, None])
+
+
+def test_on_other_streams():
+    """Work follows the current stream: inputs that another kernel of that stream is still writing."""
+    inputs, run, _ = every_call(3)
+    want = run()
+    torch.cuda.synchronize()
+    copies = [t.clone() for t in inputs]
+    side = torch.cuda.Stream()
+    busy = rand((4096, 4096), 9)
+    with torch.cuda.stream(side):
+        for t in inputs:
+            t.zero_()
+        for _ in range(8):
+            busy @ busy
+        for t, c in zip(inputs, copies):
+            t.copy_(c)
+        got = run()
+    side.synchronize()
+    same(got, want)
+
+
+def test_two_streams_at_once():
+    runs = [every_call(10 + i)[1] for i in range(2)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = []
+    for _ in range(3):
+        got = []
+        for s, r in zip(streams, runs):
+            with torch.cuda.stream(s):
+                got.append(r())
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        same(g, w)
+
+
+@pytest.mark.parametrize("T,V,C,E", [(300, 500, 264, 60), (20000, 3000, 40, 512), (2100, 100, 1250, 8)])
+def test_graph_replays(T, V, C, E):
+    """Captured once, replayed on new inputs with eager work in between, with other graphs' replays too."""
+    inputs, run, _ = every_call(20, T=T, V=V, C=C, E=E)
+    others, run2, _ = every_call(40, T=T, V=V, C=C, E=E)
+    fresh = [[t.clone() for t in every_call(60 + i, T=T, V=V, C=C, E=E)[0]] for i in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+        run2()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for fn in (run, run2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = fn()
+        graphs.append((g, out))
+    for i in range(4):
+        for t, f in zip(inputs, fresh[i % 2]):
+            t.copy_(f)
+        for t, f in zip(others, fresh[(i + 1) % 2]):
+            t.copy_(f)
+        torch.cuda.synchronize()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in out] for _, out in graphs]
+        same(got[0], run())
+        same(got[1], run2())
+        rand((64, 64), i) @ rand((64, 64), i + 1)
+
+
+def test_refusals_of_gpu_tensors():
+    x, ids = rand((6, 40), 1), integers(6, (6,), 2)
+    r = nsg.expert_route(x, 3, balance=True)
+    y, stats = nsg.layer_norm(x)
+    bad = [
+        lambda: nsg.embedding(ids.float(), x), lambda: nsg.embedding(ids.cpu(), x), lambda: nsg.embedding(ids, x.t()),
+        lambda: nsg.embedding(ids, x[0]), lambda: nsg.embedding(ids, x.double()), lambda: nsg.embedding(ids.repeat(2)[::2], x),
+        lambda: nsg.embedding_backward(x, ids[:5], 9), lambda: nsg.embedding_backward(x, ids, 9, accumulate=True),
+        lambda: nsg.embedding_backward(x, ids, 9, out=x), lambda: nsg.embedding_backward(x.t().contiguous().t(), ids, 9),
+        lambda: nsg.embedding_backward(x, ids, 9, out=torch.empty(9, 80, device="cuda")[:, :40]),
+        lambda: nsg.embedding_backward(x.expand(3, 6, 40), ids.expand(3, 6).contiguous(), 9),
+        lambda: nsg.layer_norm(x.t()), lambda: nsg.layer_norm(x[0]), lambda: nsg.layer_norm(x, x[0, :39]),
+        lambda: nsg.layer_norm(x, x[0], x[0].half()), lambda: nsg.layer_norm(x, x[0].double()), lambda: nsg.layer_norm(x, x[0].cpu()),
+        lambda: nsg.layer_norm(x[:, :1].expand(6, 40)), lambda: nsg.layer_norm(x.unsqueeze(1).expand(6, 2, 40)),
+        lambda: nsg.layer_norm_backward(x.half(), x, stats), lambda: nsg.layer_norm_backward(x[:5], x, stats),
+        lambda: nsg.layer_norm_backward(x, x, stats[:1]), lambda: nsg.layer_norm_backward(x, x, stats.double()),
+        lambda: nsg.layer_norm_backward(x, x, stats, x[0, :3]), lambda: nsg.layer_norm_backward(x, x, stats.cpu()),
+        lambda: nsg.expert_route(x, 0), lambda: nsg.expert_route(x, 41), lambda: nsg.expert_route(x, 2, score="tanh"),
+        lambda: nsg.expert_route(x, 2, bias=x[0, :5]), lambda: nsg.expert_route(x, 2, bias=x[0].half()),
+        lambda: nsg.expert_route(x, 2, mask=ids), lambda: nsg.expert_route(x, 2, mask=torch.ones(5, dtype=torch.bool, device="cuda")),
+        lambda: nsg.expert_route(x[0], 2), lambda: nsg.expert_route(x.t(), 2),
+        lambda: nsg.expert_route_backward(x, r.ids.long()), lambda: nsg.expert_route_backward(x, r.ids[:5]),
+        lambda: nsg.expert_route_backward(x, r.ids, r.weights[:, :2]), lambda: nsg.expert_route_backward(x, r.ids, r.weights.half()),
+        lambda: nsg.expert_route_backward(x, r.ids, r.weights, counts=r.counts[:-1]),
+        lambda: nsg.expert_route_backward(x, r.ids, r.weights, dloss=r.loss),
+        lambda: nsg.expert_route_backward(x, r.ids, r.weights, counts=r.counts, dloss=r.probs),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+            pytest.fail(f"call {i} was taken")
+    for call in (lambda: nsg.embedding(ids, x, float("nan")), lambda: nsg.layer_norm(x, eps=-1.0),
+                 lambda: nsg.layer_norm(x[:, :0]), lambda: nsg.expert_route(rand((2, 1025), 3), 2),
+                 lambda: nsg.expert_route(x, 2, scale=float("inf")), lambda: nsg.embedding_backward(x, ids, -1),
+                 lambda: nsg.embedding_backward(x, ids, (1 << 20) + 1)):
+        with pytest.raises((nsg.NSGError, RuntimeError)):
+            call()
+
+
+# ---------------------------------------------------------------------------
+# together with the expert layer
+# ---------------------------------------------------------------------------
+def test_a_layer_of_experts_from_token_ids_and_back():
+    """embedding -> layer norm -> router -> sort, dispatch, experts, combine, and every gradient,
+    in fp32 against autograd in 64 bits.
+
+    The tolerance: sums of at most 400 terms in each of the 8 stages between an input and the
+    last gradient, each off by 400 u of the sum of its terms' sizes; these cancel to no less than
+    a tenth here: 8 * 400 u * 10 = 2e-3 of a gradient's norm at worst, and a tenth of that
+    holds for errors that do not all have one sign."""
+    B, S, V, C, F, E, k = 3, 70, 90, 96, 40, 12, 3
+    T = B * S
+    ids = integers(V, (B, S), 1)
+    ids[:, -7:] = -1  # padding
+    mask = (ids >= 0).view(-1)
+    W, gamma, beta = rand((V, C), 2), 1 + 0.1 * rand((C,), 3), 0.1 * rand((C,), 4)
+    Wr, We = 0.3 * rand((E, C), 5), 0.2 * rand((E, F, C), 6)
+    bias, dout = 0.05 * rand((E,), 7), rand((T, F), 8)
+
+    x = nsg.embedding(ids, W, 2.0)
+    y, stats = nsg.layer_norm(x, gamma, beta)
+    flat = y.view(T, C)
+    logits = flat @ Wr.t()
+    r = nsg.expert_route(logits, k, bias=bias, mask=mask, scale=1.5, balance=True)
+    plan = nsg.expert_sort(r.ids, E)
+    rows = nsg.expert_dispatch(flat, plan)
+    cut = plan.offsets.tolist()
+    z = torch.zeros(T * k, F, device="cuda")
+    for e in range(E):
+        z[cut[e]:cut[e + 1]] = rows[cut[e]:cut[e + 1]] @ We[e].t()
+    out = nsg.expert_combine(z, plan, r.weights)
+    assert out[~mask].eq(0).all() and cut[E] == k * int(mask.sum())
+
+    dz, dw = nsg.expert_combine_backward(dout, z, plan, r.weights)
+    drows, dWe = torch.zeros_like(rows), torch.zeros_like(We)
+    for e in range(E):
+        drows[cut[e]:cut[e + 1]] = dz[cut[e]:cut[e + 1]] @ We[e]
+        dWe[e] = dz[cut[e]:cut[e + 1]].t() @ rows[cut[e]:cut[e + 1]]
+    dl = nsg.expert_route_backward(logits, r.ids, dw, scale=1.5, counts=r.counts, balance=5.0)
+    dflat = nsg.expert_combine(drows, plan) + dl @ Wr
+    dx, dgamma, dbeta = nsg.layer_norm_backward(dflat.view(B, S, C), x, stats, gamma)
+    dW = nsg.embedding_backward(dx, ids, V, 2.0)
+
+    p = [t.double().cpu().requires_grad_() for t in (W, gamma, beta, Wr, We)]
+    i = ids.view(-1).cpu()
+    keep = i >= 0
+    xr = torch.where(keep[:, None], 2.0 * p[0][i.clamp(min=0)], 0.0)
+    yr = torch.nn.functional.layer_norm(xr, (C,), p[1], p[2], 1e-5)
+    s = torch.softmax(yr @ p[3].t(), 1)
+    ch = torch.topk(s + bias.double().cpu(), k, dim=1).indices
+    assert torch.equal(torch.where(keep[:, None], ch, -1).int(), r.ids.cpu())
+    w = s.gather(1, ch)
+    w = 1.5 * w / w.sum(1, keepdim=True) * keep[:, None]
+    outr = sum(w[:, j, None] * torch.einsum("tc,tfc->tf", yr, p[4][ch[:, j]]) for j in range(k))
+    N = int(keep.sum())
+    counts = torch.bincount(ch[keep].reshape(-1), minlength=E)
+    loss = E / (k * N) * (counts.double() * (s[keep].sum(0) / N)).sum()
+    assert torch.equal(torch.cat([counts, torch.tensor([N])]).int(), r.counts.cpu())
+    assert abs(r.loss.item() - loss.item()) <= 1e-5
+    want = torch.autograd.grad((outr * dout.double().cpu()).sum() + 5.0 * loss, p)
+    for got, exp, name in zip((dW, dgamma, dbeta, dl.t() @ flat, dWe), want, ("embedding", "gamma", "beta", "router", "experts")):
+        assert (got.double().cpu() - exp).norm() <= 2e-4 * exp.norm(), name
+    assert (out.double().cpu() - outr).norm() <= 2e-4 * outr.norm()
+
+
+def test_a_training_step_with_fp8_experts():
+    """The same path in bf16 with the 8-bit products and the Muon step: twice, bit for bit, and finite."""
+    T, V, C, F, E, k = 512, 1000, 256, 128, 16, 4
+    ids = integers(V, (T,), 1, lo=-2, dtype=torch.int32)
+
+    def step():
+        W, gamma, beta = (rand(s, 2 + i, torch.bfloat16) for i, s in enumerate(((V, C), (C,), (C,))))
+        Wr, We = rand((E, C), 5, torch.bfloat16, 0.1), rand((E, F, C), 6, torch.bfloat16, 0.05)
+        M, dout = torch.zeros(E, F, C, device="cuda"), rand((T, F), 7, torch.bfloat16, 0.1)
+        x = nsg.embedding(ids, W, 16.0)
+        h, stats = nsg.layer_norm(x, gamma, beta)
+        logits = h @ Wr.t()
+        r = nsg.expert_route(logits, k, score="sigmoid", mask=ids >= 0, balance=True)
+        plan = nsg.expert_sort(r.ids, E)
+        hq, (wq, ws, wtq, wts) = nsg.quantize_fp8(h), nsg.quantize_fp8(We, block="tile", transposed=True)
+        y = nsg.expert_gemm_fp8(*hq, wq, ws, plan.offsets, rows=plan.tokens)
+        out = nsg.expert_combine(y, plan, r.weights)
+        e5m2 = torch.float8_e5m2
+        dy, dw = nsg.expert_combine_backward(dout, y, plan, r.weights)
+        dh = nsg.expert_combine(nsg.expert_gemm_fp8(*nsg.quantize_fp8(dy, dtype=e5m2), wtq, wts, plan.offsets), plan)
+        dWe = nsg.expert_wgrad_fp8(*nsg.quantize_fp8_columns(dy, plan.offsets, dtype=e5m2),
+                                   *nsg.quantize_fp8_columns(h, plan.offsets, rows=plan.tokens), plan.offsets)
+        dl = nsg.expert_route_backward(logits, r.ids, dw, score="sigmoid", counts=r.counts, balance=0.01)
+        dx, dgamma, dbeta = nsg.layer_norm_backward(dh + dl @ Wr, x, stats, gamma)
+        dW = nsg.embedding_backward(dx, ids, V, 16.0, out=torch.empty(V, C, device="cuda"))
+        nsg.muon_step(We, M, dWe, mu=0.95, lr=0.02, seed=3)
+        return out, *r, dl, dx, dgamma, dbeta, dW, We, M
+
+    a, b = step(), step()
+    same(a, b)
+    assert all(t.float().isfinite().all() for t in a)
+    assert a[0][ids < 0].eq(0).all() and a[9][0].ne(0).any()
+
+
+def test_ids_that_leave_an_expert_empty_and_the_same_index_twice():
+    """ids of the caller's own for the gradient: equal experts of a token add up."""
+    l = rand((5, 20), 1)
+    ids = torch.tensor([[3, 3], [3, 4], [-1, 19], [0, 0], [7, -5]], dtype=torch.int32, device="cuda")
+    dw = rand((5, 2), 2)
+    got = nsg.expert_route_backward(l, ids, dw, normalize=False).double().cpu()
+    s = l.double().cpu().requires_grad_()
+    p, e = torch.softmax(s, 1), ids.cpu().long()
+    total = (p.gather(1, e.clamp(min=0)) * dw.double().cpu() * ((e >= 0) & (e < 20))).sum()
+    want = torch.autograd.grad(total, s)[0]
+    assert (got - want).abs().max() <= 200 * U
+
+
+# ---------------------------------------------------------------------------
+# large sizes
+# ---------------------------------------------------------------------------
+def test_embedding_offsets_past_32_bits():
+    V, C = 1 << 20, 2304  # 2.4e9 elements
+    W = torch.zeros(V, C, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([0, V - 1, 932067, 932068, 5, V], device="cuda")
+    rows = rand((5, C), 1, torch.bfloat16)
+    W[ids[:5]] = rows
+    out = nsg.embedding(ids, W)
+    assert torch.equal(out[:5], rows) and out[5].eq(0).all()
+    del W
+    dW = nsg.embedding_backward(out, ids, V)
+    assert torch.equal(dW[ids[:5]], rows)
+    assert int(dW.count_nonzero(1).ne(0).sum()) == 5
+    nsg.embedding_backward(out, ids, V, out=dW, accumulate=True)
+    assert torch.equal(dW[ids[:5]], (rows.float() * 2).bfloat16())
+
+
+def test_embedding_of_many_rows():
+    """Output and dout past 32-bit offsets."""
+    T, V, C = 700_000, 50, 4096
+    W = rand((V, C), 1, torch.bfloat16)
+    ids = integers(V, (T,), 2, dtype=torch.int32)
+    out = nsg.embedding(ids, W)
+    for a in (0, 524_287, T - 3):
+        assert torch.equal(out[a:a + 3], W[ids[a:a + 3].long()])
+    dW = nsg.embedding_backward(out, ids, V, out=torch.empty(V, C, device="cuda"))
+    n = torch.bincount(ids, minlength=V).double()[:, None]
+    want = n * W.double()
+    # n sums in chunks of 64 and their joins: at most 64 + n / 64 additions of numbers of one size
+    assert ((dW.double() - want).abs() <= (66 + n / 64) * U * want.abs()).all()
+
+
+def test_layer_norm_offsets_past_32_bits():
+    R, C = 540_000, 4096
+    x = rand((R, C), 1, torch.bfloat16)
+    y, stats = nsg.layer_norm(x)
+    dx, dw, db = nsg.layer_norm_backward(x, x, stats)
+    for a in (0, 524_287, R - 9):
+        part, s = nsg.layer_norm(x[a:a + 9])
+        assert torch.equal(part, y[a:a + 9]) and torch.equal(s, stats[:, a:a + 9])
+        assert torch.equal(nsg.layer_norm_backward(x[a:a + 9], x[a:a + 9], s)[0], dx[a:a + 9])
+    assert dw.isfinite().all() and (db.double() - x.sum(0, dtype=torch.float64)).abs().max() <= R * U * x.abs().double().sum(0).max()
+
+
+@pytest.mark.parametrize("E", [256, 1024])
+def test_router_offsets_past_32_bits(E):
+    T, k = (1 << 31) // E + 4000, 2
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, T, 1 << 20):
+        l[a:a + (1 << 20)] = rand((min(1 << 20, T - a), E), a, torch.bfloat16)
+    r = nsg.expert_route(l, k, balance=True)
+    assert r.counts[E] == T and r.counts[:E].sum() == T * k
+    g = nsg.expert_route_backward(l, r.ids, r.weights)
+    for a in (0, T - 4100, T - 9):
+        part = nsg.expert_route(l[a:a + 9], k)
+        assert torch.equal(part.ids, r.ids[a:a + 9]) and torch.equal(part.weights, r.weights[a:a + 9])
+        want = nsg.expert_route_backward(l[a:a + 9], part.ids, part.weights).float()
+        assert (g[a:a + 9].float() - want).abs().max() <= 2 ** -8 * want.abs().max()
+
+
+def test_long_pitches():
+    """Rows far apart: offsets of the pitch times the row past 32 bits."""
+    R, C, ld = 5, 70, (1 << 29) + 64
+    room = torch.zeros((R - 1) * ld + C, dtype=torch.bfloat16, device="cuda")
+    v = room.as_strided((R, C), (ld, 1))
+    x = rand((R, C), 1, torch.bfloat16)
+    v.copy_(x)
+    same(nsg.layer_norm(v), nsg.layer_norm(x))
+    _, stats = nsg.layer_norm(x)
+    same(nsg.layer_norm_backward(v, v, stats), nsg.layer_norm_backward(x, x, stats))
+    same(nsg.expert_route(v, 3, balance=True), nsg.expert_route(x, 3, balance=True))
+    ids = torch.tensor([4, 0, 3], device="cuda")
+    assert torch.equal(nsg.embedding(ids, v), nsg.embedding(ids, x))
+    ids = torch.tensor([1, 0, 1, 2, 2], device="cuda")
+    assert torch.equal(nsg.embedding_backward(v, ids, 4), nsg.embedding_backward(x, ids, 4))
+
+
+def test_a_vocabulary_and_a_choice_at_their_limits():
+    ids = torch.tensor([(1 << 20) - 1, 1 << 20, 0], device="cuda")
+    d = rand((3, 2), 1)
+    dW = nsg.embedding_backward(d, ids, 1 << 20)
+    assert torch.equal(dW[-1], d[0]) and torch.equal(dW[0], d[2]) and int(dW.count_nonzero()) == 4
+    l = rand((70, 1024), 2)
+    r = nsg.expert_route(l, 64, balance=True)
+    assert np.array_equal(r.ids.cpu().numpy(), ref.choose(l.double().cpu().numpy(), 64, "softmax"))
+    b = rand((1024,), 3, scale=1e-7)  # keys that only 64 bits tell apart
+    flat = torch.zeros(70, 1024, device="cuda")
+    for k in (1, 5, 63, 64):
+        r = nsg.expert_route(flat, k, score="sigmoid", bias=b)
+        assert np.array_equal(r.ids.cpu().numpy(), ref.choose(flat.double().cpu().numpy(), k, "sigmoid", b.double().cpu().numpy())), k
+
+
+@pytest.mark.parametrize("E", [12, 60, 128, 200, 512, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biased_scores_that_nearly_meet(E, score):
+    """Pairs, runs and whole rows of keys a few roundings of fp32 apart: the order is that of 64 bits."""
+    g = np.random.default_rng(E)
+    T, k = 64, min(E, 8)
+    l = g.standard_normal((T, E)).astype(np.float32)
+    s = ref.scores(l.astype(np.float64), score)
+    # the bias brings each score of row 0 next to a level that neighbours share
+    level = np.repeat(g.standard_normal(E // 4 + 1), 4)[:E] * 1e-3
+    b = (level + 0.5 - s[0] + 1e-8 * g.standard_normal(E)).astype(np.float32)
+    l[1:40] = l[0] + 1e-6 * g.standard_normal((39, E)).astype(np.float32)
+    lt, bt = torch.from_numpy(l).cuda(), torch.from_numpy(b).cuda()
+    for kk in (1, k):
+        r = nsg.expert_route(lt, kk, score=score, bias=bt)
+        assert np.array_equal(r.ids.cpu().numpy(), ref.choose(l.astype(np.float64), kk, score, b.astype(np.float64)))
