@@ -17,27 +17,32 @@
 namespace nsg {
 
 // ---------------------------------------------------------------------------
-// A row belongs to WR waves; lane l of them has the NV pieces of 16 bytes
-// (j WR 64 + l) of it: at most 16 elements, rows of up to 16384.
+// A row belongs to LANES lanes; lane l of them has the NV pieces of 16 bytes
+// (j LANES + l) of it, 16 elements, above 8192 in a row 32: rows of up to 16384.  The last piece of a row whose
+// length is no multiple of a piece lies over the one before it: its first elements are
+// read and stored twice, and left out of sums.
 // ---------------------------------------------------------------------------
 template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
-constexpr int kNormLane = 16;    // elements of a lane
-constexpr int kNormWaves = 16;   // waves of a row at most
-constexpr int kNormRegisters = kNormLane * kNormWaves * 64;  // elements of a row in registers
+constexpr int kNormLane = 16;  // elements of a lane, twice as many for the longest rows
+constexpr int kNormRegisters = 16384;  // elements of a row in registers
 
-// 16 bytes of a row from element c on, zeros behind its end
 template <typename T> struct Piece {
   static constexpr int N = kPiece<T>;
   typedef T vec __attribute__((ext_vector_type(N)));
   typedef vec mem __attribute__((aligned(sizeof(T))));
   vec v;
-  __device__ __forceinline__ void load(const T *row, int c, int C) {
-    if (c + N <= C) {
-      v = *reinterpret_cast<const mem *>(row + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = c + i < C ? row[c + i] : (T)0.f;
-    }
+  __device__ __forceinline__ void load(const T *row, int c) { v = *reinterpret_cast<const mem *>(row + c); }
+};
+// where piece j of lane l lies, how many of its first elements are another's, whether it is there
+template <typename T, int LANES> struct Place {
+  static constexpr int N = kPiece<T>;
+  int c, skip;
+  bool there;
+  __device__ __forceinline__ Place(int j, int l, int C) {
+    c = (j * LANES + l) * N;
+    there = c < C;
+    skip = c + N > C ? c + N - C : 0;  // (at least N where it is not there)
+    if (skip > 0) c = C - N;
   }
 };
 
@@ -85,13 +90,14 @@ __device__ __forceinline__ float row_rstd(float m2, float rest, float eps) {
   return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
 }
 
-// Sums of a and b over the WR waves of a row, the same in all their lanes.  `sh`:
-// a pair for each wave of the workgroup, not in use by an earlier sum.
-template <int WR> __device__ __forceinline__ void row_sum(float &a, float &b, float (*sh)[2]) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  if (WR == 1) return;
-  const int wave = threadIdx.x >> 6, first = wave / WR * WR;
+// Sums of a and b over the LANES lanes of a row, the same in all of them.  `sh`: a pair
+// for each wave of the workgroup, not in use by an earlier sum.
+template <int LANES> __device__ __forceinline__ void row_sum(float &a, float &b, float (*sh)[2]) {
+  constexpr int L = LANES < 64 ? LANES : 64, WR = LANES / 64;
+  a = group_lanes_sum<L>(a);
+  b = group_lanes_sum<L>(b);
+  if (WR <= 1) return;
+  const int wave = threadIdx.x >> 6, first = wave / (WR > 0 ? WR : 1) * WR;
   if ((threadIdx.x & 63) == 0) {
     sh[wave][0] = a;
     sh[wave][1] = b;
@@ -105,54 +111,78 @@ template <int WR> __device__ __forceinline__ void row_sum(float &a, float &b, fl
   }
 }
 
-// A workgroup takes WAVES / WR rows at a time and keeps the weights; the next rows are
+// This thread's row of the THREADS / LANES that a workgroup takes at a time (the same in a
+// wave where a row has that many lanes)
+template <int LANES> __device__ __forceinline__ int own_row() {
+  return LANES >= 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / LANES) : threadIdx.x / LANES;
+}
+
+// weights as fp32 in LDS, where threads have no registers for them
+template <int THREADS> __device__ __forceinline__ void weights_to_lds(const void *w, int dtype, int C, float none, float *to) {
+#pragma unroll 8
+  for (int c = threadIdx.x; c < C; c += THREADS)
+    to[c] = w == nullptr       ? none
+            : dtype == NSG_F32 ? ((const float *)w)[c]
+            : dtype == NSG_BF16 ? (float)((const __bf16 *)w)[c] : (float)((const _Float16 *)w)[c];
+}
+
+// A workgroup takes THREADS / LANES rows at a time and keeps the weights; the next rows are
 // on their way while it works.
-template <typename T, int WAVES, int WR, int NV>
-__global__ void __launch_bounds__(WAVES * 64) layer_norm_kernel(NormArgs p) {
-  constexpr int N = kPiece<T>, kRows = WAVES / WR;
-  __shared__ float sh[2][WAVES][2];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l = (wave % WR) * 64 + (threadIdx.x & 63);
+template <typename T, int THREADS, int LANES, int NV>
+__global__ void __launch_bounds__(THREADS) layer_norm_kernel(NormArgs p) {
+  constexpr int N = kPiece<T>, kRows = THREADS / LANES;
+  __shared__ float sh[2][THREADS / 64][2];
+  const int l = threadIdx.x % LANES, C = (int)p.C;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + wave / WR;
+  int64_t r = (int64_t)blockIdx.x * kRows + own_row<LANES>();
   Piece<T> x[NV];
   auto fetch = [&](int64_t row) {
+    if (row >= p.R) return;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j].load((const T *)p.x + row * p.ldx, (j * WR * 64 + l) * N, row < p.R ? (int)p.C : 0);
+    for (int j = 0; j < NV; ++j) {
+      const Place<T, LANES> at(j, l, C);
+      if (at.there) x[j].load((const T *)p.x + row * p.ldx, at.c);
+    }
   };
-  constexpr bool kAhead = WR < 16;  // (16 waves have 128 registers each, too few for the next row)
-  if (kAhead) fetch(r);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) x[j].v = (T)0.f;
+  fetch(r);
   float w[NV][N], b[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_weights<N>(p.weight, p.w_dtype, (j * WR * 64 + l) * N, p.C, 1.f, w[j]);
-    load_weights<N>(p.bias, p.w_dtype, (j * WR * 64 + l) * N, p.C, 0.f, b[j]);
+    const Place<T, LANES> at(j, l, C);
+    if (!at.there) continue;
+    load_weights<N>(p.weight, p.w_dtype, at.c, C, 1.f, w[j]);
+    load_weights<N>(p.bias, p.w_dtype, at.c, C, 0.f, b[j]);
   }
-  const float n = (float)p.C;
+  const float n = (float)C;
   for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.R; r0 += step, r += step) {
     float f[NV][N], sum = 0.f, sq = 0.f;
-    if (!kAhead) fetch(r);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const Place<T, LANES> at(j, l, C);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         f[j][i] = (float)x[j].v[i];
-        sum += f[j][i];
+        sum += i >= at.skip ? f[j][i] : 0.f;
       }
-    if (kAhead && r0 + step < p.R) fetch(r + step);
-    row_sum<WR>(sum, sq, sh[0]);
+    }
+    fetch(r + step);
+    row_sum<LANES>(sum, sq, sh[0]);
     const float mean = sum / n;
     sum = sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const Place<T, LANES> at(j, l, C);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = (j * WR * 64 + l) * N + i < p.C ? f[j][i] - mean : 0.f;
-        f[j][i] = d;
+        f[j][i] -= mean;
+        const float d = i >= at.skip ? f[j][i] : 0.f;
         sum += d;
         sq = fmaf(d, d, sq);
       }
-    row_sum<WR>(sum, sq, sh[1]);
+    }
+    row_sum<LANES>(sum, sq, sh[1]);
     const float rest = sum / n;  // what rounding left of the mean
     const float rstd = row_rstd(sq / n, rest, p.eps);
     if (r >= p.R) continue;
@@ -163,114 +193,149 @@ __global__ void __launch_bounds__(WAVES * 64) layer_norm_kernel(NormArgs p) {
     T *y = (T *)p.out + r * p.C;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * WR * 64 + l) * N;
-      if (c >= p.C) continue;
+      const Place<T, LANES> at(j, l, C);
+      if (!at.there) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) f[j][i] = fmaf((f[j][i] - rest) * rstd, w[j][i], b[j][i]);
-      store_piece<T, N>(y, c, p.C, f[j]);
+      Row<T, N, (int)sizeof(T)>::store(y + at.c, f[j]);
     }
   }
 }
 
 // The gradient: dx, and with parts [groups][2][C] this workgroup's sums of dy xh and dy.
-// A lane has the same columns of every row, so these sums stay in its registers; the
-// rows that a workgroup takes at a time are added at the end, in LDS.
-template <typename T, int WAVES, int WR, int NV>
-__global__ void __launch_bounds__(WAVES * 64) layer_norm_backward_kernel(NormArgs p, float *__restrict__ parts) {
-  constexpr int N = kPiece<T>, kRows = WAVES / WR;
-  __shared__ float sh[2][WAVES][2];
-  __shared__ float joined[kRows > 1 ? 2 * WR * 64 * NV * N : 1];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l = (wave % WR) * 64 + (threadIdx.x & 63);
+// A lane has the same columns of every row, so these sums stay in its registers; those of
+// the rows that a workgroup takes at a time are added at the end.
+template <typename T, int THREADS, int LANES, int NV, bool KEEP>
+__global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(NormArgs p, float *__restrict__ parts) {
+  constexpr int N = kPiece<T>, kRows = THREADS / LANES;
+  constexpr int kWide = LANES < 64 ? 64 : LANES, kGroups = THREADS / kWide;  // threads that add in LDS, groups of them
+  constexpr int kCols = LANES * NV * N;
+  __shared__ float sh[2][THREADS / 64][2];
+  __shared__ float joined[kGroups > 1 ? 2 * kCols : 1];
+  const int l = threadIdx.x % LANES, C = (int)p.C;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + wave / WR;
+  int64_t r = (int64_t)blockIdx.x * kRows + own_row<LANES>();
   Piece<T> x[NV], dy[NV];
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int64_t row) {
+    if (row >= p.R) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * WR * 64 + l) * N, C = row < p.R ? (int)p.C : 0;
-      x[j].load((const T *)p.x + row * p.ldx, c, C);
-      dy[j].load((const T *)p.dy + row * p.lddy, c, C);
+      const Place<T, LANES> at(j, l, C);
+      if (!at.there) continue;
+      x[j].load((const T *)p.x + row * p.ldx, at.c);
+      dy[j].load((const T *)p.dy + row * p.lddy, at.c);
     }
-    mean = row < p.R ? p.stats[row] : 0.f;
-    rstd = row < p.R ? p.stats[p.R + row] : 0.f;
+    mean = p.stats[row];
+    rstd = p.stats[p.R + row];
   };
-  constexpr bool kAhead = WR < 16;
-  if (kAhead) fetch(r);
-  float w[NV][N], aw[NV][N], ab[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) x[j].v = dy[j].v = (T)0.f;
+  fetch(r);
+  __shared__ float lds[KEEP ? 1 : LANES * NV * N];
+  if (!KEEP) {
+    weights_to_lds<THREADS>(p.weight, p.w_dtype, C, 1.f, lds);
+    __syncthreads();
+  }
+  float w[KEEP ? NV : 1][N], aw[NV][N], ab[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_weights<N>(p.weight, p.w_dtype, (j * WR * 64 + l) * N, p.C, 1.f, w[j]);
+    const Place<T, LANES> at(j, l, C);
+    if (KEEP && at.there) load_weights<N>(p.weight, p.w_dtype, at.c, C, 1.f, w[KEEP ? j : 0]);
 #pragma unroll
     for (int i = 0; i < N; ++i) aw[j][i] = ab[j][i] = 0.f;
   }
-  const float n = (float)p.C;
+  const float n = (float)C;
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.R; r0 += step, r += step, turn ^= 1) {
     float xh[NV][N], g[NV][N], a = 0.f, b = 0.f;
-    if (!kAhead) fetch(r);
     const float rs = rstd;
+    const bool own = r < p.R;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Place<T, LANES> at(j, l, C);
+      if (!KEEP && at.there) {
+        int c = at.c;
+        asm volatile("" : "+v"(c));  // read for each row: kept for all, they would need too many registers
+        Row<float, N, 4>::load(lds + c, w[0]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = (float)dy[j].v[i];
+        xh[j][i] = ((float)x[j].v[i] - mean) * rs;
+        g[j][i] = at.there ? d * w[KEEP ? j : 0][i] : 0.f;
+        if (own) {
+          aw[j][i] = fmaf(d, xh[j][i], aw[j][i]);
+          ab[j][i] += d;
+        }
+        if (i >= at.skip) {
+          a += g[j][i];
+          b = fmaf(g[j][i], xh[j][i], b);
+        }
+      }
+    }
+    fetch(r + step);
+    row_sum<LANES>(a, b, sh[turn]);
+    a /= n;
+    b /= n;
+    if (!own) continue;
+    T *dx = (T *)p.out + r * p.C;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Place<T, LANES> at(j, l, C);
+      if (!at.there) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[j][i] = rs * (g[j][i] - a - xh[j][i] * b);
+      Row<T, N, (int)sizeof(T)>::store(dx + at.c, g[j]);
+    }
+  }
+  if (parts == nullptr) return;
+  // rows of a wave, then of the workgroup
+  if (LANES < 64) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = (float)dy[j].v[i];
-        xh[j][i] = (j * WR * 64 + l) * N + i < p.C ? ((float)x[j].v[i] - mean) * rs : 0.f;
-        aw[j][i] = fmaf(d, xh[j][i], aw[j][i]);
-        ab[j][i] += d;
-        g[j][i] = d * w[j][i];
-        a += g[j][i];
-        b = fmaf(g[j][i], xh[j][i], b);
+#pragma unroll
+        for (int off = LANES; off < 64; off <<= 1) {
+          aw[j][i] += __shfl_xor(aw[j][i], off, 64);
+          ab[j][i] += __shfl_xor(ab[j][i], off, 64);
+        }
       }
-    if (kAhead && r0 + step < p.R) fetch(r + step);
-    row_sum<WR>(a, b, sh[turn]);
-    a /= n;
-    b /= n;
-    if (r >= p.R) continue;
-    T *dx = (T *)p.out + r * p.C;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * WR * 64 + l) * N;
-      if (c >= p.C) continue;
-#pragma unroll
-      for (int i = 0; i < N; ++i) g[j][i] = rs * (g[j][i] - a - xh[j][i] * b);
-      store_piece<T, N>(dx, c, p.C, g[j]);
-    }
   }
-  if (parts == nullptr) return;
-  constexpr int kCols = WR * 64 * NV * N;
-  for (int k = 1; k < kRows; ++k) {
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kWide);
+  const bool adds = LANES >= 64 || (threadIdx.x & 63) < LANES;
+  for (int k = 1; k < kGroups; ++k) {
     __syncthreads();
-    if (wave / WR == k) {
+    if (group == k && adds) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        Row<float, N>::store(joined + (j * WR * 64 + l) * N, aw[j]);
-        Row<float, N>::store(joined + kCols + (j * WR * 64 + l) * N, ab[j]);
+        Row<float, N>::store(joined + (j * LANES + l) * N, aw[j]);
+        Row<float, N>::store(joined + kCols + (j * LANES + l) * N, ab[j]);
       }
     }
     __syncthreads();
-    if (wave < WR) {
+    if (group == 0 && adds) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float v[N];
-        Row<float, N>::load(joined + (j * WR * 64 + l) * N, v);
+        Row<float, N>::load(joined + (j * LANES + l) * N, v);
 #pragma unroll
         for (int i = 0; i < N; ++i) aw[j][i] += v[i];
-        Row<float, N>::load(joined + kCols + (j * WR * 64 + l) * N, v);
+        Row<float, N>::load(joined + kCols + (j * LANES + l) * N, v);
 #pragma unroll
         for (int i = 0; i < N; ++i) ab[j][i] += v[i];
       }
     }
   }
-  if (wave >= WR) return;
+  if (group > 0 || !adds) return;
   float *to = parts + (size_t)blockIdx.x * 2 * p.C;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * WR * 64 + l) * N;
-    if (c >= p.C) continue;
-    store_piece<float, N>(to, c, p.C, aw[j]);
-    store_piece<float, N>(to + p.C, c, p.C, ab[j]);
+    const Place<T, LANES> at(j, l, C);
+    if (!at.there) continue;
+    Row<float, N, 4>::store(to + at.c, aw[j]);
+    Row<float, N, 4>::store(to + p.C + at.c, ab[j]);
   }
 }
 
@@ -288,7 +353,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_ke
 #pragma unroll
       for (int i = 0; i < N; ++i) a += f[i];
     }
-    row_sum<16>(a, b, sh[0]);
+    row_sum<1024>(a, b, sh[0]);
     float mean = a / n;
     a = b = 0.f;
     for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
@@ -300,7 +365,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_ke
         b = fmaf(d, d, b);
       }
     }
-    row_sum<16>(a, b, sh[1]);
+    row_sum<1024>(a, b, sh[1]);
     const float rest = a / n, rstd = row_rstd(b / n, rest, p.eps);
     if (threadIdx.x == 0) {
       p.stats[r] = mean + rest;
@@ -346,7 +411,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_wide_dx
         b = fmaf(g[i], f[i], b);
       }
     }
-    row_sum<16>(a, b, sh[turn]);
+    row_sum<1024>(a, b, sh[turn]);
     a /= (float)p.C;
     b /= (float)p.C;
     for (int c = (int)threadIdx.x * N; c < p.C; c += 1024 * N) {
@@ -411,24 +476,31 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(NormArgs p, int g
 }
 
 // ---------------------------------------------------------------------------
-// How many waves a row takes and how many pieces a lane of it has
+// How many lanes a row takes.  (Rows shorter than a piece: the kernel for wide ones takes
+// any length.)
 template <typename T, class K> static hipError_t by_width(const NormArgs &a, hipStream_t s) {
   constexpr int NV = kNormLane / kPiece<T>;
-  if (a.C <= 512) return K::template rows<T, 1, NV / 2>(a, s);
-  if (a.C <= 1024) return K::template rows<T, 1, NV>(a, s);
-  if (a.C <= 2048) return K::template rows<T, 2, NV>(a, s);
-  if (a.C <= 4096) return K::template rows<T, 4, NV>(a, s);
-  if (a.C <= 8192) return K::template rows<T, 8, NV>(a, s);
-  if (a.C <= kNormRegisters) return K::template rows<T, 16, NV>(a, s);
+  if (a.C < kPiece<T>) return K::template wide<T>(a, s);
+  if (a.C <= 4 * kNormLane) return K::template rows<T, 4, NV>(a, s);
+  if (a.C <= 8 * kNormLane) return K::template rows<T, 8, NV>(a, s);
+  if (a.C <= 16 * kNormLane) return K::template rows<T, 16, NV>(a, s);
+  if (a.C <= 32 * kNormLane) return K::template rows<T, 32, NV>(a, s);
+  if (a.C <= 64 * kNormLane) return K::template rows<T, 64, NV>(a, s);
+  if (a.C <= 128 * kNormLane) return K::template rows<T, 128, NV>(a, s);
+  if (a.C <= 256 * kNormLane) return K::template rows<T, 256, NV>(a, s);
+  if (a.C <= 512 * kNormLane) return K::template rows<T, 512, NV>(a, s);
+  if (a.C <= kNormRegisters) return K::template rows<T, K::kLongest, NV * 1024 / K::kLongest>(a, s);
   return K::template wide<T>(a, s);
 }
 static int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
 
 struct NormForward {
-  template <typename T, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
-    constexpr int waves = WR < 4 ? 4 : WR, most = 256 * 24 / waves;
-    hipLaunchKernelGGL((layer_norm_kernel<T, waves, WR, NV>), dim3((unsigned)fewer((a.R + waves / WR - 1) / (waves / WR), most)),
-                       dim3(waves * 64), 0, s, a);
+  static constexpr int kLongest = 1024;  // lanes of a row above 8192
+  template <typename T, int LANES, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
+    constexpr int threads = LANES < 256 ? 256 : LANES, rows = threads / LANES;
+    constexpr int most = threads == 1024 ? 512 : 256 * 1536 / threads;
+    hipLaunchKernelGGL((layer_norm_kernel<T, threads, LANES, NV>),
+                       dim3((unsigned)fewer((a.R + rows - 1) / rows, most)), dim3(threads), 0, s, a);
     return hipGetLastError();
   }
   template <typename T> static hipError_t wide(const NormArgs &a, hipStream_t s) {
@@ -455,12 +527,16 @@ static hipError_t norm_join(const NormArgs &a, int groups, hipStream_t s) {
 }
 
 struct NormBackward {
+  static constexpr int kLongest = 512;  // (of 256 registers: the sums are two more for each element)
   static float *parts(const NormArgs &a) { return a.dweight == nullptr && a.dbias == nullptr ? nullptr : (float *)a.workspace; }
-  template <typename T, int WR, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
-    constexpr int waves = WR < 8 ? 8 : WR, most = kNormGroups * 8 / waves;
-    const int groups = (int)fewer((a.R + waves / WR - 1) / (waves / WR), most);
+  template <typename T, int LANES, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
+    constexpr int threads = LANES < 512 ? 512 : LANES, rows = threads / LANES;
+    constexpr bool keep = NV * kPiece<T> == kNormLane;
+    constexpr int most = keep ? kNormGroups : 256;
+    const int groups = (int)fewer((a.R + rows - 1) / rows, most);
     if (groups > 0) {
-      hipLaunchKernelGGL((layer_norm_backward_kernel<T, waves, WR, NV>), dim3((unsigned)groups), dim3(waves * 64), 0, s, a, parts(a));
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, threads, LANES, NV, keep>),
+                         dim3((unsigned)groups), dim3(threads), 0, s, a, parts(a));
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

@@ -49,4 +49,20 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+// Sums over groups of L lanes, L a power of two of at least 4, the same in all lanes of a
+// group: both lanes of a pair join the same two values
+template <int L> __device__ __forceinline__ float group_lanes_sum(float v) {
+  if (L == 64) return wave_sum(v);
+  v += lanes_moved<0xB1, 0xf>(v);  // lanes 1, 0, 3, 2 of four
+  v += lanes_moved<0x4E, 0xf>(v);  // lanes 2, 3, 0, 1
+  if (L >= 8) v += lanes_moved<0x141, 0xf>(v);  // eight lanes mirrored
+  if (L >= 16) v += lanes_moved<0x140, 0xf>(v);  // sixteen
+  if (L >= 32) {
+    const unsigned x = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);  // the values of two rows of 16
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
 }  // namespace nsg
