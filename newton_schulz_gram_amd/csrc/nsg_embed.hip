@@ -19,21 +19,69 @@
 namespace nsg {
 
 // ---------------------------------------------------------------------------
-// forward: one wave per 64 x 16 bytes of a token (a part); four waves of a workgroup
-// take 1 << lp parts of 4 >> lp tokens.
+// Rows in pieces of 16 bytes.  Long ones: one wave per 64 pieces (a part), four waves of a
+// workgroup take 1 << lp parts of 4 >> lp rows.  Rows of at most 32 pieces (SHORT): 1 << lp
+// lanes a row, several rows to a wave (524288 rows of 64 in bf16: 81 us, so 18).
 // ---------------------------------------------------------------------------
-struct EmbedParts {
-  int64_t t, part;
-  __device__ __forceinline__ explicit EmbedParts(int lp) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    t = (int64_t)blockIdx.x * (4 >> lp) + (wave >> lp);
-    part = ((int64_t)blockIdx.y << lp) + (wave & ((1 << lp) - 1));
+template <bool SHORT> struct Lane {
+  int64_t t, piece;
+  __device__ __forceinline__ explicit Lane(int lp) {
+    if (SHORT) {
+      t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lp;
+      piece = threadIdx.x & ((1 << lp) - 1);
+    } else {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      t = (int64_t)blockIdx.x * (4 >> lp) + (wave >> lp);
+      piece = (((int64_t)blockIdx.y << lp) + (wave & ((1 << lp) - 1))) * 64 + (threadIdx.x & 63);
+    }
   }
 };
 // (HIP counts a launch's threads in 32 bits)
-static int parts_log(int64_t rows, int64_t parts) { return rows > (1 << 23) || parts < 2 ? 0 : parts < 4 ? 1 : 2; }
-static dim3 parts_grid(int64_t rows, int64_t parts, int lp) {
-  return dim3((unsigned)((rows + (4 >> lp) - 1) / (4 >> lp)), (unsigned)((parts + (1 << lp) - 1) >> lp));
+struct LaneGrid {
+  bool is_short;
+  int lp;
+  dim3 grid;
+  LaneGrid(int64_t rows, int64_t pieces, bool can_be_short = true) {
+    is_short = can_be_short && pieces <= 32;
+    const int64_t parts = (pieces + 63) / 64;
+    if (is_short) {
+      lp = 0;
+      while ((1 << lp) < pieces) ++lp;
+      grid = dim3((unsigned)(((rows << lp) + 255) / 256));
+    } else {
+      lp = rows > (1 << 23) || parts < 2 ? 0 : parts < 4 ? 1 : 2;
+      grid = dim3((unsigned)((rows + (4 >> lp) - 1) / (4 >> lp)), (unsigned)((parts + (1 << lp) - 1) >> lp));
+    }
+  }
+};
+
+// N elements of a row from c on, zeros behind its end
+template <typename T, int N> struct Cells {
+  typedef T vec __attribute__((ext_vector_type(N)));
+  typedef vec mem __attribute__((aligned(sizeof(T))));
+  vec v;
+  __device__ __forceinline__ void load(const T *row, int64_t c, int64_t C) {
+    if (c + N <= C) {
+      v = *reinterpret_cast<const mem *>(row + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = c + i < C ? row[c + i] : (T)0.f;
+    }
+  }
+};
+template <typename T, int N> __device__ __forceinline__ void store_cells(T *row, int64_t c, int64_t C, const float (&f)[N]) {
+  if (c + N <= C) {
+    Row<T, N, (int)sizeof(T)>::store(row + c, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < C) row[c + i] = (T)f[i];
+  }
+}
+// A last piece that is not whole lies over the one before it: two lanes write the same there
+template <int N> __device__ __forceinline__ int64_t piece_at(int64_t piece, int64_t C) {
+  const int64_t c = piece * N;
+  return c + N > C && C >= N ? C - N : c;
 }
 
 // id i, or -1 where it is none of 0 .. V - 1
@@ -42,39 +90,32 @@ __device__ __forceinline__ int id_at(const void *ids, int wide, int64_t i, int64
   return v >= 0 && v < V ? (int)v : -1;
 }
 
-template <typename T, int ALIGN>
+template <typename T, bool SHORT>
 __global__ void __launch_bounds__(256) embedding_kernel(const void *__restrict__ ids, int wide, int64_t ntok,
                                                         const T *__restrict__ W, int64_t V, int64_t C, int64_t ldw,
                                                         float scale, int lp, T *__restrict__ out) {
   constexpr int N = 16 / (int)sizeof(T);
-  const EmbedParts at(lp);
-  const int64_t t = at.t, c = (at.part * 64 + (threadIdx.x & 63)) * N;
-  if (t >= ntok || c >= C) return;
-  const int v = id_at(ids, wide, t, V);
-  const T *from = W + (int64_t)v * ldw;
-  T *to = out + t * C;
-  if (c + N <= C) {
-    float f[N];
-    if (v >= 0) Row<T, N, ALIGN>::load(from + c, f);
+  const Lane<SHORT> at(lp);
+  if (at.t >= ntok || at.piece * N >= C) return;
+  const int64_t c = piece_at<N>(at.piece, C);
+  const int v = id_at(ids, wide, at.t, V);
+  Cells<T, N> row;
+  if (v >= 0) row.load(W + (int64_t)v * ldw, c, C);
+  float f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = v >= 0 ? f[i] * scale : 0.f;
-    Row<T, N, ALIGN>::store(to + c, f);
-  } else {
-    for (int64_t i = c; i < C; ++i) to[i] = (T)(v >= 0 ? (float)from[i] * scale : 0.f);
-  }
+  for (int i = 0; i < N; ++i) f[i] = v >= 0 ? (float)row.v[i] * scale : 0.f;
+  store_cells<T, N>(out + at.t * C, c, C, f);
 }
 
 template <typename T> static hipError_t embedding_t(const EmbedArgs &a, hipStream_t s) {
   constexpr int N = 16 / (int)sizeof(T);
-  const int64_t parts = (a.C + 64 * N - 1) / (64 * N);
-  const int lp = parts_log(a.T, parts);
-  const dim3 grid = parts_grid(a.T, parts, lp);
-  if (aligned16(a.x) && aligned16(a.out) && a.C % N == 0 && a.ld % N == 0)
-    hipLaunchKernelGGL((embedding_kernel<T, 16>), grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V, a.C, a.ld,
-                       a.scale, lp, (T *)a.out);
+  const LaneGrid g(a.T, (a.C + N - 1) / N);
+  if (g.is_short)
+    hipLaunchKernelGGL((embedding_kernel<T, true>), g.grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V, a.C, a.ld,
+                       a.scale, g.lp, (T *)a.out);
   else
-    hipLaunchKernelGGL((embedding_kernel<T, (int)sizeof(T)>), grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V,
-                       a.C, a.ld, a.scale, lp, (T *)a.out);
+    hipLaunchKernelGGL((embedding_kernel<T, false>), g.grid, dim3(256), 0, s, a.ids, a.wide, a.T, (const T *)a.x, a.V, a.C, a.ld,
+                       a.scale, g.lp, (T *)a.out);
   return hipGetLastError();
 }
 
@@ -339,12 +380,12 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortInput in, 
 // ---------------------------------------------------------------------------
 constexpr int kRunUnroll = 8;
 
-// Sorted tokens of a chunk: enough waves (a chunk's 64 x 16 bytes each) to fill the
-// chip, at least one round of loads, and few sums of parts of runs.
+// Sorted tokens of a chunk: enough rows on their way to keep the memory busy, at least one
+// round of loads, and few sums of parts of runs (524288 rows of 64 in bf16, chunks of 16,
+// 32 and 64: sums 18, 25 and 42 us, joining them 15, 9 and 6; 262144 in fp32: 19, 17, 24 and 12, 8, 5).
 static int64_t run_chunk(int64_t N, int64_t C) {
-  const int64_t parts = (C + 511) / 512;
   int64_t S = kRunUnroll;
-  while (S < 64 && N / (2 * S) * parts >= 8192) S *= 2;
+  while (S < 64 && N / (2 * S) * C >= 2048 * 512) S *= 2;
   return S;
 }
 static int64_t run_chunks(int64_t N, int64_t C) { return (N + run_chunk(N, C) - 1) / run_chunk(N, C); }
@@ -353,7 +394,7 @@ static int64_t run_chunks(int64_t N, int64_t C) { return (N + run_chunk(N, C) - 
 // run has here if it began before, and what its last one has if it began here and goes on
 static int64_t part_pitch(int64_t C) { return (C + 3) / 4 * 4; }
 
-// a chunk's runs; every value is the same in all lanes
+// a chunk's runs
 struct Chunk {
   int64_t p0, p1;
   bool before, after;  // the first run began in an earlier chunk; the last one goes on
@@ -365,40 +406,17 @@ struct Chunk {
   }
 };
 
-// N elements of a row from c on, zeros behind its end
-template <typename T, int N> struct Cells {
-  typedef T vec __attribute__((ext_vector_type(N)));
-  typedef vec mem __attribute__((aligned(sizeof(T))));
-  vec v;
-  __device__ __forceinline__ void load(const T *row, int64_t c, int64_t C) {
-    if (c + N <= C) {
-      v = *reinterpret_cast<const mem *>(row + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = c + i < C ? row[c + i] : (T)0.f;
-    }
-  }
-};
-template <typename T, int N> __device__ __forceinline__ void store_cells(T *row, int64_t c, int64_t C, const float (&f)[N]) {
-  if (c + N <= C) {
-    Row<T, N, (int)sizeof(T)>::store(row + c, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (c + i < C) row[c + i] = (T)f[i];
-  }
-}
-
-// One wave per chunk and 64 x 16 bytes of its rows.  With ADD a run's row of dW is read
-// together with its first row of dout.
-template <typename T, typename O, bool ADD>
+// A lane sums its piece of a chunk's rows.  With ADD a run's row of dW is read together with
+// its first row of dout.
+template <typename T, typename O, bool ADD, bool SHORT>
 __global__ void __launch_bounds__(256) embed_runs_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S, int64_t chunks, const T *__restrict__ dout,
                                                          int64_t ld, int64_t C, float scale, int lp,
                                                          O *__restrict__ out, float *__restrict__ parts, int64_t pitch) {
   constexpr int N = 16 / (int)sizeof(T);
-  const EmbedParts at(lp);
-  const int64_t c = (at.part * 64 + (threadIdx.x & 63)) * N;
-  if (at.t >= chunks || c >= C) return;
+  const Lane<SHORT> at(lp);
+  if (at.t >= chunks || at.piece * N >= C) return;
+  // (with ADD no element may be read and written by two lanes)
+  const int64_t c = ADD ? at.piece * N : piece_at<N>(at.piece, C);
   const Chunk ch(pairs, ntok, S, at.t);
   float acc[N];
   Cells<O, N> old;
@@ -459,9 +477,9 @@ template <typename O>
 __global__ void __launch_bounds__(256) embed_join_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S,
                                                          int64_t chunks, int64_t C, float scale, bool add, int lp,
                                                          O *__restrict__ out, const float *__restrict__ parts, int64_t pitch) {
-  const EmbedParts at(lp);
+  const Lane<false> at(lp);
   const int lane = threadIdx.x & 63;
-  const int64_t c = (at.part * 64 + lane) * 4;
+  const int64_t c = at.piece * 4;
   if (at.t >= chunks) return;
   const Chunk ch(pairs, ntok, S, at.t);
   const int run = pairs[ch.p1 - 1].key;
@@ -517,21 +535,18 @@ template <typename T, typename O> static hipError_t runs_to(const EmbedArgs &a, 
   const Pair *pairs = (const Pair *)(ws + sp.pairs);
   float *parts = (float *)(ws + sp.parts);
   const int64_t S = run_chunk(a.T, a.C), chunks = run_chunks(a.T, a.C), pitch = part_pitch(a.C);
-  int64_t n = (a.C + 64 * N - 1) / (64 * N);
-  int lp = parts_log(chunks, n);
-  const dim3 grid = parts_grid(chunks, n, lp);
-  if (a.accumulate)
-    hipLaunchKernelGGL((embed_runs_kernel<T, O, true>), grid, dim3(256), 0, s, pairs, a.T, S, chunks, (const T *)a.x, a.ld,
-                       a.C, a.scale, lp, (O *)a.out, parts, pitch);
-  else
-    hipLaunchKernelGGL((embed_runs_kernel<T, O, false>), grid, dim3(256), 0, s, pairs, a.T, S, chunks, (const T *)a.x, a.ld,
-                       a.C, a.scale, lp, (O *)a.out, parts, pitch);
+  const LaneGrid g(chunks, (a.C + N - 1) / N);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, g.grid, dim3(256), 0, s, pairs, a.T, S, chunks, (const T *)a.x, a.ld, a.C, a.scale, g.lp, (O *)a.out,
+                       parts, pitch);
+  };
+  if (a.accumulate) g.is_short ? go(embed_runs_kernel<T, O, true, true>) : go(embed_runs_kernel<T, O, true, false>);
+  else g.is_short ? go(embed_runs_kernel<T, O, false, true>) : go(embed_runs_kernel<T, O, false, false>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks < 2) return e;
-  n = (a.C + 255) / 256;
-  lp = parts_log(chunks, n);
-  hipLaunchKernelGGL((embed_join_kernel<O>), parts_grid(chunks, n, lp), dim3(256), 0, s, pairs, a.T, S, chunks, a.C, a.scale,
-                     a.accumulate != 0, lp, (O *)a.out, parts, pitch);
+  const LaneGrid j(chunks, (a.C + 3) / 4, false);
+  hipLaunchKernelGGL((embed_join_kernel<O>), j.grid, dim3(256), 0, s, pairs, a.T, S, chunks, a.C, a.scale, a.accumulate != 0, j.lp,
+                     (O *)a.out, parts, pitch);
   return hipGetLastError();
 }
 template <typename T> static hipError_t runs_t(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {
