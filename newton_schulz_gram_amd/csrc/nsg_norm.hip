@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(NormArgs p
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) x[j].v = dy[j].v = (T)0.f;
-  fetch(r);
+  constexpr bool kAhead = KEEP;  // (else the registers hold no next row: 6096 rows of 11008 102 us so, 3048 in fp32 97, ahead 100 and 139)
+  if (kAhead) fetch(r);
   __shared__ float lds[KEEP ? 1 : LANES * NV * N];
   if (!KEEP) {
     weights_to_lds<THREADS>(p.weight, p.w_dtype, C, 1.f, lds);
@@ -249,6 +250,7 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(NormArgs p
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.R; r0 += step, r += step, turn ^= 1) {
     float xh[NV][N], g[NV][N], a = 0.f, b = 0.f;
+    if (!kAhead) fetch(r);
     const float rs = rstd;
     const bool own = r < p.R;
 #pragma unroll
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(NormArgs p
         }
       }
     }
-    fetch(r + step);
+    if (kAhead) fetch(r + step);
     row_sum<LANES>(a, b, sh[turn]);
     a /= n;
     b /= n;

@@ -406,8 +406,8 @@ template <bool SIGMOID> __device__ __forceinline__ float chosen_weight(const Rou
 }
 
 // ---- several tokens to a wave: up to 256 experts ---------------------------------
-// LDS of a token: the chosen experts and their logits; with a bias also those that come
-// next, their exact keys and the order of these
+// LDS of a token: the chosen experts and their keys, then logits; with a bias also those
+// that come next, their exact keys and the order of these
 static __host__ __device__ int group_kept(int k, int E, bool bias) { return bias ? (k + kNext <= E ? k + kNext : E + 1) : k; }
 static __host__ __device__ int group_room(int k, int E, bool bias) { return group_kept(k, E, bias) * (bias ? 20 : 8); }
 
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
   double *const exact = reinterpret_cast<double *>(room) + (BIAS ? token * kept : 0);
   int32_t *const id = reinterpret_cast<int32_t *>(room + (BIAS ? tokens * kept * 8 : 0)) + token * kept;
   float *const val = reinterpret_cast<float *>(id + tokens * kept);
-  int32_t *const sorted = id + 2 * tokens * kept;  // (BIAS)
+  int32_t *const order = id + 2 * tokens * kept;  // (BIAS)
   const bool balance = rows != nullptr;
   if (balance) balance_clear(p, count);
   float acc[N], bias[N];
@@ -455,33 +455,35 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     if (BIAS) unit = !SIGMOID ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
     make_keys<N, BIAS>(l, s, unit, bias, key);
     int found, whole_key[N];
+    bool moved = false;  // choice j lies at order[j]
 #pragma unroll
     for (int i = 0; i < N; ++i) whole_key[i] = key_of(key[i]);
     if (BIAS) {
       Closeness c;
       found = choose_near<N, L>(whole_key, p.k, sub, id, val, SIGMOID ? 1.f : unit, c);
+      wave_sync();
+      for (int j = sub; j < c.taken; j += L) val[j] = logit(p, t, id[j]);
       if (__ballot(c.close) != 0) {
         // keys in 64 bits: of the taken experts, or all where the next ones did not end
         const double all = SIGMOID ? 1.0 : exact_sum<N, L>(l, top);
-        const bool few = c.close && !c.more;
-        for (int j = sub; few && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(logit(p, t, id[j]), top, all, p.bias[id[j]]);
+        moved = c.close && !c.more;
         wave_sync();
-        for (int j = sub; few && j < c.taken; j += L) {
+        for (int j = sub; moved && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(val[j], top, all, p.bias[id[j]]);
+        wave_sync();
+        for (int j = sub; moved && j < c.taken; j += L) {
           int rank = 0;
           for (int i = 0; i < c.taken; ++i) rank += exact[i] > exact[j] || (exact[i] == exact[j] && id[i] < id[j]);
-          sorted[rank] = id[j];
+          order[rank] = j;
         }
-        wave_sync();
-        for (int j = sub; few && j < found; j += L) id[j] = sorted[j];
         if (__ballot(c.more) != 0) {
           double key64[N];
           exact_keys<N, SIGMOID>(l, bias, top, all, key64);
           wave_sync();
           choose<N, L, double>(key64, p.k, sub, id, val, c.more);
+          wave_sync();
+          for (int j = sub; c.more && j < found; j += L) val[j] = logit(p, t, id[j]);
         }
-        wave_sync();
       }
-      for (int j = sub; j < found; j += L) val[j] = logit(p, t, id[j]);
     } else {
       found = choose<N, L, int>(whole_key, p.k, sub, id, val, true);
     }
@@ -491,11 +493,11 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     if (p.normalize) {
       if (BIAS) {
         high = -INFINITY;
-        for (int j = sub; j < found; j += L) high = fmaxf(high, val[j]);
+        for (int j = sub; j < found; j += L) high = fmaxf(high, val[moved ? order[j] : j]);
         high = group_max<L>(high);
       }
       high = score_shift<SIGMOID>(high);
-      for (int j = sub; j < found; j += L) whole += shifted_score<SIGMOID>(val[j], high);
+      for (int j = sub; j < found; j += L) whole += shifted_score<SIGMOID>(val[BIAS && moved ? order[j] : j], high);
       whole = p.scale * inverse_sum(group_sum<L>(whole));
     } else if (!SIGMOID) {
       whole = p.scale * inverse_sum(sum);
@@ -503,12 +505,15 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     if (t < p.T) {
       for (int j = sub; j < p.k; j += L) {
         float w = 0.f;
+        int e = -1;
         if (j < found) {
-          w = chosen_weight<SIGMOID>(p, val[j], high, whole);
+          const int at = BIAS && moved ? order[j] : j;
+          e = id[at];
+          w = chosen_weight<SIGMOID>(p, val[at], high, whole);
           if (!SIGMOID && sum != sum) w = sum;  // with softmax a NaN among the logits is in all weights
-          if (balance) atomicAdd(&count[id[j]], 1);
+          if (balance) atomicAdd(&count[e], 1);
         }
-        p.ids[t * p.k + j] = j < found ? id[j] : -1;
+        p.ids[t * p.k + j] = e;
         p.weights[t * p.k + j] = w;
       }
     }
