@@ -266,7 +266,10 @@ template <int N, bool BIAS> __device__ __forceinline__ void make_keys(const floa
 // fp32 keys as whole numbers in the same order (both zeros alike), which take fewer
 // instructions; never chosen: kNever
 constexpr int kNever = INT32_MIN;
-__device__ __forceinline__ int key_of(float f) { return f > -INFINITY ? ordered(f + 0.f) : kNever; }
+__device__ __forceinline__ int key_of(float f) {
+  const int i = __builtin_bit_cast(int, f + 0.f);
+  return f > -INFINITY ? i ^ ((i >> 31) & 0x7fffffff) : kNever;
+}
 
 __device__ __forceinline__ bool never(int key) { return key == kNever; }
 __device__ __forceinline__ bool never(double key) { return !(key > -(double)INFINITY); }
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
   fetch((int64_t)blockIdx.x * tokens + token);
   for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < p.T; t0 += step) {
     const int64_t t = t0 + token;
-    float l[N], s[N], key[N];
+    float l[N], s[N];
     next.get(p, l);
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = counts ? l[i] : -INFINITY;
@@ -453,14 +456,16 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     float sum = 0.f, unit = 1.f;
     if (balance || BIAS || !SIGMOID) sum = scores<SIGMOID, N, L>(l, shift, s);
     if (BIAS) unit = !SIGMOID ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
-    make_keys<N, BIAS>(l, s, unit, bias, key);
-    int found, whole_key[N];
+    int found, key[N];
     bool moved = false;  // choice j lies at order[j]
 #pragma unroll
-    for (int i = 0; i < N; ++i) whole_key[i] = key_of(key[i]);
+    for (int i = 0; i < N; ++i) {
+      key[i] = key_of(BIAS ? fmaf(s[i], unit, bias[i]) : l[i]);
+      if (BIAS) key[i] = l[i] > -INFINITY ? key[i] : kNever;
+    }
     if (BIAS) {
       Closeness c;
-      found = choose_near<N, L>(whole_key, p.k, sub, id, val, SIGMOID ? 1.f : unit, c);
+      found = choose_near<N, L>(key, p.k, sub, id, val, SIGMOID ? 1.f : unit, c);
       wave_sync();
       for (int j = sub; j < c.taken; j += L) val[j] = logit(p, t, id[j]);
       if (__ballot(c.close) != 0) {
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
         }
       }
     } else {
-      found = choose<N, L, int>(whole_key, p.k, sub, id, val, true);
+      found = choose<N, L, int>(key, p.k, sub, id, val, true);
     }
     wave_sync();
     // a choice to a lane
