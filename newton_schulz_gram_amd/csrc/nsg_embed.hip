@@ -41,8 +41,8 @@ struct LaneGrid {
   bool is_short;
   int lp;
   dim3 grid;
-  LaneGrid(int64_t rows, int64_t pieces, bool can_be_short = true) {
-    is_short = can_be_short && pieces <= 32;
+  LaneGrid(int64_t rows, int64_t pieces) {
+    is_short = pieces <= 32;
     const int64_t parts = (pieces + 63) / 64;
     if (is_short) {
       lp = 0;
@@ -472,39 +472,78 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const Pair *__restrict_
   if (run >= 0) close(ch.after);
 }
 
-// The run that begins in chunk t and goes on: its parts in the order of the chunks.
+// The run that begins in chunk t and goes on: its parts in the order of the chunks.  A wave
+// takes 256 elements of it, a workgroup as many of 16 chunks.  A run of many parts (a
+// padding token's; at most one begins in a workgroup's chunks) is summed by all its waves,
+// wave w every 16th part from w on: one of 8192 parts of 1024 takes 134 us, by one wave 609;
+// joining the runs of 65536 tokens of 4096, half of which are the same, 33 us, by one wave each 73.
+constexpr int kJoinWaves = 16;
+constexpr int kJoinAlone = 32;  // parts of a run that one wave sums
+static_assert(kJoinAlone >= kJoinWaves, "one run of many parts in a workgroup");
 template <typename O>
-__global__ void __launch_bounds__(256) embed_join_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S,
-                                                         int64_t chunks, int64_t C, float scale, bool add, int lp,
-                                                         O *__restrict__ out, const float *__restrict__ parts, int64_t pitch) {
-  const Lane<false> at(lp);
-  const int lane = threadIdx.x & 63;
-  const int64_t c = at.piece * 4;
-  if (at.t >= chunks) return;
-  const Chunk ch(pairs, ntok, S, at.t);
-  const int run = pairs[ch.p1 - 1].key;
-  if (!ch.after || (ch.before && pairs[ch.p0].key == run)) return;
-  // chunks that the run goes on in
-  int64_t more = 0;
-  for (;;) {
-    const int64_t q = (at.t + 1 + more + lane) * S;
-    const uint64_t on = __ballot(q < ntok && pairs[q < ntok ? q : 0].key == run);
-    if (on != ~0ull) {
-      more += __ffsll((long long)~on) - 1;
-      break;
+__global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S,
+                                                                     int64_t chunks, int64_t C, float scale, bool add,
+                                                                     O *__restrict__ out, const float *__restrict__ parts,
+                                                                     int64_t pitch) {
+  __shared__ int64_t many;  // parts of the run that all waves sum, 0: none
+  __shared__ int who;       // whose run that is
+  __shared__ float sums[kJoinWaves][256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * kJoinWaves, t = t0 + wave, c = (int64_t)blockIdx.y * 256 + lane * 4;
+  if (threadIdx.x == 0) many = 0;
+  __syncthreads();
+  int run = -1;
+  int64_t more = 0;  // chunks that the run goes on in
+  if (t < chunks) {
+    const Chunk ch(pairs, ntok, S, t);
+    const int last = pairs[ch.p1 - 1].key;
+    if (ch.after && !(ch.before && pairs[ch.p0].key == last)) run = last;
+  }
+  if (run >= 0) {
+    // chunks behind t that begin with it: the first so many of `left`
+    for (int64_t left = chunks - 1 - t, unit = 1; left > 0; unit = (left + 63) / 64) {
+      const int64_t q = more + (lane + 1) * unit;
+      const uint64_t on = __ballot(q <= more + left && pairs[(q <= more + left ? t + q : t) * S].key == run);
+      const int n = on == ~0ull ? 64 : __ffsll((long long)~on) - 1;
+      more += n * unit;
+      left = min(left - n * unit, n == 64 ? left : unit - 1);
     }
-    more += 64;
+    if (more > kJoinAlone && lane == 0) {
+      many = more;
+      who = wave;
+    }
   }
-  if (c >= C) return;
-  float acc[4];
-  Row<float, 4>::load(parts + (at.t * 2 + 1) * pitch + c, acc);
+  __syncthreads();
+  // parts i, i + step, ... of the run that begins in chunk `from`
+  auto add_parts = [&](int64_t from, int64_t i, int64_t step, int64_t n, float(&acc)[4]) {
+    if (c >= C) return;
 #pragma unroll 8
-  for (int64_t i = 1; i <= more; ++i) {
-    float f[4];
-    Row<float, 4>::load(parts + (at.t + i) * 2 * pitch + c, f);
+    for (; i <= n; i += step) {
+      float f[4];
+      Row<float, 4>::load(parts + (from + i) * 2 * pitch + c, f);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] += f[v];
+      for (int v = 0; v < 4; ++v) acc[v] += f[v];
+    }
+  };
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (run >= 0 && c < C) Row<float, 4>::load(parts + (t * 2 + 1) * pitch + c, acc);
+  if (more <= kJoinAlone) add_parts(t, 1, 1, more, acc);
+  if (many > 0) {
+    float own[4] = {0.f, 0.f, 0.f, 0.f};
+    add_parts(t0 + who, 1 + wave, kJoinWaves, many, own);
+    Row<float, 4>::store(&sums[wave][lane * 4], own);
+    __syncthreads();
+    if (wave == who) {
+#pragma unroll
+      for (int i = 0; i < kJoinWaves; ++i) {
+        float f[4];
+        Row<float, 4>::load(&sums[i][lane * 4], f);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] += f[v];
+      }
+    }
   }
+  if (run < 0 || c >= C) return;
   O *row = out + (int64_t)run * C;
   Cells<O, 4> old;
   if (add) old.load(row, c, C);
@@ -544,9 +583,9 @@ template <typename T, typename O> static hipError_t runs_to(const EmbedArgs &a, 
   else g.is_short ? go(embed_runs_kernel<T, O, false, true>) : go(embed_runs_kernel<T, O, false, false>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks < 2) return e;
-  const LaneGrid j(chunks, (a.C + 3) / 4, false);
-  hipLaunchKernelGGL((embed_join_kernel<O>), j.grid, dim3(256), 0, s, pairs, a.T, S, chunks, a.C, a.scale, a.accumulate != 0, j.lp,
-                     (O *)a.out, parts, pitch);
+  const dim3 grid((unsigned)((chunks + kJoinWaves - 1) / kJoinWaves), (unsigned)((a.C + 255) / 256));
+  hipLaunchKernelGGL((embed_join_kernel<O>), grid, dim3(kJoinWaves * 64), 0, s, pairs, a.T, S, chunks, a.C, a.scale,
+                     a.accumulate != 0, (O *)a.out, parts, pitch);
   return hipGetLastError();
 }
 template <typename T> static hipError_t runs_t(const EmbedArgs &a, const EmbedSpace &sp, hipStream_t s) {

@@ -318,6 +318,26 @@ def test_embedding_offsets_past_32_bits():
     assert torch.equal(dW[ids[:5]], (rows.float() * 2).bfloat16())
 
 
+@pytest.mark.parametrize("C", [3, 64, 260, 1030])
+@pytest.mark.parametrize("lengths", ["one id", "half of them", "around 32 parts", "many long ones"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_gradient_of_ids_that_come_often(C, lengths, accumulate):
+    """Runs of equal ids over few and many chunks of the sorted list (of 8 tokens or more),
+    whole numbers whose sums are exact in fp32 in any order."""
+    n = {"one id": [30000],
+         "half of them": [1] * 9000 + [15000] + [3] * 2000,
+         "around 32 parts": [8 * k + d for k in range(29, 37) for d in (-1, 0, 1, 5)] * 3 + [1, 0, 2],
+         "many long ones": [2000, 0, 1, 1999, 2001] * 4 + [513] * 7}[lengths]
+    ids = torch.arange(len(n)).repeat_interleave(torch.tensor(n))
+    ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(5))].cuda()
+    dout = integers(4, (len(ids), C), 6, lo=-4).to(torch.bfloat16)
+    out = integers(100, (len(n), C), 7, lo=-100).float()
+    want = out.double().cpu() if accumulate else torch.zeros(len(n), C, dtype=torch.float64)
+    want.index_add_(0, ids.cpu(), dout.double().cpu(), alpha=2)
+    got = nsg.embedding_backward(dout, ids, len(n), scale=2.0, out=out, accumulate=accumulate)
+    assert torch.equal(got.double().cpu(), want)
+
+
 def test_embedding_of_many_rows():
     """Output and dout past 32-bit offsets."""
     T, V, C = 700_000, 50, 4096
