@@ -144,8 +144,8 @@ __device__ __forceinline__ int ordered(float f) {
 __device__ __forceinline__ float unordered(int i) { return __builtin_bit_cast(float, i ^ ((i >> 31) & 0x7fffffff)); }
 // Largest of the group in whole numbers, which a move between lanes and the comparison
 // take one instruction for (floats: three)
-template <int L> __device__ __forceinline__ int group_max(int v) {
-  auto moved = [](int x, auto ctrl) { return __builtin_amdgcn_update_dpp(x, x, decltype(ctrl)::value, 0xf, 0xf, true); };
+template <int L, typename I> __device__ __forceinline__ I group_max_of(I v) {
+  auto moved = [](I x, auto ctrl) { return (I)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(ctrl)::value, 0xf, 0xf, true); };
   v = max(v, moved(v, std::integral_constant<int, 0xB1>()));
   v = max(v, moved(v, std::integral_constant<int, 0x4E>()));
   if (L >= 16) {
@@ -154,14 +154,16 @@ template <int L> __device__ __forceinline__ int group_max(int v) {
   }
   if (L >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
-    v = max((int)r[0], (int)r[1]);
+    v = max((I)r[0], (I)r[1]);
   }
   if (L >= 64) {
     const auto r = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
-    v = max((int)r[0], (int)r[1]);
+    v = max((I)r[0], (I)r[1]);
   }
   return v;
 }
+template <int L> __device__ __forceinline__ int group_max(int v) { return group_max_of<L, int>(v); }
+template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t v) { return group_max_of<L, uint32_t>(v); }
 template <int L> __device__ __forceinline__ float group_max(float v) { return unordered(group_max<L>(ordered(v))); }
 template <int L> __device__ __forceinline__ float group_sum(float v) {
   return group_join<L>(v, [](float a, float b) { return a + b; });
@@ -180,7 +182,7 @@ __device__ __forceinline__ void wave_sync() {
 // ---------------------------------------------------------------------------
 // scores
 // ---------------------------------------------------------------------------
-// e^x for x <= 0 by the hardware's 2^x (within 1 unit): the argument's rounding makes it |x|
+// e^x, mostly for x <= 0, by the hardware's 2^x (within 1 unit): the argument's rounding makes it |x|
 // roundings, which for the scores e^(l - top) of a token is less than one of the largest
 __device__ __forceinline__ float exp_down(float x) {
   return __builtin_amdgcn_exp2f(fmaf(x, 1.44269502f, x * 1.9259630e-8f));  // the two parts of log2 e
@@ -195,10 +197,8 @@ template <bool SIGMOID> __device__ __forceinline__ float shifted_score(float l, 
   if (!SIGMOID) return exp_down(l - shift);
   return exp_down(fminf(l, 0.f) - shift) * inverse(1.f + exp_down(-fabsf(l)));
 }
-__device__ __forceinline__ float sigmoid(float l) {
-  const float e = exp_down(-fabsf(l));
-  return (l >= 0.f ? 1.f : e) * inverse(1.f + e);
-}
+// (below -88, where e^-l leaves fp32, and the score its normal numbers: 0)
+__device__ __forceinline__ float sigmoid(float l) { return inverse(1.f + exp_down(-l)); }
 
 // A token's scores times a factor that they share, so that none that matters under- or
 // overflows: softmax e^(l - shift) with shift the largest logit, sigmoid
@@ -224,12 +224,13 @@ template <bool SIGMOID, int N, int L> __device__ __forceinline__ float scores(co
 // ---------------------------------------------------------------------------
 // choice
 // ---------------------------------------------------------------------------
-// fp32 keys of scores with a bias are off by rounding: the scores, at most `size`, by less
+// fp32 keys of scores with a bias are off by rounding: softmax scores, at most `size`, by less
 // than 44 roundings of it (5 of the exponential; its sum's 4 + ln 1024 of the terms and 22
-// of adding; the quotient's), the keys by one of their own.  Two that are further apart
-// than this are in the order of the exact ones.
-__device__ __forceinline__ float key_margin(float size, float a, float b) {
-  return 0x1p-24f * (96.f * size + 8.f * fmaxf(fabsf(a), fabsf(b)));
+// of adding; the quotient's), sigmoid ones by less than 6 of 1 (1.3 of the exponential, which
+// s (1 - s) weakens, 1 of the sum, 2 of its inverse, 1 of a product), the keys by one of their
+// own.  Two that are further apart than this are in the order of the exact ones.
+template <bool SIGMOID> __device__ __forceinline__ float key_margin(float size, float a, float b) {
+  return 0x1p-24f * (SIGMOID ? 12.f + 4.f * fmaxf(fabsf(a), fabsf(b)) : fmaf(96.f, size, 4.f * fmaxf(fabsf(a), fabsf(b))));
 }
 // The key in 64 bits; `all`: the sum of e^(l - top)
 template <bool SIGMOID> __device__ __forceinline__ double exact_key(float l, float top, double all, float bias) {
@@ -253,7 +254,7 @@ template <int N, bool SIGMOID> __device__ __forceinline__ void exact_keys(const 
     if (!(key[i] > -(double)INFINITY)) key[i] = -(double)INFINITY;
   }
 }
-// fp32 keys: logits, or scores s `whole` with the bias; -inf (kNever) for what is never chosen
+// fp32 keys: logits, or scores s `whole` with the bias; -inf for what is never chosen
 template <int N, bool BIAS> __device__ __forceinline__ void make_keys(const float (&l)[N], const float (&s)[N], float whole,
                                                                       const float (&bias)[N], float (&key)[N]) {
 #pragma unroll
@@ -329,41 +330,79 @@ __device__ __forceinline__ int choose(K (&key)[N], int k, int sub, int32_t *id, 
   return found;
 }
 
-// The same with fp32 keys of scores with a bias.  Where two that follow each other are too
-// near to tell (`close`), the first k in the right order are among them and those that come
-// next, until one is far enough from the k-th: these are taken too (`taken` in all), at most
-// kNext of them; `more`: there are more.
+// Up to 256 experts: keys of 31 bits, the fp32 key's order in the upper ones and the expert
+// in the lowest kIdBits, lower ones first; 0: never chosen.  No two are equal, so the largest
+// key below the one before it is the next choice: a subtraction for each and a maximum, about
+// 20 instructions a choice of 8 experts a lane; finding the lane and taking the key out are
+// 50 (16384 tokens of 256, k = 8: 8.2 us, with a bias 14; so 10.1 and 17.2).  16-bit logits
+// keep all of their bits.  Of other keys the last bits are lost: the first k in the right
+// order are among the first k and those that come next, until one is too far from the k-th.
+// These are taken too (`taken` in all), at most kNext of them; `more`: there are more.
 constexpr int kNext = 16;
-struct Closeness {
-  bool close, more;
-  int taken;
+template <int N, int L> struct Packed {
+  static constexpr uint32_t kLast = N * L - 1;
+  // -inf and NaN: what is never chosen, below kLeast
+  static constexpr uint32_t kLeast = 0x400000;
+  static __device__ __forceinline__ uint32_t pack(float key, uint32_t e) {
+    const uint32_t i = __builtin_bit_cast(uint32_t, fmaxf(key, -INFINITY));
+    return ((i ^ ((uint32_t)((int)i >> 31) | 0x80000000u)) >> 1 & ~kLast) | (kLast - e);
+  }
+  static __device__ __forceinline__ int expert(uint32_t k) { return (int)(kLast - (k & kLast)); }
+  // the fp32 key, of a 16-bit one all, else up to 2 N L steps of fp32 below it
+  static __device__ __forceinline__ float key(uint32_t k) {
+    const int i = (int)((k & ~kLast) << 1 ^ 0x80000000u);
+    return unordered(i < 0 ? i | (int)(2 * kLast + 1) : i);
+  }
+  uint32_t top;  // the last choice; at first above all keys, or where nothing is chosen 0
+  __device__ __forceinline__ explicit Packed(bool counts) : top(counts ? 1u << 31 : 0) {}
+  __device__ __forceinline__ bool next(const uint32_t (&keys)[N]) {
+    uint32_t best = keys[0] - top;  // of keys below it in the upper half, largest for the largest
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = max(best, keys[i] - top);
+    best = group_max<L>(best);
+    const bool below = best >> 31;
+    top = below ? top + best : top;
+    return below && top >= kLeast;
+  }
 };
-template <int N, int L>
-__device__ __forceinline__ int choose_near(int (&key)[N], int k, int sub, int32_t *id, float *val, float size, Closeness &c) {
-  const uint64_t group = group_lanes<L>();
-  c.taken = choose<N, L, int>(key, k, sub, id, val, true);
-  const int found = c.taken;
-  // one that comes next tells how close the k-th is to it
-  bool on = choose_one<N, L, int>(key, k, sub, id, val, true);
-  c.taken += on;
-  wave_sync();
-  const float margin = c.taken > 0 ? key_margin(size, val[0], val[c.taken - 1]) : 0.f;
-  bool near = false;
-  for (int j = sub; j + 1 < c.taken; j += L) near = near || !(val[j] - val[j + 1] > margin);
-  c.close = (__ballot(near) & group) != 0;
-  on = on && !(val[k - 1] - val[k] > margin);
-  c.more = false;
-  for (int j = k + 1; __ballot(on) != 0; ++j) {
+struct Taken {
+  int found, taken;  // at most k; with those that come next
+  bool more;
+};
+// The largest keys to list.  `look`: with those that come next, for keys of scores of at most
+// `size` with a bias, or of logits, which are near where only lost bits differ.
+template <int N, int L, bool SIGMOID, bool BIAS>
+__device__ __forceinline__ Taken choose_packed(const uint32_t (&keys)[N], bool counts, int k, int sub, uint32_t *list, bool look,
+                                               float size) {
+  typedef Packed<N, L> P;
+  P r(counts);
+  Taken c{0, 0, false};
+  for (int j = 0; j < k; ++j) {
+    c.found += r.next(keys);
+    if (sub == 0) list[j] = r.top;
+  }
+  c.taken = c.found;
+  if (!look) return c;
+  const uint32_t kth = r.top;
+  // (of the k-th, one that comes next is always taken: the order of neighbours shows how
+  // close they are)
+  bool on = c.found == k;
+  for (int j = k; __ballot(on) != 0; ++j) {
     if (j == k + kNext) {
       c.more = on;
       break;
     }
-    on = choose_one<N, L, int>(key, j, sub, id, val, on) && on;
-    wave_sync();
+    on = r.next(keys) && on;
+    if (on && sub == 0) list[j] = r.top;
     c.taken += on;
-    on = on && !(val[k - 1] - val[j] > margin);
+    if (!BIAS) {
+      on = on && (kth & ~P::kLast) == (r.top & ~P::kLast);
+    } else {
+      const float x = P::key(kth), y = P::key(r.top), lost = 0x1p-24f * (4 * P::kLast + 4);
+      on = on && !(x - y > key_margin<SIGMOID>(size, x, y) + lost * fmaxf(fabsf(x), fabsf(y)));
+    }
   }
-  return found;
+  return c;
 }
 
 struct BalanceRow {  // a workgroup's sum and count of an expert; behind the last one, its tokens
@@ -409,10 +448,11 @@ template <bool SIGMOID> __device__ __forceinline__ float chosen_weight(const Rou
 }
 
 // ---- several tokens to a wave: up to 256 experts ---------------------------------
-// LDS of a token: the chosen experts and their keys, then logits; with a bias also those
-// that come next, their exact keys and the order of these
-static __host__ __device__ int group_kept(int k, int E, bool bias) { return bias ? (k + kNext <= E ? k + kNext : E + 1) : k; }
-static __host__ __device__ int group_room(int k, int E, bool bias) { return group_kept(k, E, bias) * (bias ? 20 : 8); }
+// LDS of a token: the chosen keys, then experts, and their logits; where keys lose bits
+// (`look`) also those that come next, their whole keys and the order of these
+static __host__ __device__ bool group_looks(const RouteArgs &p) { return p.bias != nullptr || p.dtype == NSG_F32; }
+static __host__ __device__ int group_kept(int k, int E, bool look) { return look ? (k + kNext <= E ? k + kNext : E + 1) : k; }
+static __host__ __device__ int group_room(int k, int E, bool look) { return group_kept(k, E, look) * (look ? 20 : 8); }
 
 template <int N, int L, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, BalanceRow *__restrict__ rows, int64_t pitch) {
@@ -420,11 +460,13 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
   __shared__ int32_t count[N * L + 1];
   const int tokens = blockDim.x / L;
   const int sub = threadIdx.x % L, token = threadIdx.x / L, e0 = sub * N;
-  const int kept = group_kept(p.k, p.E, BIAS);
-  double *const exact = reinterpret_cast<double *>(room) + (BIAS ? token * kept : 0);
-  int32_t *const id = reinterpret_cast<int32_t *>(room + (BIAS ? tokens * kept * 8 : 0)) + token * kept;
+  const bool look = group_looks(p);
+  const int kept = group_kept(p.k, p.E, look);
+  double *const exact = reinterpret_cast<double *>(room) + (look ? token * kept : 0);
+  int32_t *const id = reinterpret_cast<int32_t *>(room + (look ? tokens * kept * 8 : 0)) + token * kept;
   float *const val = reinterpret_cast<float *>(id + tokens * kept);
-  int32_t *const order = id + 2 * tokens * kept;  // (BIAS)
+  int32_t *const order = id + 2 * tokens * kept;  // (look)
+  float *const whole = reinterpret_cast<float *>(exact);  // (before exact is)
   const bool balance = rows != nullptr;
   if (balance) balance_clear(p, count);
   float acc[N], bias[N];
@@ -444,8 +486,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     const int64_t t = t0 + token;
     float l[N], s[N];
     next.get(p, l);
-#pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = counts ? l[i] : -INFINITY;
+    const bool counted = counts;  // (else what follows is computed of no one's logits, and nothing is chosen)
     if (t0 + step < p.T) fetch(t + step);
     float top = l[0];
 #pragma unroll
@@ -456,45 +497,79 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     float sum = 0.f, unit = 1.f;
     if (balance || BIAS || !SIGMOID) sum = scores<SIGMOID, N, L>(l, shift, s);
     if (BIAS) unit = !SIGMOID ? inverse(sum) : shift == 0.f ? 1.f : exp_down(shift);
-    int found, key[N];
-    bool moved = false;  // choice j lies at order[j]
+    typedef Packed<N, L> P;
+    uint32_t keys[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      key[i] = key_of(BIAS ? fmaf(s[i], unit, bias[i]) : l[i]);
-      if (BIAS) key[i] = l[i] > -INFINITY ? key[i] : kNever;
+      const float key = fmaf(s[i], unit, bias[i]);
+      keys[i] = P::pack(!BIAS ? l[i] + 0.f : l[i] > -INFINITY ? key : -INFINITY, e0 + i);  // (+ 0: both zeros alike)
     }
-    if (BIAS) {
-      Closeness c;
-      found = choose_near<N, L>(key, p.k, sub, id, val, SIGMOID ? 1.f : unit, c);
+    const Taken c = choose_packed<N, L, SIGMOID, BIAS>(keys, counted, p.k, sub, reinterpret_cast<uint32_t *>(id), look, unit);
+    const int found = c.found;
+    bool moved = false;  // choice j lies at order[j]
+    wave_sync();
+    // a choice to a lane: its logit and whole key
+    for (int j = sub; j < c.taken; j += L) {
+      const uint32_t k = (uint32_t)id[j];
+      const int e = P::expert(k);
+      const float x = look ? logit(p, t, e) : P::key(k);
+      id[j] = e;
+      val[j] = x;
+      if (look) whole[j] = BIAS ? fmaf(shifted_score<SIGMOID>(x, shift), unit, p.bias[e]) : x;
+    }
+    if (look) {
       wave_sync();
-      for (int j = sub; j < c.taken; j += L) val[j] = logit(p, t, id[j]);
-      if (__ballot(c.close) != 0) {
-        // keys in 64 bits: of the taken experts, or all where the next ones did not end
-        const double all = SIGMOID ? 1.0 : exact_sum<N, L>(l, top);
-        moved = c.close && !c.more;
-        wave_sync();
-        for (int j = sub; moved && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(val[j], top, all, p.bias[id[j]]);
-        wave_sync();
-        for (int j = sub; moved && j < c.taken; j += L) {
-          int rank = 0;
-          for (int i = 0; i < c.taken; ++i) rank += exact[i] > exact[j] || (exact[i] == exact[j] && id[i] < id[j]);
-          order[rank] = j;
-        }
-        if (__ballot(c.more) != 0) {
-          double key64[N];
-          exact_keys<N, SIGMOID>(l, bias, top, all, key64);
-          wave_sync();
-          choose<N, L, double>(key64, p.k, sub, id, val, c.more);
-          wave_sync();
-          for (int j = sub; c.more && j < found; j += L) val[j] = logit(p, t, id[j]);
-        }
+      bool off = false;  // not in order, or too near to tell
+      for (int j = sub; j + 1 < c.taken; j += L) {
+        const float x = whole[j], y = whole[j + 1];
+        off = off || !(BIAS ? x - y > key_margin<SIGMOID>(unit, x, y) : x >= y);
       }
-    } else {
-      found = choose<N, L, int>(key, p.k, sub, id, val, true);
+      const uint64_t group = group_lanes<L>();
+      const bool sort = (__ballot(off) & group) != 0 || c.more;
+      if (__builtin_expect(__ballot(sort) != 0, 0)) {
+        // the order of the whole keys, where some are too near of those in 64 bits, or of all
+        // experts where those that come next did not end
+        moved = sort && !c.more;
+        auto set_order = [&](bool mine, auto *key, bool loose) {
+          wave_sync();
+          bool near = false;
+          for (int j = sub; mine && j < c.taken; j += L) {
+            const auto x = key[j];
+            int rank = 0;
+            for (int i = 0; i < c.taken; ++i) {
+              const auto y = key[i];
+              rank += y > x || (y == x && id[i] < id[j]);
+              if (loose) near = near || (i != j && !(fabsf((float)(x - y)) > key_margin<SIGMOID>(unit, (float)x, (float)y)));
+            }
+            order[rank] = j;
+          }
+          wave_sync();
+          return (__ballot(near) & group) != 0;
+        };
+        const bool near = set_order(moved, whole, BIAS);
+        if (BIAS && __ballot(near || c.more) != 0) {
+          const double all = SIGMOID ? 1.0 : exact_sum<N, L>(l, top);
+          for (int j = sub; near && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(val[j], top, all, p.bias[id[j]]);
+          set_order(near, exact, false);
+          if (__ballot(c.more) != 0) {
+            double key64[N];
+            exact_keys<N, SIGMOID>(l, bias, top, all, key64);
+            choose<N, L, double>(key64, p.k, sub, id, val, c.more);
+          }
+        }
+        if (!BIAS && __ballot(c.more) != 0) {
+          int key[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) key[i] = key_of(l[i]);
+          choose<N, L, int>(key, p.k, sub, id, val, c.more);
+        }
+        wave_sync();
+        for (int j = sub; c.more && j < found; j += L) val[j] = logit(p, t, id[j]);
+      }
     }
     wave_sync();
     // a choice to a lane
-    float high = top, whole = 0.f;
+    float high = top, factor = 0.f;
     if (p.normalize) {
       if (BIAS) {
         high = -INFINITY;
@@ -502,19 +577,19 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
         high = group_max<L>(high);
       }
       high = score_shift<SIGMOID>(high);
-      for (int j = sub; j < found; j += L) whole += shifted_score<SIGMOID>(val[BIAS && moved ? order[j] : j], high);
-      whole = p.scale * inverse_sum(group_sum<L>(whole));
+      for (int j = sub; j < found; j += L) factor += shifted_score<SIGMOID>(val[moved ? order[j] : j], high);
+      factor = p.scale * inverse_sum(group_sum<L>(factor));
     } else if (!SIGMOID) {
-      whole = p.scale * inverse_sum(sum);
+      factor = p.scale * inverse_sum(sum);
     }
     if (t < p.T) {
       for (int j = sub; j < p.k; j += L) {
         float w = 0.f;
         int e = -1;
         if (j < found) {
-          const int at = BIAS && moved ? order[j] : j;
+          const int at = moved ? order[j] : j;
           e = id[at];
-          w = chosen_weight<SIGMOID>(p, val[at], high, whole);
+          w = chosen_weight<SIGMOID>(p, val[at], high, factor);
           if (!SIGMOID && sum != sum) w = sum;  // with softmax a NaN among the logits is in all weights
           if (balance) atomicAdd(&count[e], 1);
         }
@@ -671,7 +746,7 @@ __global__ void __launch_bounds__((kWaveThreads<N, BIAS>())) expert_route_kernel
       if (BIAS) {
         wave_sync();
         const int last = n < need ? n - 1 : p.k;
-        const float margin = n > 1 ? key_margin(SIGMOID ? 1.f : unit, skey[0], skey[last]) : 0.f;
+        const float margin = n > 1 ? key_margin<SIGMOID>(unit, skey[0], skey[last]) : 0.f;
         const int at = lane < last ? lane : 0;
         const uint64_t close = __ballot(lane < last && !(skey[at] - skey[at + 1 < 64 ? at + 1 : 63] > margin));
         if (close != 0) {
@@ -1060,7 +1135,7 @@ struct RouteForward {
       const bool balance = a.counts != nullptr;
       // with the balance loss as many threads as their LDS allows: few rows to join
       int threads = balance ? 1024 : kRouteThreads;
-      const int room = group_room(a.k, a.E, B);
+      const int room = group_room(a.k, a.E, group_looks(a));
       while (threads > 64 && threads / L * room > 48 << 10) threads /= 2;
       unsigned lds = threads / L * room;
       if (balance && lds < threads / 64 * N * L * 4u) lds = threads / 64 * N * L * 4u;  // the waves' sums
@@ -1082,6 +1157,12 @@ struct RouteForward {
   }
 };
 
+// Lanes and experts of a lane: with few experts a wave of its own for each token has too
+// little to do (16384 tokens, k = 8, of 64 / 128 / 256 experts: 4.6 / 5.3 / 8.2 us, a wave each
+// 14 / 15 / 16), with many the groups' k rounds go over too many (512 / 1024: 24 / 35 us, a wave
+// each, which chooses among few candidates, 17 / 21).  Of 16 experts 2 and 8 lanes take 3.6 us
+// for 4.0 with k = 8, but 4.9 for 3.7 with 65536 tokens and k = 1; of 256, 16 and 16 lanes 20 us
+// for 25 with 65536 tokens, but 20 for 16 with a bias and fp64 keys to settle.
 hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s) {
   if (a.E <= 16) return RouteForward::group<4, 4>(a, s);
   if (a.E <= 64) return RouteForward::group<4, 16>(a, s);
@@ -1100,8 +1181,11 @@ template <int N, int L> static hipError_t route_backward(const RouteArgs &a, hip
   return hipGetLastError();
 }
 
+// Few tokens leave the chip empty: a wave for each is done sooner (1024 / 2048 / 4096 tokens of
+// 256 experts: 4.0 / 4.4 / 5.4 us, 16 lanes each 5.2 / 5.4 / 5.6; of 64: 3.6 / 4.0 / 4.5 and
+// 4.1 / 4.2 / 4.4).
 hipError_t launch_expert_route_backward(const RouteArgs &a, hipStream_t s) {
-  const bool few = a.T <= 1024;
+  const bool few = a.T <= 2048;
   if (a.E <= 16) return route_backward<4, 4>(a, s);
   if (a.E <= 64) return few ? route_backward<1, 64>(a, s) : route_backward<4, 16>(a, s);
   if (a.E <= 128) return few ? route_backward<2, 64>(a, s) : route_backward<8, 16>(a, s);

@@ -429,3 +429,35 @@ def test_biased_scores_that_nearly_meet(E, score):
     for kk in (1, k):
         r = nsg.expert_route(lt, kk, score=score, bias=bt)
         assert np.array_equal(r.ids.cpu().numpy(), ref.choose(l.astype(np.float64), kk, score, b.astype(np.float64)))
+
+
+@pytest.mark.parametrize("E", [2, 12, 16, 60, 128, 200, 256, 512, 1000])
+@pytest.mark.parametrize("kind,bias", [("last bits", False), ("few values", False), ("few values", True), ("all equal", False),
+                                       ("all equal", True), ("zeros of both signs", False), ("zeros of both signs", True),
+                                       ("ends of the range", False)])
+def test_logits_that_differ_by_little(E, kind, bias):
+    """The k largest in their exact order, equal ones by index: fp32 logits in their last bits,
+    and 16-bit ones of few values; with a bias of zeros the order of softmax's scores is theirs."""
+    T, k = 700, min(E, 11)
+    g = torch.Generator().manual_seed(E)
+    at = torch.randint(0, {"last bits": 1 << 9, "few values": 7}.get(kind, 2), (T, E), generator=g)
+    sign = torch.randint(0, 2, (T, 1), generator=g) * 2.0 - 1
+    if kind == "last bits":
+        l = sign * (1.5 + at * 2.0 ** -23)
+    elif kind == "few values":
+        l = (sign * at * 0.5).bfloat16()
+    elif kind == "all equal":
+        l = torch.full((T, E), -3.25).to(torch.float16)
+    elif kind == "zeros of both signs":
+        l = torch.where(at > 0, 0.0, -0.0)
+    else:
+        l = torch.tensor([3.4e38, 1e-45, 0.0, -1e-45, -3.4e38, 3.4028234e38, -3.4028234e38])[torch.randint(0, 7, (T, E), generator=g)]
+    l = l.cuda()
+    r = nsg.expert_route(l, k, normalize=True, bias=torch.zeros(E, device="cuda") if bias else None)
+    x = l.double().cpu().numpy() + 0.0
+    order = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(r.ids.cpu().numpy(), order)
+    if kind != "ends of the range":
+        v = np.exp(np.take_along_axis(x, order, 1) - x.max(1, keepdims=True))
+        # exponentials within 3 of 2^-24 and of their arguments (at most 3), their sum, the quotient
+        assert np.allclose(r.weights.cpu().numpy(), v / v.sum(1, keepdims=True), rtol=(2 * (3 + 3) + k + 4) * U, atol=0)
