@@ -485,13 +485,10 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair 
                                                                      int64_t chunks, int64_t C, float scale, bool add,
                                                                      O *__restrict__ out, const float *__restrict__ parts,
                                                                      int64_t pitch) {
-  __shared__ int64_t many;  // parts of the run that all waves sum, 0: none
-  __shared__ int who;       // whose run that is
+  __shared__ int many[kJoinWaves];  // parts of a wave's run that all waves sum, 0: none
   __shared__ float sums[kJoinWaves][256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = (int64_t)blockIdx.x * kJoinWaves, t = t0 + wave, c = (int64_t)blockIdx.y * 256 + lane * 4;
-  if (threadIdx.x == 0) many = 0;
-  __syncthreads();
   int run = -1;
   int64_t more = 0;  // chunks that the run goes on in
   if (t < chunks) {
@@ -508,11 +505,8 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair 
       more += n * unit;
       left = min(left - n * unit, n == 64 ? left : unit - 1);
     }
-    if (more > kJoinAlone && lane == 0) {
-      many = more;
-      who = wave;
-    }
   }
+  if (lane == 0) many[wave] = more > kJoinAlone ? (int)more : 0;
   __syncthreads();
   // parts i, i + step, ... of the run that begins in chunk `from`
   auto add_parts = [&](int64_t from, int64_t i, int64_t step, int64_t n, float(&acc)[4]) {
@@ -528,9 +522,11 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair 
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   if (run >= 0 && c < C) Row<float, 4>::load(parts + (t * 2 + 1) * pitch + c, acc);
   if (more <= kJoinAlone) add_parts(t, 1, 1, more, acc);
-  if (many > 0) {
+  const uint64_t shared = __ballot(many[lane % kJoinWaves] > 0);
+  if (shared != 0) {
+    const int who = __ffsll((long long)shared) - 1;  // whose run that is
     float own[4] = {0.f, 0.f, 0.f, 0.f};
-    add_parts(t0 + who, 1 + wave, kJoinWaves, many, own);
+    add_parts(t0 + who, 1 + wave, kJoinWaves, many[who], own);
     Row<float, 4>::store(&sums[wave][lane * 4], own);
     __syncthreads();
     if (wave == who) {
