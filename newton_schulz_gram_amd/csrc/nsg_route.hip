@@ -478,22 +478,22 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
   float acc[N], bias[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = bias[i] = 0.f;
-  if (BIAS) load_as(p.bias, e0, p.E, bias);
   // the next tokens' logits are on their way while these are worked on
-  const int64_t step = (int64_t)gridDim.x * tokens;
+  const int step = (int)gridDim.x * tokens, T = (int)p.T;  // (at most NSG_MAX_ROWS)
   Logits<N> next;
   int counts = 0;
-  auto fetch = [&](int64_t t) {
-    counts = t < p.T && (p.mask == nullptr || p.mask[t]);
-    next.load(p, t < p.T ? t : 0, e0);
+  auto fetch = [&](int t) {
+    counts = t < T && (p.mask == nullptr || p.mask[t]);
+    next.load(p, t < T ? t : 0, e0);
   };
-  fetch((int64_t)blockIdx.x * tokens + token);
-  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < p.T; t0 += step) {
-    const int64_t t = t0 + token;
+  fetch((int)blockIdx.x * tokens + token);
+  for (int t0 = (int)blockIdx.x * tokens; t0 < T; t0 += step) {
+    const int t = t0 + token;
     float l[N], s[N];
     next.get(p, l);
+    if (BIAS) load_as(p.bias, e0, p.E, bias);  // (for each token: there are no registers to keep it in)
     const bool counted = counts;  // (else what follows is computed of no one's logits, and nothing is chosen)
-    if (t0 + step < p.T) fetch(t + step);
+    if (t0 + step < T) fetch(t + step);
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, l[i]);
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
     } else if (!SIGMOID) {
       factor = p.scale * inverse_sum(sum);
     }
-    if (t < p.T) {
+    if (t < T) {
       for (int j = sub; j < p.k; j += L) {
         float w = 0.f;
         int e = -1;
@@ -599,8 +599,9 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
           if (!SIGMOID && sum != sum) w = sum;  // with softmax a NaN among the logits is in all weights
           if (balance) atomicAdd(&count[e], 1);
         }
-        p.ids[t * p.k + j] = e;
-        p.weights[t * p.k + j] = w;
+        const int64_t to = (int64_t)t * p.k + j;
+        p.ids[to] = e;
+        p.weights[to] = w;
       }
     }
     if (balance && found > 0) {
