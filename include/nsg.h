@@ -590,7 +590,8 @@ nsg_status_t nsg_expert_route(const void *logits, int32_t dtype, int64_t T, int6
 /* The gradient of nsg_expert_route with respect to the logits: dlogits [T][E] of dtype,
  * for the weights' gradient dweights [T][k] (NULL: none) and balance times that of the
  * balance loss (counts NULL: none; *dloss times as much where dloss is not NULL).  ids
- * and counts as nsg_expert_route gives them (the experts of a token differ); counts
+ * and counts as nsg_expert_route gives them (the experts of a token differ; what dweights
+ * holds at an id of -1 does not matter); counts
  * are constants, so where they were summed over several processes the gradient is that
  * of the loss over all their tokens.  A token without a choice gets zeros. */
 nsg_status_t nsg_expert_route_backward(const void *logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, int64_t k,

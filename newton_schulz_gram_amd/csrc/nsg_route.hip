@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
       e[m] = next_e[m] < p.E ? next_e[m] : -1;
-      g[m] = next_g[m] * p.scale;
+      g[m] = e[m] >= 0 ? next_g[m] * p.scale : 0.f;  // (what stands at no choice may be NaN)
       any = any || e[m] >= 0;
       x[m] = e[m] >= 0 ? logit(p, t, e[m]) : -INFINITY;
     }

@@ -461,3 +461,22 @@ def test_logits_that_differ_by_little(E, kind, bias):
         v = np.exp(np.take_along_axis(x, order, 1) - x.max(1, keepdims=True))
         # exponentials within 3 of 2^-24 and of their arguments (at most 3), their sum, the quotient
         assert np.allclose(r.weights.cpu().numpy(), v / v.sum(1, keepdims=True), rtol=(2 * (3 + 3) + k + 4) * U, atol=0)
+
+
+@pytest.mark.parametrize("E", [8, 60, 256, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("T", [50, 3000])
+def test_gradients_of_weights_that_are_none(E, score, normalize, T):
+    """A token with fewer experts than k: what stands where its ids are -1 is not read, be it NaN."""
+    k = 5
+    l, dw = rand((T, E), 50), rand((T, k), 51)
+    few = integers(k + 2, (T, 1), 52)
+    l = torch.where(l.argsort(1, descending=True).argsort(1) < few, l, -float("inf"))
+    r = nsg.expert_route(l, k, score=score, normalize=normalize, balance=True)
+    none = r.ids < 0
+    assert none.any() and not none.all()
+    grads = [nsg.expert_route_backward(l, r.ids, torch.where(none, v, dw), score=score, normalize=normalize, counts=r.counts)
+             for v in (0.0, float("nan"), float("inf"))]
+    assert grads[0].isfinite().all()
+    same(grads[1:], [grads[0]] * 2)
