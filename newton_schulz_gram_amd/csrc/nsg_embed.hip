@@ -192,7 +192,7 @@ constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortKept = 4;                           // steps of 64 tokens that a wave keeps in registers
 constexpr int kSortChunk = kSortThreads * kSortKept;   // tokens of one workgroup, then
 constexpr int kSortMaxChunks = 128;                    // every workgroup reads the whole table
-// Steps of a sort by one workgroup, in LDS: 8192 tokens take 18 us, in four launches 20 (1024: 7)
+// Steps of a sort by one workgroup, in LDS: 8192 tokens take 16 us, in four launches 17 (1024: 7)
 constexpr int kSortAlone = 8;
 static_assert(NSG_MAX_VOCAB <= kSortBins * kSortBins, "two digits");
 
@@ -312,26 +312,35 @@ __device__ __forceinline__ void place_chunk(Get get, Put put, int64_t N, int64_t
     }
   }
   __syncthreads();
-  volatile int *mine = at + wave * bins;
+  int *const mine = at + wave * bins;
+  auto wave_sync = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
   auto place = [&](Pair v) {
     const int d = (v.key >> shift) & (bins - 1);
     const uint64_t there = __ballot(v.key >= 0);
     unsigned lo = (unsigned)there, hi = (unsigned)(there >> 32);
-#pragma unroll
-    for (int b = 0; b < kSortBits; ++b) {  // (bits that no digit has change nothing)
-      const int set = (int)((unsigned)d << (31 - b)) >> 31;  // all bits of it
+    auto match = [&](int b) {  // (bits that no digit has change nothing)
+      const int set = (d << (31 - b)) >> 31;  // all bits of it
       const uint64_t one = __ballot(set);
-      lo &= ~((unsigned)one ^ (unsigned)set);
-      hi &= ~((unsigned)(one >> 32) ^ (unsigned)set);
+      lo = __builtin_amdgcn_bitop3_b32(lo, (unsigned)one, (unsigned)set, 0x90);  // lo & ~(one ^ set)
+      hi = __builtin_amdgcn_bitop3_b32(hi, (unsigned)(one >> 32), (unsigned)set, 0x90);
+    };
+#pragma unroll
+    for (int b = 0; b < 8; ++b) match(b);
+    if (bits > 8) {
+#pragma unroll
+      for (int b = 8; b < kSortBits; ++b) match(b);
     }
     if (v.key >= 0) {
       const int rank = (int)__builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0)), n = __popc(lo) + __popc(hi);
       const int base = mine[d];
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (rank == n - 1) mine[d] = base + n;
       put(base + rank, v);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   };
   if (KEPT > 0) {
 #pragma unroll
@@ -399,12 +408,18 @@ static int64_t part_pitch(int64_t C) { return (C + 3) / 4 * 4; }
 // a chunk's runs
 struct Chunk {
   int64_t p0, p1;
-  bool before, after;  // the first run began in an earlier chunk; the last one goes on
+  int last;  // its last run
+  bool before, after, whole;  // the first run began in an earlier chunk; the last one goes on; they are one
   __device__ __forceinline__ Chunk(const Pair *pairs, int64_t N, int64_t S, int64_t c) {
     p0 = c * S;
     p1 = min(N, p0 + S);
-    before = p0 > 0 && pairs[p0].key >= 0 && pairs[p0 - 1].key == pairs[p0].key;
-    after = p1 < N && pairs[p1].key >= 0 && pairs[p1].key == pairs[p1 - 1].key;
+    // (all four loads at once)
+    const int first = pairs[p0].key, prev = pairs[p0 > 0 ? p0 - 1 : 0].key;
+    last = pairs[p1 - 1].key;
+    const int next = pairs[p1 < N ? p1 : p1 - 1].key;
+    before = p0 > 0 && first >= 0 && prev == first;
+    after = p1 < N && last >= 0 && next == last;
+    whole = before && first == last;
   }
 };
 
@@ -495,8 +510,7 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair 
   int64_t more = 0;  // chunks that the run goes on in
   if (t < chunks) {
     const Chunk ch(pairs, ntok, S, t);
-    const int last = pairs[ch.p1 - 1].key;
-    if (ch.after && !(ch.before && pairs[ch.p0].key == last)) run = last;
+    if (ch.after && !ch.whole) run = ch.last;
   }
   if (run >= 0) {
     // chunks behind t that begin with it: the first so many of `left`
