@@ -455,10 +455,10 @@ template <bool SIGMOID> __device__ __forceinline__ float chosen_weight(const Rou
 
 // ---- several tokens to a wave: up to 256 experts ---------------------------------
 // LDS of a token: the chosen keys, then experts, and their logits; where keys lose bits
-// (`look`) also those that come next, their whole keys and the order of these
+// (`look`) also those that come next, their exact keys, the order of these, and whole keys
 static __host__ __device__ bool group_looks(const RouteArgs &p) { return p.bias != nullptr || p.dtype == NSG_F32; }
 static __host__ __device__ int group_kept(int k, int E, bool look) { return look ? (k + kNext <= E ? k + kNext : E + 1) : k; }
-static __host__ __device__ int group_room(int k, int E, bool look) { return group_kept(k, E, look) * (look ? 20 : 8); }
+static __host__ __device__ int group_room(int k, int E, bool look) { return group_kept(k, E, look) * (look ? 24 : 8); }
 
 template <int N, int L, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, BalanceRow *__restrict__ rows, int64_t pitch) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
   int32_t *const id = reinterpret_cast<int32_t *>(room + (look ? tokens * kept * 8 : 0)) + token * kept;
   float *const val = reinterpret_cast<float *>(id + tokens * kept);
   int32_t *const order = id + 2 * tokens * kept;  // (look)
-  float *const whole = reinterpret_cast<float *>(exact);  // (before exact is)
+  float *const whole = reinterpret_cast<float *>(id + 3 * tokens * kept);
   const bool balance = rows != nullptr;
   if (balance) balance_clear(p, count);
   float acc[N], bias[N];
@@ -533,29 +533,33 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
       const uint64_t group = group_lanes<L>();
       const bool sort = (__ballot(off) & group) != 0 || c.more;
       if (__builtin_expect(__ballot(sort) != 0, 0)) {
-        // the order of the whole keys, where some are too near of those in 64 bits, or of all
-        // experts where those that come next did not end
+        // the order of the whole keys, of those that are too near by their 64 bits, or of all
+        // experts' where those that come next did not end
         moved = sort && !c.more;
-        auto set_order = [&](bool mine, auto *key, bool loose) {
+        // `which` of this lane's choices, a bit for each; those that are near another
+        auto set_order = [&](uint32_t which, auto *key, bool loose) {
           wave_sync();
-          bool near = false;
-          for (int j = sub; mine && j < c.taken; j += L) {
+          uint32_t near = 0;
+          for (int j = sub; j < c.taken; j += L) {
+            const uint32_t bit = 1u << (j / L);
+            if (!(which & bit)) continue;
             const auto x = key[j];
             int rank = 0;
             for (int i = 0; i < c.taken; ++i) {
               const auto y = key[i];
               rank += y > x || (y == x && id[i] < id[j]);
-              if (loose) near = near || (i != j && !(fabsf((float)(x - y)) > key_margin<SIGMOID>(unit, (float)x, (float)y)));
+              if (loose && i != j && !(fabsf((float)(x - y)) > key_margin<SIGMOID>(unit, (float)x, (float)y))) near |= bit;
             }
             order[rank] = j;
           }
           wave_sync();
-          return (__ballot(near) & group) != 0;
+          return near;
         };
-        const bool near = set_order(moved, whole, BIAS);
-        if (BIAS && __ballot(near || c.more) != 0) {
+        const uint32_t near = set_order(moved ? ~0u : 0, whole, BIAS);
+        if (BIAS && __ballot(near != 0 || c.more) != 0) {
           const double all = SIGMOID ? 1.0 : exact_sum<N, L>(l, top);
-          for (int j = sub; near && j < c.taken; j += L) exact[j] = exact_key<SIGMOID>(val[j], top, all, p.bias[id[j]]);
+          for (int j = sub; moved && j < c.taken; j += L)
+            exact[j] = near >> (j / L) & 1 ? exact_key<SIGMOID>(val[j], top, all, p.bias[id[j]]) : (double)whole[j];
           set_order(near, exact, false);
           if (__ballot(c.more) != 0) {
             double key64[N];
@@ -1143,7 +1147,7 @@ struct RouteForward {
       // with the balance loss as many threads as their LDS allows: few rows to join
       int threads = balance ? 1024 : kRouteThreads;
       const int room = group_room(a.k, a.E, group_looks(a));
-      while (threads > 64 && threads / L * room > 48 << 10) threads /= 2;
+      while (threads > 64 && threads / L * room > 60 << 10) threads /= 2;
       unsigned lds = threads / L * room;
       if (balance && lds < threads / 64 * N * L * 4u) lds = threads / 64 * N * L * 4u;  // the waves' sums
       return launch(a, threads, threads / L, s, [&](dim3 grid, dim3 block, BalanceRow *rows, int64_t pitch) {

@@ -480,3 +480,22 @@ def test_gradients_of_weights_that_are_none(E, score, normalize, T):
              for v in (0.0, float("nan"), float("inf"))]
     assert grads[0].isfinite().all()
     same(grads[1:], [grads[0]] * 2)
+
+
+@pytest.mark.parametrize("E", [16, 64, 65, 128, 200, 256, 257, 1024])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("near", [False, True])
+def test_as_many_choices_as_can_be(E, score, near):
+    """k = 64 or all experts, with a bias and the balance loss: the largest launches in shared memory."""
+    T, k = 600, min(E, 64)
+    l, b = rand((T, E), 60), rand((E,), 61, scale=1e-7 if near else 0.1)
+    if near:  # a quarter of the tokens: keys that only 64 bits tell apart
+        l[::4] = 0.25
+    r = nsg.expert_route(l, k, score=score, bias=b, balance=True)
+    x = l.double().cpu().numpy()
+    ids = r.ids.cpu().numpy()
+    assert np.array_equal(ids, ref.choose(x, k, score, b.double().cpu().numpy()))
+    counts = r.counts.cpu().numpy()
+    assert np.array_equal(counts[:-1], np.bincount(ids.ravel(), minlength=E)) and counts[-1] == T
+    if k == E:
+        assert (counts[:-1] == T).all()
