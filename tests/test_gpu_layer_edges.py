@@ -499,3 +499,26 @@ def test_as_many_choices_as_can_be(E, score, near):
     assert np.array_equal(counts[:-1], np.bincount(ids.ravel(), minlength=E)) and counts[-1] == T
     if k == E:
         assert (counts[:-1] == T).all()
+
+
+@pytest.mark.parametrize("E", [3, 16, 60, 128, 256, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T", [77, 3001])
+def test_what_padded_tokens_hold(E, score, bias, T):
+    """Whatever stands in a token that does not count, all results are those of zeros there."""
+    k = min(E, 4)
+    l, dw, mask = rand((T, E), 70, torch.bfloat16), rand((T, k), 71), integers(5, (T,), 72) > 0
+    b = rand((E,), 73, scale=0.1) if bias else None
+    want = None
+    for v in (0.0, float("nan"), float("inf"), -float("inf"), 3e38):
+        x = torch.where(mask[:, None], l, v)
+        g = torch.where(mask[:, None], dw, v)
+        r = nsg.expert_route(x, k, score=score, bias=b, mask=mask, balance=True)
+        got = (*r, nsg.expert_route_backward(x, r.ids, g, score=score, counts=r.counts))
+        assert r.ids[~mask].eq(-1).all() and got[-1][~mask].eq(0).all() and r.loss.isfinite() and got[-1].isfinite().all()
+        want = want or got
+        same(got, want)
+        ids = torch.where(mask, integers(50, (T,), 74), -1)
+        dW = nsg.embedding_backward(torch.where(mask[:, None], l, v), ids, 50)
+        assert dW.isfinite().all()
