@@ -189,7 +189,9 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortBits = 10;
 constexpr int kSortBins = 1 << kSortBits;
-constexpr int kSortKept = 4;                           // steps of 64 tokens that a wave keeps in registers
+// steps of 64 tokens that a wave keeps in registers (131072 and 524288 tokens: the call takes
+// 41.6 and 69 us so, 42.5 and 71 with the tokens read again)
+constexpr int kSortKept = 4;
 constexpr int kSortChunk = kSortThreads * kSortKept;   // tokens of one workgroup, then
 constexpr int kSortMaxChunks = 128;                    // every workgroup reads the whole table
 // Steps of a sort by one workgroup, in LDS: 8192 tokens take 16 us, in four launches 17 (1024: 7)
@@ -495,7 +497,9 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const Pair *__restrict_
 // wave w every 16th part from w on: one of 8192 parts of 1024 takes 134 us, by one wave 609;
 // joining the runs of 65536 tokens of 4096, half of which are the same, 33 us, by one wave each 73.
 constexpr int kJoinWaves = 16;
-constexpr int kJoinAlone = 32;  // parts of a run that one wave sums
+// Parts of a run that one wave sums (65536 tokens of 1024, 2000 of an id, 32 parts: the call
+// takes 50 us so, with all waves 48)
+constexpr int kJoinAlone = 16;
 static_assert(kJoinAlone >= kJoinWaves, "one run of many parts in a workgroup");
 template <typename O>
 __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(const Pair *__restrict__ pairs, int64_t ntok, int64_t S,

@@ -319,13 +319,14 @@ def test_embedding_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("C", [3, 64, 260, 1030])
-@pytest.mark.parametrize("lengths", ["one id", "half of them", "around 32 parts", "many long ones"])
+@pytest.mark.parametrize("lengths", ["one id", "half of them", "around 16 parts", "around 32 parts", "many long ones"])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_embedding_gradient_of_ids_that_come_often(C, lengths, accumulate):
     """Runs of equal ids over few and many chunks of the sorted list (of 8 tokens or more),
     whole numbers whose sums are exact in fp32 in any order."""
     n = {"one id": [30000],
          "half of them": [1] * 9000 + [15000] + [3] * 2000,
+         "around 16 parts": [8 * k + d for k in range(13, 21) for d in (-1, 0, 1, 5)] * 5 + [1, 0, 2],
          "around 32 parts": [8 * k + d for k in range(29, 37) for d in (-1, 0, 1, 5)] * 3 + [1, 0, 2],
          "many long ones": [2000, 0, 1, 1999, 2001] * 4 + [513] * 7}[lengths]
     ids = torch.arange(len(n)).repeat_interleave(torch.tensor(n))
