@@ -523,3 +523,73 @@ def test_what_padded_tokens_hold(E, score, bias, T):
         ids = torch.where(mask, integers(50, (T,), 74), -1)
         dW = nsg.embedding_backward(torch.where(mask[:, None], l, v), ids, 50)
         assert dW.isfinite().all()
+
+
+@pytest.mark.parametrize("E", [8, 60, 128, 256, 512, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [50, 2500])
+def test_logits_that_are_not_finite_in_tokens_that_count(E, score, bias, dtype, T):
+    """What a NaN or an infinity does to its own token, in the choice, the weights, the loss and the
+    gradient; and that it does nothing to the other tokens."""
+    k, inf, nan = 4, float("inf"), float("nan")
+    clean = rand((T, E), 80, dtype)
+    l = clean.clone()
+    l[3, E // 2] = nan
+    l[5, E - 1] = inf
+    l[7] = nan
+    l[9, 0], l[9, E - 2] = nan, inf
+    l[11, 1:] = nan  # one expert left
+    l[13] = -inf
+    l[13, 2], l[13, 5] = 1.0, nan  # one expert left, of those that are finite
+    l[T - 1, 1] = l[T - 1, E - 3] = inf
+    l[T - 2, ::2] = nan
+    special = torch.tensor([3, 5, 7, 9, 11, 13, T - 1, T - 2], device="cuda")
+    infs = torch.tensor([5, 9, T - 1], device="cuda")  # rows with +inf
+    ours = torch.ones(T, dtype=torch.bool, device="cuda")
+    ours[special] = False
+    b = rand((E,), 81, scale=0.1) if bias else None
+    x = l.double().cpu().numpy()
+    ids = ref.choose(x, k, score, None if b is None else b.double().cpu().numpy())
+    chosen = torch.from_numpy(ids >= 0).cuda()
+    dw = rand((T, k), 82)
+    for normalize in (True, False):
+        kw = dict(score=score, normalize=normalize)
+        r, plain = nsg.expert_route(l, k, bias=b, balance=True, **kw), nsg.expert_route(clean, k, bias=b, **kw)
+        assert np.array_equal(r.ids.cpu().numpy(), ids)
+        assert torch.equal(r.ids, nsg.expert_route(l, k, bias=b, **kw).ids)
+        assert torch.equal(r.weights[ours], plain.weights[ours])
+        w = r.weights[special]
+        assert w[~chosen[special]].eq(0).all()
+        if score == "softmax":
+            assert w[chosen[special]].isnan().all()
+        else:
+            want = torch.from_numpy(ref.weights(np.where(np.isnan(x), -inf, x), ids, score, normalize, 1.0)).cuda()[special]
+            a = 2 * clean.double().abs().max().item()  # of logits, as of the differences that are taken of them
+            assert ((w.double() - want).abs() <= (2 * a + k + 40) * U * want).all()
+        # the loss: tokens with a choice whose scores' sum is a NaN (softmax of an infinity too)
+        some = chosen.any(1)
+        assert r.counts[E] == int(some.sum())
+        bad = torch.isnan(l).any(1)
+        if score == "softmax":
+            bad[infs] = True
+        assert bool(r.probs.isnan().all()) == bool(r.loss.isnan()) == bool((bad & some).any())
+        assert bool((bad & some).any()) != (score == "softmax" and bias)  # there a NaN leaves a token no choice
+
+        for counts in (None, r.counts):
+            got = nsg.expert_route_backward(l, r.ids, dw, counts=counts, balance=3.0, **kw)
+            want = nsg.expert_route_backward(clean, r.ids, dw, counts=counts, balance=3.0, **kw)
+            assert torch.equal(got[ours], want[ours]) and got[ours].isfinite().all()
+            assert got[~some].eq(0).all()
+            rows = got[special]
+            hit = (bad & some)[special]
+            if counts is not None:  # p is a NaN in all of the token
+                assert rows[hit].isnan().all() and rows[~hit].isfinite().all()
+            elif score == "sigmoid":  # the chosen's scores are finite
+                assert rows.isfinite().all()
+            elif normalize:  # the chosen's weights are NaN
+                at = torch.where(chosen, r.ids, 0).long()
+                assert torch.gather(got, 1, at)[chosen & (bad & some)[:, None]].isnan().all()
+            else:  # softmax: each logit is in each score
+                assert rows[hit].isnan().all()
