@@ -209,8 +209,12 @@ __device__ __forceinline__ float sigmoid(float l) { return inverse(1.f + exp_dow
 // A token's scores times a factor that they share, so that none that matters under- or
 // overflows: softmax e^(l - shift) with shift the largest logit, sigmoid
 // sigmoid(l) e^-shift with shift 0 unless the largest logit is far below it.
-template <bool SIGMOID> __device__ __forceinline__ float score_shift(float top) {
-  return SIGMOID ? (top < -60.f ? top : 0.f) : top;
+constexpr float kFar = -60.f;
+// The gradient multiplies scores by numbers of any size before it divides by their sum: with
+// the largest score at least e^-8 what underflows there is below E 2^-150 e^8 < 2^-126
+constexpr float kFarBackward = -8.f;
+template <bool SIGMOID> __device__ __forceinline__ float score_shift(float top, float far = kFar) {
+  return SIGMOID ? (top < far ? top : 0.f) : top;
 }
 // scores s and their sum; behind the last expert, where l is -inf, they are 0
 template <bool SIGMOID, int N, int L> __device__ __forceinline__ float scores(const float (&l)[N], float shift, float (&s)[N]) {
@@ -1045,7 +1049,7 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
     top = group_max<L>(top);
     if (!(top > -INFINITY)) top = 0.f;
     float s[N], pc = 0.f;
-    const float sum = inverse_sum(scores<SIGMOID, N, L>(l, score_shift<SIGMOID>(top), s));
+    const float sum = inverse_sum(scores<SIGMOID, N, L>(l, score_shift<SIGMOID>(top, kFarBackward), s));
 #pragma unroll
     for (int i = 0; i < N; ++i) pc = fmaf(s[i], c[i], pc);
     pc = group_sum<L>(pc) * sum;
@@ -1055,7 +1059,7 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
 #pragma unroll
       for (int m = 0; m < kMine; ++m) high = fmaxf(high, x[m]);
       high = group_max<L>(high);
-      high = high > -INFINITY ? score_shift<SIGMOID>(high) : 0.f;
+      high = high > -INFINITY ? SIGMOID ? fminf(high, 0.f) : high : 0.f;  // (the largest v at least 1/2)
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         v[m] = p.normalize ? shifted_score<SIGMOID>(x[m], high) : softmax ? exp_down(x[m] - top) : 0.f;

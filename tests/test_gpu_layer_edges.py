@@ -593,3 +593,29 @@ def test_logits_that_are_not_finite_in_tokens_that_count(E, score, bias, dtype, 
                 assert torch.gather(got, 1, at)[chosen & (bad & some)[:, None]].isnan().all()
             else:  # softmax: each logit is in each score
                 assert rows[hit].isnan().all()
+
+
+@pytest.mark.parametrize("E", [8, 60, 128, 256, 512, 1000])
+@pytest.mark.parametrize("T", [50, 3000])
+@pytest.mark.parametrize("level", [-15.0, -40.0, -58.0, -200.0])
+@pytest.mark.parametrize("size", [1.0, 1e-19, 1e-30])
+def test_small_gradients_of_small_sigmoid_scores(E, T, level, size):
+    """Normalised weights and the balance loss of a token whose scores are all small: the shares that
+    they are made of are not, so the gradient is as exact as any other's, however small it is.
+
+    The tolerance of the router's gradient: (4 a + 2 k + 80) u of the sum of its terms' sizes, a the
+    largest |l| that an exponential is taken of; then fp32's own rounding, and of numbers below
+    2^-126 its step."""
+    k = min(E, 6)
+    l, dw = level + 0.5 * rand((T, E), 90), size * rand((T, k), 91)
+    r = nsg.expert_route(l, k, score="sigmoid", balance=True)
+    x, ids, counts = l.double().cpu().numpy(), r.ids.cpu().numpy(), r.counts.cpu().numpy()
+    d = dw.double().cpu().numpy()
+    a = np.abs(x).max()
+    for dweights, c, coef in ((dw, None, 0.0), (None, r.counts, size), (dw, r.counts, size)):
+        got = nsg.expert_route_backward(l, r.ids, dweights, score="sigmoid", counts=c, balance=coef).double().cpu().numpy()
+        want, terms = ref.route_backward(x, ids, None if dweights is None else d, "sigmoid", True, 1.0,
+                                         None if c is None else counts, float(np.float32(coef)))
+        tol = (4 * a + 2 * k + 80) * U * terms
+        bad = ~(np.abs(got - want) <= tol + U * np.abs(want) + 2.0 ** -126)
+        assert not bad.any(), (int(bad.sum()), got[bad][:3], want[bad][:3], tol[bad][:3])
