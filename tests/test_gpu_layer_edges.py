@@ -619,3 +619,23 @@ def test_small_gradients_of_small_sigmoid_scores(E, T, level, size):
         tol = (4 * a + 2 * k + 80) * U * terms
         bad = ~(np.abs(got - want) <= tol + U * np.abs(want) + 2.0 ** -126)
         assert not bad.any(), (int(bad.sum()), got[bad][:3], want[bad][:3], tol[bad][:3])
+
+
+@pytest.mark.parametrize("E", [12, 16, 60, 128, 200, 256, 512, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_biases_of_any_size(E, score, dtype):
+    """Infinities, NaN, numbers beside which scores are nothing, and numbers that are nothing beside them."""
+    l = rand((300, E), 95, dtype)
+    b = rand((E,), 96, scale=0.1)
+    for i, v in enumerate((float("inf"), -float("inf"), 1e30, float("nan"), -1e30, 1e-40)):
+        b[i::11] = v
+    x, bd = l.double().cpu().numpy(), b.double().cpu().numpy()
+    a = 2 * np.abs(x).max()
+    for k in sorted({1, 3, min(E, 8), min(E, 31), min(E, 64)}):
+        for normalize in (True, False):
+            r = nsg.expert_route(l, k, score=score, bias=b, normalize=normalize)
+            ids = ref.choose(x, k, score, bd)
+            assert np.array_equal(r.ids.cpu().numpy(), ids), k
+            want = ref.weights(x, ids, score, normalize, 1.0)
+            assert (np.abs(r.weights.double().cpu().numpy() - want) <= (2 * a + k + 40) * U * want).all(), k
