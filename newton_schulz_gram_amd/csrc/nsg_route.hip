@@ -216,6 +216,9 @@ constexpr float kFarBackward = -8.f;
 template <bool SIGMOID> __device__ __forceinline__ float score_shift(float top, float far = kFar) {
   return SIGMOID ? (top < far ? top : 0.f) : top;
 }
+// The same for those of the chosen, of which a token's weights are shares: the largest becomes
+// at least 1/2, so that any scale or gradient may be multiplied by them and by their sum's inverse
+template <bool SIGMOID> __device__ __forceinline__ float chosen_shift(float top) { return SIGMOID ? fminf(top, 0.f) : top; }
 // scores s and their sum; behind the last expert, where l is -inf, they are 0
 template <bool SIGMOID, int N, int L> __device__ __forceinline__ float scores(const float (&l)[N], float shift, float (&s)[N]) {
   float sum = 0.f;
@@ -450,7 +453,7 @@ __device__ __forceinline__ void balance_store(const RouteArgs &p, float (&acc)[N
   }
 }
 
-// The weight of a chosen expert with logit x.  `high`: score_shift of the largest chosen
+// The weight of a chosen expert with logit x.  `high`: chosen_shift of the largest chosen
 // logit, `whole`: scale / sum of the chosen's shifted scores; not normalised, softmax:
 // the largest logit and scale / sum of all.
 template <bool SIGMOID> __device__ __forceinline__ float chosen_weight(const RouteArgs &p, float x, float high, float whole) {
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(1024) expert_route_group_kernel(RouteArgs p, B
         for (int j = sub; j < found; j += L) high = fmaxf(high, val[moved ? order[j] : j]);
         high = group_max<L>(high);
       }
-      high = score_shift<SIGMOID>(high);
+      high = chosen_shift<SIGMOID>(high);
       for (int j = sub; j < found; j += L) factor += shifted_score<SIGMOID>(val[moved ? order[j] : j], high);
       factor = p.scale * inverse_sum(group_sum<L>(factor));
     } else if (!SIGMOID) {
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__((kWaveThreads<N, BIAS>())) expert_route_kernel
     const float x = in ? val[lane] : -INFINITY;
     float high = top, whole = 0.f;
     if (p.normalize) {
-      high = score_shift<SIGMOID>(BIAS ? wave_max(x) : top);
+      high = chosen_shift<SIGMOID>(BIAS ? wave_max(x) : top);
       whole = p.scale / wave_sum(in ? shifted_score<SIGMOID>(x, high) : 0.f);
     } else if (!SIGMOID) {
       whole = p.scale / sum;
@@ -1059,7 +1062,7 @@ __global__ void __launch_bounds__(kRouteThreads) expert_route_backward_kernel(Ro
 #pragma unroll
       for (int m = 0; m < kMine; ++m) high = fmaxf(high, x[m]);
       high = group_max<L>(high);
-      high = high > -INFINITY ? SIGMOID ? fminf(high, 0.f) : high : 0.f;  // (the largest v at least 1/2)
+      high = high > -INFINITY ? chosen_shift<SIGMOID>(high) : 0.f;
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         v[m] = p.normalize ? shifted_score<SIGMOID>(x[m], high) : softmax ? exp_down(x[m] - top) : 0.f;

@@ -639,3 +639,21 @@ def test_biases_of_any_size(E, score, dtype):
             assert np.array_equal(r.ids.cpu().numpy(), ids), k
             want = ref.weights(x, ids, score, normalize, 1.0)
             assert (np.abs(r.weights.double().cpu().numpy() - want) <= (2 * a + k + 40) * U * want).all(), k
+
+
+@pytest.mark.parametrize("E", [8, 60, 128, 256, 512, 1000])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("level", [-15.0, -40.0, -58.0, -200.0])
+@pytest.mark.parametrize("scale", [1e30, -1e15, 1.0, 1e-30])
+def test_weights_of_any_scale_of_small_sigmoid_scores(E, bias, level, scale):
+    """Normalised weights are shares of the scale, whatever the scores are."""
+    T, k = 200, min(E, 6)
+    l = level + 0.5 * rand((T, E), 97)
+    b = rand((E,), 98, scale=0.1) if bias else None
+    x = l.double().cpu().numpy()
+    r = nsg.expert_route(l, k, score="sigmoid", bias=b, scale=scale)
+    ids = ref.choose(x, k, "sigmoid", None if b is None else b.double().cpu().numpy())
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    want = ref.weights(x, ids, "sigmoid", True, float(np.float32(scale)))
+    # a: the largest |l| that an exponential is taken of
+    assert (np.abs(r.weights.double().cpu().numpy() - want) <= (2 * np.abs(x).max() + k + 40) * U * np.abs(want)).all()
