@@ -248,6 +248,17 @@ def test_layer_norm_of_large_means_and_small_spreads(C, shift, scale):
     check_norm(x, w, b, 1e-12, *nsg.layer_norm(x, w, b, 1e-12))
 
 
+@pytest.mark.parametrize("C", [3, 300, 4096, 16384, 20000])
+@pytest.mark.parametrize("scale", [1e-18, 1e16])
+def test_layer_norm_at_the_ends_of_its_range(C, scale):
+    """Squares of 1e-36 (above 2^-126), and of 1e32, whose sum is below 2^128; no eps."""
+    x, w, b = norm_case(9, C, "f32", "f32", seed=C, scale=scale)
+    y, stats = nsg.layer_norm(x, w, b, 0.0)
+    check_norm(x, w, b, 0.0, y, stats)
+    dy = normal((9, C), "f32", seed=1)
+    check_norm_gradient(dy, x, stats, w, *nsg.layer_norm_backward(dy, x, stats, w))
+
+
 def test_layer_norm_of_constant_and_non_finite_rows():
     x = torch.full((6, 300), 3.5, device="cuda")
     x[1] = normal((300,), "f32", seed=1)
