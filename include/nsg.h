@@ -545,8 +545,9 @@ nsg_status_t nsg_embedding_backward(const void *dout, int32_t dtype, int64_t T, 
  * y [R][C] and x of dtype; weight and bias [C] of w_dtype, or NULL (1 and 0).
  *   stats  [2][R] fp32: the means, then the rstd, which the gradient takes
  * eps >= 0 and finite; C = 0 with rows is NSG_ERR_SHAPE.  The variance is that of the
- * differences from the mean, also where the mean is large beside them; their squares
- * must not overflow fp32. */
+ * differences from the mean, also where the mean is large beside them.  A row's sum and
+ * the sum of the squared differences must not overflow fp32, and the variance is exact
+ * to fp32's rounding where it is above 2^-126 (below, eps should outweigh it). */
 nsg_status_t nsg_layer_norm(const void *x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, const void *weight,
                             const void *bias, int32_t w_dtype, float eps, void *y, float *stats, void *stream);
 
@@ -577,7 +578,9 @@ nsg_status_t nsg_layer_norm_backward(const void *dy, int64_t lddy, const void *x
  *   probs    [E] fp32: the mean of s / sum s
  *   loss     [1] fp32: E / (k N) sum_e counts[e] probs[e], 0 where N = 0
  * NaN among a token's logits (with softmax +inf too) makes its probabilities NaN, with
- * softmax its weights.  k <= min(E, NSG_MAX_CHOICES), T k <= NSG_MAX_ROWS; scale finite.
+ * softmax its weights.  Scores are fp32, those below 2^-126 (a sigmoid's logit below -87)
+ * 0; normalised weights, probs and their gradients are shares of them, as exact where
+ * all of a token's scores are small.  k <= min(E, NSG_MAX_CHOICES), T k <= NSG_MAX_ROWS; scale finite.
  *   workspace  nsg_expert_route_workspace_size bytes; none is needed without the loss */
 #define NSG_SCORE_SOFTMAX 0
 #define NSG_SCORE_SIGMOID 1

@@ -1052,7 +1052,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     """Layer norm over the last dimension of x [..., C]: (y, stats) with
     y = (x - mean) * rstd * weight + bias of x's dtype and stats [2, R] float32 the R rows'
     means and rstd = 1 / sqrt(var + eps), which layer_norm_backward takes.  weight and
-    bias [C]: of one dtype, float32 or another; None for 1 and 0."""
+    bias [C]: of one dtype, float32 or another; None for 1 and 0.  fp32 sums: a row's and
+    that of its squared differences must not overflow."""
     device = _gpu(x, "layer_norm")
     R, C, ld = _vectors(x, "x")
     code = NSG_F32

@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(256) embed_runs_kernel(const Pair *__restrict_
 // wave w every 16th part from w on: one of 8192 parts of 1024 takes 134 us, by one wave 609;
 // joining the runs of 65536 tokens of 4096, half of which are the same, 33 us, by one wave each 73.
 constexpr int kJoinWaves = 16;
-// Parts of a run that one wave sums (65536 tokens of 1024, 2000 of an id, 32 parts: the call
-// takes 50 us so, with all waves 48)
+// Parts of a run that one wave sums, more by all (65536 tokens of 1024, 2000 of an id, so 32
+// parts: the call takes 50 us where one wave sums them, 48 where all do)
 constexpr int kJoinAlone = 16;
 static_assert(kJoinAlone >= kJoinWaves, "one run of many parts in a workgroup");
 template <typename O>

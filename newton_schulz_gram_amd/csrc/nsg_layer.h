@@ -39,7 +39,7 @@ struct NormArgs {
   const void *weight = nullptr, *bias = nullptr;  // [C] of w_dtype, or NULL
   int w_dtype = NSG_F32;
   float eps = 0.f;
-  void *out = nullptr;                     // y or dx [R][C], or NULL (dx)
+  void *out = nullptr;                     // y or dx [R][C]
   float *stats = nullptr;                  // mean [R], rstd [R]
   void *dweight = nullptr, *dbias = nullptr;  // [C] of w_dtype, or NULL
   void *workspace = nullptr;

@@ -25,8 +25,8 @@ namespace nsg {
 // ---------------------------------------------------------------------------
 template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
 constexpr int kNormLane = 16;          // elements of a lane
-// Elements of a row in registers: 4096 rows of 16384 in bf16 take 50 us and their gradient 106,
-// of 16392, which are read again for each sum, 65 and 171.
+// Elements of a row in registers: 4096 rows of 16384 in bf16 take 57 us and their gradient 106,
+// of 16392, which are read again for each sum, 81 and 173.
 constexpr int kNormRegisters = 16384;
 
 template <typename T> struct Piece {
@@ -486,8 +486,13 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(NormArgs p, int g
 // ---------------------------------------------------------------------------
 // How many lanes a row takes: enough for 16 elements each.  With 8, 16 and 32 of them 16384
 // rows of 4096 in bf16 take 52, 46 and 45 us, their gradient 82, 85 and 86; 1003 of 1250 in fp32
-// 4.6, 4.7 and 5.5, and 12, 11 and 20; 32768 of 1024 44, 42 and 42, and 78, 80 and 145.  (Rows
-// shorter than a piece: the kernel for wide ones takes any length.)
+// 4.6, 4.7 and 5.5, and 12, 11 and 20; 32768 of 1024 44, 42 and 42, and 78, 80 and 145.  (Calls
+// one after the other on the same memory, where the last-level cache takes part of the
+// stores; 16384 rows of 4096 with an output of their own for each call: 51 us for 43.)
+//
+// Rows shorter than a piece go to the kernel for wide ones, which takes any length but has a
+// workgroup for each row: 1048576 rows of 7 in bf16 take 7.5 ms and their gradient 13, of 8
+// 25 and 41 us.
 // ---------------------------------------------------------------------------
 template <typename T, class K> static hipError_t by_width(const NormArgs &a, hipStream_t s) {
   constexpr int NV = kNormLane / kPiece<T>;
@@ -510,7 +515,7 @@ struct NormForward {
   template <typename T, int LANES, int NV> static hipError_t rows(const NormArgs &a, hipStream_t s) {
     constexpr int threads = LANES < 256 ? 256 : LANES, rows = threads / LANES;
     // (1024, 1536 and 4096 workgroups of 256: 16384 rows of 4096 47, 46 and 43 us; 256, 512 and
-    // 1024 of 1024 threads: 6096 rows of 11008 61, 63 and 67)
+    // 1024 of 1024 threads: 6096 rows of 11008 61, 63 and 67; calls on the same memory, see below)
     constexpr int most = threads == 1024 ? 256 : 256 * 4096 / threads;
     hipLaunchKernelGGL((layer_norm_kernel<T, threads, LANES, NV>),
                        dim3((unsigned)fewer((a.R + rows - 1) / rows, most)), dim3(threads), 0, s, a);
