@@ -566,7 +566,8 @@ nsg_status_t nsg_layer_norm_backward(const void *dy, int64_t lddy, const void *x
 /* The router: each of T tokens chooses k of E experts by its logits l [T][E] (ld).
  *   s = softmax(l) (NSG_SCORE_SOFTMAX) or sigmoid(l) (NSG_SCORE_SIGMOID)
  *   ids      [T][k]: the experts of the k largest l; with a bias [E] (fp32), of the k
- *            largest s + bias, compared in fp64.  Largest first, equal ones by index.
+ *            largest s + bias, compared in fp64 (to the roundings of its exponentials,
+ *            sum and quotient).  Largest first, equal ones by index.
  *            An expert whose logit is -inf or NaN (or whose s + bias is) is not chosen;
  *            -1 where none is left, as nsg_expert_sort drops it.
  *   weights  [T][k] fp32: scale s; normalize 1: scale s / sum of the token's chosen s;

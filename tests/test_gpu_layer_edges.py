@@ -657,3 +657,14 @@ def test_weights_of_any_scale_of_small_sigmoid_scores(E, bias, level, scale):
     want = ref.weights(x, ids, "sigmoid", True, float(np.float32(scale)))
     # a: the largest |l| that an exponential is taken of
     assert (np.abs(r.weights.double().cpu().numpy() - want) <= (2 * np.abs(x).max() + k + 40) * U * np.abs(want)).all()
+
+
+def test_embedding_of_more_rows_than_a_workgroup_each_can_take():
+    """More than 2^23 rows of several parts: four rows to a workgroup, parts in the grid's second direction."""
+    T, V, C = (1 << 23) + 77, 100, 1030
+    W = rand((V, C), 1, torch.bfloat16)
+    ids = integers(V, (T,), 2, lo=-1, dtype=torch.int32)
+    out = nsg.embedding(ids, W)
+    for a in range(0, T, 1 << 20):
+        i = ids[a:a + (1 << 20)].long()
+        assert torch.equal(out[a:a + (1 << 20)], torch.where((i >= 0)[:, None], W[i.clamp(min=0)], 0)), a
